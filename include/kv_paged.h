@@ -158,6 +158,54 @@ kv_status paged_kv_append(kv_pool* pool, const void* k_new, const void* v_new, i
                           const int32_t* block_tables, int max_blocks,
                           const int32_t* context_lens, int batch, void* stream);
 
+/* Pairs of numbers a rotary rotation turns together (first rope_dim numbers of a head). */
+typedef enum kv_rope_style {
+    KV_ROPE_HALF = 0,           /* number i with number i + rope_dim / 2 */
+    KV_ROPE_INTERLEAVED = 1     /* number 2 i with number 2 i + 1 */
+} kv_rope_style;
+
+/*
+ * paged_norm_rope_append -- what stands between the q/k/v projections and the
+ * attention of a layer, in one pass: per-head RMS norm of queries and keys, the
+ * rotary rotation by position, and the append of keys and values to the pool
+ * (paged_kv_append's addresses and error bits).
+ *   q, k, v: bf16; token i's q_heads (k, v: kv_heads) rows of head_dim numbers
+ *     start at element i * q_stride (k_stride, v_stride): slices of one fused
+ *     projection or separate arrays.  16-byte aligned; strides are multiples of
+ *     8 and at least a token's row.
+ *   q_weight, k_weight: float32 [head_dim] each, both or neither NULL (no norm):
+ *     y = x / sqrt(mean(x^2) + eps) * weight, over the head_dim numbers of a row;
+ *     eps >= 0 (read only with weights).
+ *   rope: float32 [rope_positions, rope_dim] or NULL (no rotation): row p holds
+ *     rope_dim / 2 cosines, then rope_dim / 2 sines, of position p; 16-byte
+ *     aligned.  The pair (a, b) becomes (a cos - b sin, b cos + a sin); the
+ *     numbers behind the first rope_dim are left as they are.  rope_dim a
+ *     multiple of 16, at most head_dim.
+ *   token_seq, token_pos, block_tables, context_lens: as in paged_kv_append,
+ *     with q_len new tokens per sequence: without token_seq / token_pos token i
+ *     is token i % q_len of sequence i / q_len, at position context_lens[seq] -
+ *     q_len + i % q_len (then num_tokens <= batch * q_len).  With either array
+ *     q_len must be 1.
+ *   q_out: bf16 [num_tokens / q_len, q_heads, q_len, head_dim], the layout
+ *     paged_attention_multi_query takes; must not overlap any input.
+ *   fp32 arithmetic, each number rounded once: q and bf16 pools to nearest even,
+ *     fp8 pools as paged_kv_append rounds (from the fp32 number, not from bf16).
+ *   A token whose sequence or position is invalid (KV_DEVERR_SEQ,
+ *     KV_DEVERR_POSITION; also a position at or past rope_positions) writes
+ *     nothing, its rows of q_out included; one whose block id is invalid
+ *     (KV_DEVERR_BLOCK_ID) writes q_out only.  num_tokens == 0 is a no-op.
+ *   Two tokens with the same slot in one call race, row by row.
+ *   Latent pools: KV_ERR_INVALID_ARG.
+ */
+kv_status paged_norm_rope_append(kv_pool* pool, const void* q, int64_t q_stride, const void* k,
+                                 int64_t k_stride, const void* v, int64_t v_stride, int q_heads,
+                                 int num_tokens, const float* q_weight, const float* k_weight,
+                                 float eps, const float* rope, int rope_positions, int rope_dim,
+                                 kv_rope_style style, const int32_t* token_seq,
+                                 const int32_t* token_pos, const int32_t* block_tables,
+                                 int max_blocks, const int32_t* context_lens, int batch, int q_len,
+                                 void* q_out, void* stream);
+
 /*
  * Resolves the split-KV plan paged_decode_attention will use for these
  * sizes: *split_tokens (a multiple of block_size) and *max_splits (the most

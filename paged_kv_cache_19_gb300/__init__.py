@@ -15,7 +15,8 @@ import threading
 import torch
 
 __all__ = [
-    "KVError", "Pool", "kv_pool_create", "kv_pool_destroy", "paged_kv_append", "paged_decode_plan",
+    "KVError", "Pool", "kv_pool_create", "kv_pool_destroy", "paged_kv_append",
+    "paged_norm_rope_append", "paged_decode_plan",
     "paged_decode_cta_heads", "kv_debug_decode_stall",
     "paged_decode_workspace_size", "paged_decode_attention", "paged_decode_attention_split_merge",
     "paged_merge_attention_states",
@@ -89,6 +90,8 @@ def load_library():
             "kv_pool_set_scales": ([P, P, P], I),
             "kv_pool_device_errors": ([P, ctypes.POINTER(ctypes.c_uint32), I], I),
             "paged_kv_append": ([P, P, P, I, P, P, P, I, P, I, P], I),
+            "paged_norm_rope_append": ([P, P, L, P, L, P, L, I, I, P, P, ctypes.c_float, P, I, I, I, P,
+                                        P, P, I, P, I, I, P, P], I),
             "paged_decode_plan": ([P, I, I, I, I, ctypes.POINTER(I), ctypes.POINTER(I)], I),
             "paged_decode_cta_heads": ([P, I, I, I, I, I, ctypes.POINTER(I)], I),
             "kv_debug_decode_stall": ([I, ctypes.c_ulonglong], I),
@@ -258,6 +261,66 @@ def paged_kv_append(pool: Pool, k_new, v_new, block_tables, context_lens=None, t
     _check(lib.paged_kv_append(pool.handle, _ptr(k_new), _ptr(v_new), int(n), _ptr(token_seq),
                                _ptr(token_pos), _ptr(block_tables), int(max_blocks),
                                _ptr(context_lens), int(batch), _stream(stream)), "paged_kv_append")
+
+
+def _rows(t, heads, d, name):
+    """Token stride of a [tokens, heads, d] bf16 tensor whose token rows are contiguous."""
+    if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1:] != (heads, d):
+        raise ValueError(f"{name} must be a CUDA bf16 tensor [tokens, {heads}, {d}], got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {st}")
+    return st[0] if t.shape[0] > 1 else heads * d
+
+
+def paged_norm_rope_append(pool: Pool, q, k, v, block_tables, context_lens=None, q_weight=None,
+                           k_weight=None, eps: float = 1e-6, rope_table=None,
+                           interleaved: bool = False, q_len: int = 1, token_seq=None,
+                           token_pos=None, out=None, stream=None):
+    """RMS norm of every query and key head (weights float32 [d]), rotary rotation by position
+    (rope_table float32 [positions, rope_dim]: cosines then sines), and the append of k and v.
+
+    q [T, Hq, d], k and v [T, Hkv, d]: bf16, rows of a token contiguous, any token stride (slices
+    of one fused projection).  Tokens are addressed as in paged_kv_append, q_len per sequence.
+    Returns the queries [T / q_len, Hq, q_len, d] ([T, Hq, d] for q_len 1 when out is not given)."""
+    lib = load_library()
+    n, heads = q.shape[0], q.shape[1]
+    d = pool.head_dim
+    qs, ks, vs = (_rows(q, heads, d, "q"), _rows(k, pool.kv_heads, d, "k"), _rows(v, pool.kv_heads, d, "v"))
+    if k.shape[0] != n or v.shape[0] != n:
+        raise ValueError("q, k and v must hold the same tokens")
+    _need(block_tables, torch.int32, "block_tables")
+    _need(context_lens, torch.int32, "context_lens")
+    _need(token_seq, torch.int32, "token_seq")
+    _need(token_pos, torch.int32, "token_pos")
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if _need(t, torch.float32, name) is not None and t.shape != (d,):
+            raise ValueError(f"{name} must have shape [{d}]")
+    _need(rope_table, torch.float32, "rope_table")
+    if rope_table is not None and rope_table.dim() != 2:
+        raise ValueError("rope_table must be [positions, rope_dim]")
+    batch, max_blocks = block_tables.shape
+    for t, name in ((token_seq, "token_seq"), (token_pos, "token_pos")):
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{name} must hold one entry per token")
+    if context_lens is not None and context_lens.numel() != batch:
+        raise ValueError("context_lens must hold one entry per sequence")
+    if n % q_len:
+        raise ValueError("the tokens must be q_len per sequence")
+    if out is None:
+        shape = (n, heads, d) if q_len == 1 else (n // q_len, heads, q_len, d)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    _need(out, torch.bfloat16, "out")
+    if out.numel() != n * heads * d:
+        raise ValueError("out does not hold the queries")
+    positions, rope_dim = rope_table.shape if rope_table is not None else (0, 0)
+    _check(lib.paged_norm_rope_append(
+        pool.handle, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, heads, n, _ptr(q_weight),
+        _ptr(k_weight), float(eps), _ptr(rope_table), positions, rope_dim, int(interleaved),
+        _ptr(token_seq), _ptr(token_pos), block_tables.data_ptr(), max_blocks, _ptr(context_lens),
+        batch, int(q_len), out.data_ptr(), _stream(stream)), "paged_norm_rope_append")
+    return out
 
 
 def paged_decode_plan(pool: Pool, batch: int, q_heads: int, max_blocks: int,

@@ -455,6 +455,84 @@ kv_status paged_kv_append(kv_pool* pool, const void* k_new, const void* v_new, i
                                                                                    : KV_ERR_CUDA;
 }
 
+kv_status paged_norm_rope_append(kv_pool* pool, const void* q, int64_t q_stride, const void* k,
+                                 int64_t k_stride, const void* v, int64_t v_stride, int q_heads,
+                                 int num_tokens, const float* q_weight, const float* k_weight,
+                                 float eps, const float* rope, int rope_positions, int rope_dim,
+                                 kv_rope_style style, const int32_t* token_seq,
+                                 const int32_t* token_pos, const int32_t* block_tables,
+                                 int max_blocks, const int32_t* context_lens, int batch, int q_len,
+                                 void* q_out, void* stream)
+{
+    if (pool == nullptr || pool->mla || num_tokens < 0 || batch < 0 || max_blocks <= 0 || q_heads <= 0 ||
+        q_len <= 0)
+        return KV_ERR_INVALID_ARG;
+    if (static_cast<long long>(max_blocks) * pool->block_size > std::numeric_limits<int>::max())
+        return KV_ERR_INVALID_ARG;                  // positions are 32-bit
+    if (num_tokens == 0) return KV_OK;
+    if (q == nullptr || k == nullptr || v == nullptr || q_out == nullptr || block_tables == nullptr || batch == 0)
+        return KV_ERR_INVALID_ARG;
+    if ((token_seq != nullptr || token_pos != nullptr) && q_len != 1) return KV_ERR_INVALID_ARG;
+    if (token_pos == nullptr && context_lens == nullptr) return KV_ERR_INVALID_ARG;
+    if (token_seq == nullptr && num_tokens > static_cast<long long>(batch) * q_len) return KV_ERR_INVALID_ARG;
+    if ((q_weight == nullptr) != (k_weight == nullptr)) return KV_ERR_INVALID_ARG;
+    if (q_weight != nullptr && !(std::isfinite(eps) && eps >= 0.f)) return KV_ERR_INVALID_ARG;
+    if (rope != nullptr && (rope_positions <= 0 || rope_dim <= 0 || rope_dim % 16 != 0 || rope_dim > pool->head_dim))
+        return KV_ERR_INVALID_ARG;
+    if (style != KV_ROPE_HALF && style != KV_ROPE_INTERLEAVED) return KV_ERR_INVALID_ARG;
+    const int64_t d = pool->head_dim;
+    if (q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0 || q_stride < q_heads * d ||
+        k_stride < pool->kv_heads * d || v_stride < pool->kv_heads * d)
+        return KV_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(q_weight, 16) ||
+        !aligned(k_weight, 16) || !aligned(rope, 16) || !aligned(block_tables, 4) || !aligned(token_seq, 4) ||
+        !aligned(token_pos, 4) || !aligned(context_lens, 4))
+        return KV_ERR_INVALID_ARG;
+    // one lane group per row at most, in 32 bits with room for the last CTA's groups
+    if (static_cast<long long>(num_tokens) * (static_cast<long long>(q_heads) + 2 * pool->kv_heads) >
+        std::numeric_limits<int>::max() - 64)
+        return KV_ERR_UNSUPPORTED;
+    kv_status st = check_device(pool);
+    if (st != KV_OK) return st;
+    kvp::NormRopeParams p;
+    p.q = static_cast<const uint16_t*>(q);
+    p.k = static_cast<const uint16_t*>(k);
+    p.v = static_cast<const uint16_t*>(v);
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.q_weight = q_weight;
+    p.k_weight = k_weight;
+    p.rope = rope;
+    p.rope_positions = rope_positions;
+    p.rope_dim = rope != nullptr ? rope_dim : 0;
+    p.interleaved = style == KV_ROPE_INTERLEAVED;
+    p.eps = eps;
+    p.token_seq = token_seq;
+    p.token_pos = token_pos;
+    p.tables = block_tables;
+    p.ctx = context_lens;
+    p.k_pool = pool->k;
+    p.v_pool = pool->v;
+    p.k_scale = pool->k_scale;
+    p.v_scale = pool->v_scale;
+    p.q_out = static_cast<uint16_t*>(q_out);
+    p.err = pool->err;
+    p.num_tokens = num_tokens;
+    p.batch = batch;
+    p.q_heads = q_heads;
+    p.kv_heads = pool->kv_heads;
+    p.max_blocks = max_blocks;
+    p.num_blocks = pool->num_blocks;
+    p.block_size = pool->block_size;
+    p.q_len = q_len;
+    p.chunks = 0;
+    return kvp::launch_norm_rope_append(p, pool->head_dim, pool->dtype == KV_DTYPE_FP8_E4M3,
+                                        static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? KV_OK
+               : KV_ERR_CUDA;
+}
+
 kv_status kv_copy_blocks(kv_pool* pool, const kv_block_copy* copies, int n, void* stream)
 {
     if (pool == nullptr || n < 0) return KV_ERR_INVALID_ARG;

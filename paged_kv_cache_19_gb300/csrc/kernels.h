@@ -71,6 +71,32 @@ struct AppendParams {
                               // sequence i / q_len, at position ctx - q_len + i % q_len
 };
 
+// Norm, rotation and append (norm_rope_append.cu): row r of token i is query head r, key head
+// r - q_heads or value head r - q_heads - kv_heads; strides in elements between tokens.
+struct NormRopeParams {
+    const uint16_t* q;        // bf16, q_heads rows of head_dim per token
+    const uint16_t* k;        // bf16, kv_heads rows per token
+    const uint16_t* v;
+    long long q_stride, k_stride, v_stride;
+    const float* q_weight;    // [head_dim] or null (no norm)
+    const float* k_weight;
+    const float* rope;        // [rope_positions, rope_dim]: cosines then sines; or null
+    int rope_positions, rope_dim, interleaved;
+    float eps;
+    const int32_t* token_seq; // or null: token i is token i % q_len of sequence i / q_len
+    const int32_t* token_pos; // or null: position ctx - q_len + i % q_len
+    const int32_t* tables;
+    const int32_t* ctx;
+    uint8_t* k_pool;
+    uint8_t* v_pool;
+    const float* k_scale;
+    const float* v_scale;
+    uint16_t* q_out;          // bf16 [tokens / q_len, q_heads, q_len, head_dim]
+    uint32_t* err;
+    int num_tokens, batch, q_heads, kv_heads, max_blocks, num_blocks, block_size, q_len;
+    uint32_t chunks;          // lane groups per token (set by the launcher)
+};
+
 // Absorbed multi-head latent attention over a latent pool [num_blocks,
 // block_size, MLA_DK] (latent numbers then the rotary key).  One CTA per
 // (sequence, tile of 16 query heads, split chunk).
@@ -163,6 +189,7 @@ cudaError_t launch_merge_attention_states(const uint16_t* outs, const float* lse
                                           long long rows, int head_dim, uint16_t* out,
                                           float* lse_out, cudaStream_t s);
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
+cudaError_t launch_norm_rope_append(const NormRopeParams& p, int head_dim, bool fp8, cudaStream_t s);
 // Tokens per pipeline stage of the latent decode (0: block size not supported);
 // prod: the variant with a producer warp (small grids), else the three-CTA one.
 int mla_stage_tokens(int block_size, bool prod);
