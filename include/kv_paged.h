@@ -353,6 +353,46 @@ kv_status paged_multi_query_workspace_size(const kv_pool* pool, int batch, int q
                                            int q_len, int max_blocks, int kv_split_tokens,
                                            size_t* bytes);
 
+/* What changes the scores and the keys of paged_attention_masked; a zero-filled
+ * struct changes nothing.  Arrays are device pointers. */
+typedef struct kv_attention_mask {
+    float softcap;              /* scores become softcap * tanh(score / softcap); 0: as they are */
+    int32_t window;             /* a query sees at most this many keys back, its own included; 0: all */
+    const float* alibi_slopes;  /* float32 [q_heads]: score -= slope * |query pos - key pos|; NULL: none */
+    const int32_t* first_keys;  /* int32 [batch]: keys before this position are not seen; NULL: 0 */
+    const int32_t* prefix_lens; /* int32 [batch]: keys before this position are seen by every query,
+                                   later ones than it included; NULL: 0 */
+} kv_attention_mask;
+
+/*
+ * paged_attention_masked -- paged_attention_multi_query (q_len == 1: the decode)
+ * with capped scores, a bias by distance, and masks other than the causal one:
+ * sliding windows, documents packed into one sequence, bidirectional prefixes.
+ *   The query at position p of sequence b sees the keys t with
+ *     max(first_keys[b], p - window + 1) <= t < max(p + 1, min(prefix_lens[b], ctx)),
+ *   ctx = context_lens[b]; the score of a seen key is
+ *     x = scale * q . K[t];  x = softcap * tanh(x / softcap);  x -= slope_h * |p - t|.
+ *   A query that sees no key gets out = 0, lse = -inf.  Blocks that no query of a
+ *   tile of rows sees are not read, and their table entries not looked at: blocks
+ *   that fell out of a window may have been freed and reused.
+ *   mask: HOST struct, copied by the call; NULL = no change.  softcap >= 0 with a
+ *   finite 2 / softcap, window >= 0; slopes finite (not checked).
+ *   Shapes, tables, split, workspace (zero-filled before its first use), outputs
+ *   and errors as in paged_attention_multi_query; the chunks of a sequence begin
+ *   at the first block its queries see.
+ */
+kv_status paged_attention_masked(const kv_pool* pool, const void* q, int q_heads, int q_len,
+                                 const int32_t* block_tables, int max_blocks,
+                                 const int32_t* context_lens, int batch, float scale,
+                                 const kv_attention_mask* mask, int kv_split_tokens,
+                                 void* workspace, size_t workspace_bytes, void* out,
+                                 float* lse_out, void* stream);
+
+/* Workspace bytes of paged_attention_masked for these sizes (window as in the mask). */
+kv_status paged_attention_masked_workspace_size(const kv_pool* pool, int batch, int q_heads,
+                                                int q_len, int max_blocks, int window,
+                                                int kv_split_tokens, size_t* bytes);
+
 /*
  * paged_decode_step -- one decode step of every sequence of the batch: the
  * append of its q_len new tokens (xuewyang.github.io/posts/kv, "A toy vLLM",

@@ -22,6 +22,7 @@ __all__ = [
     "paged_merge_attention_states",
     "paged_attention_multi_query",
     "paged_decode_step",
+    "paged_attention_masked", "paged_attention_masked_workspace_size",
     "paged_multi_query_workspace_size", "library_path", "load_library", "BlockManager",
     "kv_copy_blocks", "BM_FIFO", "BM_LIFO", "BM_PREFIX_CACHING", "kv_mla_pool_create",
     "paged_mla_decode_plan", "paged_mla_workspace_size", "paged_mla_decode_attention",
@@ -55,6 +56,12 @@ _lib = None
 
 class _BlockCopy(ctypes.Structure):
     _fields_ = [("src", ctypes.c_int32), ("dst", ctypes.c_int32)]
+
+
+class _AttentionMask(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("alibi_slopes", ctypes.c_void_p), ("first_keys", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p)]
 
 
 class KVError(RuntimeError):
@@ -103,6 +110,9 @@ def load_library():
             "paged_attention_multi_query": ([P, P, I, I, P, I, P, I, ctypes.c_float, I, P, S, P, P,
                                              P], I),
             "paged_multi_query_workspace_size": ([P, I, I, I, I, I, ctypes.POINTER(S)], I),
+            "paged_attention_masked": ([P, P, I, I, P, I, P, I, ctypes.c_float,
+                                        ctypes.POINTER(_AttentionMask), I, P, S, P, P, P], I),
+            "paged_attention_masked_workspace_size": ([P, I, I, I, I, I, I, ctypes.POINTER(S)], I),
             "paged_decode_step": ([P, P, P, P, I, I, P, I, P, I, ctypes.c_float, I, P, S, P, P, P],
                                   I),
             "kv_bm_create": ([I, I, I, ctypes.POINTER(P)], I),
@@ -481,6 +491,68 @@ def paged_attention_multi_query(pool: Pool, q, block_tables, context_lens, scale
                                            _ptr(workspace), int(ws_bytes), _ptr(out), _ptr(lse),
                                            _stream(stream)),
            "paged_attention_multi_query")
+    return out
+
+
+def paged_attention_masked_workspace_size(pool: Pool, batch: int, q_heads: int, q_len: int,
+                                          max_blocks: int, window: int = 0,
+                                          kv_split_tokens: int = 0) -> int:
+    lib = load_library()
+    n = ctypes.c_size_t()
+    _check(lib.paged_attention_masked_workspace_size(pool.handle, int(batch), int(q_heads), int(q_len),
+                                                     int(max_blocks), int(window),
+                                                     int(kv_split_tokens), ctypes.byref(n)),
+           "paged_attention_masked_workspace_size")
+    return n.value
+
+
+def _queries(pool, q, block_tables, context_lens, out, lse):
+    """Checks of an attention call over q [B, Hq, q_len, d] or [B, Hq, d]; (batch, heads, q_len)."""
+    _need(q, torch.bfloat16, "q")
+    _need(block_tables, torch.int32, "block_tables")
+    _need(context_lens, torch.int32, "context_lens")
+    _need(out, torch.bfloat16, "out")
+    _need(lse, torch.float32, "lse")
+    if q.dim() not in (3, 4) or q.shape[-1] != pool.head_dim:
+        raise ValueError(f"q must be [batch, q_heads, {pool.head_dim}] or [batch, q_heads, q_len, {pool.head_dim}]")
+    batch, heads = q.shape[0], q.shape[1]
+    q_len = q.shape[2] if q.dim() == 4 else 1
+    if block_tables.dim() != 2 or block_tables.shape[0] != batch or context_lens.numel() != batch:
+        raise ValueError("block_tables and context_lens must hold one row per sequence of q")
+    if out.numel() != q.numel() or (lse is not None and lse.numel() != batch * heads * q_len):
+        raise ValueError("out / lse sizes do not match q")
+    return batch, heads, q_len
+
+
+def paged_attention_masked(pool: Pool, q, block_tables, context_lens, scale: float,
+                           softcap: float = 0.0, window: int = 0, alibi_slopes=None,
+                           first_keys=None, prefix_lens=None, kv_split_tokens: int = 0,
+                           workspace=None, out=None, lse=None, stream=None):
+    """Attention of the new tokens of every sequence with capped scores (softcap * tanh(x /
+    softcap)), a sliding window, a bias by distance (alibi_slopes float32 [Hq]), a first visible
+    key per sequence (first_keys int32 [B]) and a prefix every query sees (prefix_lens int32
+    [B]); q bf16 [B, Hq, d] or [B, Hq, q_len, d].  Returns out (shaped like q)."""
+    lib = load_library()
+    if out is None:
+        out = torch.empty_like(q)
+    batch, heads, q_len = _queries(pool, q, block_tables, context_lens, out, lse)
+    _need(alibi_slopes, torch.float32, "alibi_slopes")
+    if alibi_slopes is not None and alibi_slopes.numel() != heads:
+        raise ValueError("alibi_slopes must hold one slope per query head")
+    for t, name in ((first_keys, "first_keys"), (prefix_lens, "prefix_lens")):
+        if _need(t, torch.int32, name) is not None and t.numel() != batch:
+            raise ValueError(f"{name} must hold one position per sequence")
+    max_blocks = block_tables.shape[1]
+    if workspace is None:
+        need = paged_attention_masked_workspace_size(pool, batch, heads, q_len, max_blocks, window, kv_split_tokens)
+        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device) if need else None
+    _need(workspace, torch.uint8, "workspace")
+    mask = _AttentionMask(float(softcap), int(window), _ptr(alibi_slopes), _ptr(first_keys), _ptr(prefix_lens))
+    _check(lib.paged_attention_masked(
+        pool.handle, q.data_ptr(), heads, q_len, block_tables.data_ptr(), max_blocks,
+        context_lens.data_ptr(), batch, float(scale), ctypes.byref(mask), int(kv_split_tokens),
+        _ptr(workspace), 0 if workspace is None else workspace.numel(), out.data_ptr(), _ptr(lse),
+        _stream(stream)), "paged_attention_masked")
     return out
 
 

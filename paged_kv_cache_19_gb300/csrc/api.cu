@@ -211,6 +211,57 @@ kv_status make_plan(const kv_pool* pl, int batch, int q_heads, int q_len, int ma
     return KV_OK;
 }
 
+// Split plan of the span kernel, whose tiles see at most `span_blocks` blocks of a sequence:
+// one CTA per kv head and row tile, and chunks about a sixth of what one SM would take, at
+// least 16 blocks.
+kv_status make_span_plan(const kv_pool* pl, int batch, int q_heads, int q_len, int max_blocks,
+                         int span_blocks, int split_tokens, Plan* out)
+{
+    Plan p;
+    kv_status st = make_plan(pl, batch, q_heads, q_len, max_blocks, split_tokens, &p);
+    if (st != KV_OK) return st;
+    p.cta_heads = 1;
+    if (split_tokens > 0) {
+        p.split_blocks = split_tokens / pl->block_size;
+    } else {
+        const long long units = static_cast<long long>(batch > 0 ? batch : 1) * pl->kv_heads * p.head_groups;
+        const long long target = static_cast<long long>(pl->num_sms > 0 ? pl->num_sms : 148) * 6;
+        long long sb = (units * span_blocks + target - 1) / target;
+        if (sb < 16) sb = 16;
+        if (sb > 192) sb = 192;
+        p.split_blocks = static_cast<int>(sb);
+    }
+    if (p.split_blocks > span_blocks) p.split_blocks = span_blocks;
+    p.max_splits = (span_blocks + p.split_blocks - 1) / p.split_blocks;
+    if (p.max_splits > 65535) return KV_ERR_UNSUPPORTED;      // grid z limit
+    *out = p;
+    return KV_OK;
+}
+
+// Window as the kernel takes it: one that covers every position is none.
+int effective_window(const kv_pool* pl, int window, int max_blocks)
+{
+    return window >= static_cast<long long>(max_blocks) * pl->block_size ? 0 : window;
+}
+
+// Most blocks that a tile's rows see: window + q_len - 1 tokens at any offset, or all.
+int masked_span_blocks(const kv_pool* pl, int q_len, int max_blocks, int window)
+{
+    if (window <= 0) return max_blocks;
+    const long long tokens = static_cast<long long>(window) + q_len - 1;
+    const long long blocks = (tokens + pl->block_size - 2) / pl->block_size + 1;
+    return blocks < max_blocks ? static_cast<int>(blocks) : max_blocks;
+}
+
+kv_status make_masked_plan(const kv_pool* pl, int batch, int q_heads, int q_len, int max_blocks,
+                           int window, int split_tokens, Plan* out)
+{
+    if (pl == nullptr || window < 0 || q_len <= 0 || max_blocks <= 0) return KV_ERR_INVALID_ARG;
+    window = effective_window(pl, window, max_blocks);
+    return make_span_plan(pl, batch, q_heads, q_len, max_blocks,
+                          masked_span_blocks(pl, q_len, max_blocks, window), split_tokens, out);
+}
+
 // Workspace layout (only when a sequence can have several chunks): partial
 // outputs [batch, q_heads, max_splits, d], (max, sum) pairs [batch, q_heads,
 // max_splits, 2], then one ticket per (sequence, kv head, head tile).
@@ -332,6 +383,9 @@ kv_status kv_pool_create(int num_blocks, int block_size, int kv_heads, int head_
         for (int nt : {8, 16}) {
             cudaError_t e = fp8 ? kvp::prepare_decode_fp8(head_dim, block_size, nt)
                                 : kvp::prepare_decode_bf16(head_dim, block_size, nt);
+            if (e == cudaSuccess)
+                e = fp8 ? kvp::prepare_span_fp8(head_dim, block_size, nt)
+                        : kvp::prepare_span_bf16(head_dim, block_size, nt);
             if (e != cudaSuccess) st = KV_ERR_CUDA;
         }
         if (kvp::prepare_decode_heads(fp8, head_dim, block_size) != cudaSuccess) st = KV_ERR_CUDA;
@@ -602,17 +656,15 @@ kv_status paged_decode_workspace_size(const kv_pool* pool, int batch, int q_head
 
 namespace {
 
-// Validates a decode call and fills its kernel parameters and grid (nothing launched).
-kv_status make_decode_launch(const kv_pool* pool, const void* q, int q_heads, int q_len,
-                             const int32_t* block_tables, int max_blocks,
-                             const int32_t* context_lens, int batch, float scale,
-                             int kv_split_tokens, void* workspace, size_t workspace_bytes,
-                             void* out, float* lse_out, Plan* plan_out, kvp::DecodeParams* pp,
-                             dim3* grid)
+// Validates a decode call of a given plan and fills its kernel parameters and grid (nothing
+// launched).  extra_workspace: bytes the call needs beside the plan's own.
+kv_status fill_decode_launch(const kv_pool* pool, const Plan& plan, const void* q, int q_heads,
+                             int q_len, const int32_t* block_tables, int max_blocks,
+                             const int32_t* context_lens, int batch, float scale, void* workspace,
+                             size_t workspace_bytes, size_t extra_workspace, void* out,
+                             float* lse_out, kvp::DecodeParams* pp, dim3* grid)
 {
-    Plan plan;
-    kv_status st = make_plan(pool, batch, q_heads, q_len, max_blocks, kv_split_tokens, &plan);
-    if (st != KV_OK) return st;
+    kv_status st;
     if (pool->mla) return KV_ERR_INVALID_ARG;        // latent pools: paged_mla_decode_attention
     if (batch == 0) return KV_OK;
     if (q == nullptr || block_tables == nullptr || context_lens == nullptr || out == nullptr)
@@ -624,7 +676,8 @@ kv_status make_decode_launch(const kv_pool* pool, const void* q, int q_heads, in
     if (batch > 65535 || static_cast<long long>(pool->kv_heads) * plan.head_groups > 65535)
         return KV_ERR_UNSUPPORTED;                  // grid x / y limits
     const size_t need = workspace_bytes_for(pool, batch, plan);
-    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KV_ERR_INVALID_ARG;
+    const size_t whole = extra_workspace > 0 ? round_up(need, kAlign) + extra_workspace : need;
+    if (whole > 0 && (workspace == nullptr || workspace_bytes < whole)) return KV_ERR_INVALID_ARG;
     st = check_device(pool);
     if (st != KV_OK) return st;
 
@@ -664,8 +717,24 @@ kv_status make_decode_launch(const kv_pool* pool, const void* q, int q_heads, in
     // chunk-major grid: x = (kv head group, row tile), y = sequence, z = chunk
     *grid = dim3(static_cast<unsigned>(pool->kv_heads / plan.cta_heads * plan.head_groups),
                  static_cast<unsigned>(batch), static_cast<unsigned>(plan.max_splits));
-    *plan_out = plan;
     return KV_OK;
+}
+
+// Validates a decode call and fills its kernel parameters and grid (nothing launched).
+kv_status make_decode_launch(const kv_pool* pool, const void* q, int q_heads, int q_len,
+                             const int32_t* block_tables, int max_blocks,
+                             const int32_t* context_lens, int batch, float scale,
+                             int kv_split_tokens, void* workspace, size_t workspace_bytes,
+                             void* out, float* lse_out, Plan* plan_out, kvp::DecodeParams* pp,
+                             dim3* grid)
+{
+    Plan plan;
+    kv_status st = make_plan(pool, batch, q_heads, q_len, max_blocks, kv_split_tokens, &plan);
+    if (st != KV_OK) return st;
+    st = fill_decode_launch(pool, plan, q, q_heads, q_len, block_tables, max_blocks, context_lens,
+                            batch, scale, workspace, workspace_bytes, 0, out, lse_out, pp, grid);
+    if (st == KV_OK) *plan_out = plan;
+    return st;
 }
 
 kv_status launch_decode(const kv_pool* pool, const Plan& plan, dim3 grid, const kvp::DecodeParams& p,
@@ -687,6 +756,15 @@ kv_status launch_decode(const kv_pool* pool, const Plan& plan, dim3 grid, const 
     return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }
 
+kv_status launch_span(const kv_pool* pool, const Plan& plan, dim3 grid, const kvp::SpanParams& p, void* stream)
+{
+    const auto launch = pool->dtype == KV_DTYPE_BF16 ? kvp::launch_span_bf16 : kvp::launch_span_fp8;
+    return launch(pool->head_dim, pool->block_size, plan.head_tile, grid, pool->tmk, pool->tmv, p,
+                  static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? KV_OK
+               : KV_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -706,6 +784,48 @@ kv_status paged_attention_multi_query(const kv_pool* pool, const void* q, int q_
                                             workspace_bytes, out, lse_out, &plan, &p, &grid);
     if (st != KV_OK || batch == 0) return st;
     return launch_decode(pool, plan, grid, p, stream);
+}
+
+kv_status paged_attention_masked_workspace_size(const kv_pool* pool, int batch, int q_heads,
+                                                int q_len, int max_blocks, int window,
+                                                int kv_split_tokens, size_t* bytes)
+{
+    if (bytes == nullptr) return KV_ERR_INVALID_ARG;
+    Plan p;
+    kv_status st = make_masked_plan(pool, batch, q_heads, q_len, max_blocks, window, kv_split_tokens, &p);
+    if (st != KV_OK) return st;
+    *bytes = workspace_bytes_for(pool, batch, p);
+    return KV_OK;
+}
+
+kv_status paged_attention_masked(const kv_pool* pool, const void* q, int q_heads, int q_len,
+                                 const int32_t* block_tables, int max_blocks,
+                                 const int32_t* context_lens, int batch, float scale,
+                                 const kv_attention_mask* mask, int kv_split_tokens,
+                                 void* workspace, size_t workspace_bytes, void* out,
+                                 float* lse_out, void* stream)
+{
+    kv_attention_mask m = {};
+    if (mask != nullptr) m = *mask;
+    if (!(m.softcap >= 0.f) || !std::isfinite(m.softcap) || (m.softcap > 0.f && !std::isfinite(2.f / m.softcap)))
+        return KV_ERR_INVALID_ARG;
+    if (!aligned(m.alibi_slopes, 4) || !aligned(m.first_keys, 4) || !aligned(m.prefix_lens, 4))
+        return KV_ERR_INVALID_ARG;
+    Plan plan;
+    kv_status st = make_masked_plan(pool, batch, q_heads, q_len, max_blocks, m.window, kv_split_tokens, &plan);
+    if (st != KV_OK) return st;
+    kvp::SpanParams p;
+    dim3 grid;
+    st = fill_decode_launch(pool, plan, q, q_heads, q_len, block_tables, max_blocks, context_lens, batch, scale,
+                            workspace, workspace_bytes, 0, out, lse_out, &p.d, &grid);
+    if (st != KV_OK || batch == 0) return st;
+    p.window = effective_window(pool, m.window, max_blocks);
+    p.cap_log2 = m.softcap * 1.4426950408889634f;
+    p.cap_in = m.softcap > 0.f ? 2.f / m.softcap : 0.f;
+    p.slopes = m.alibi_slopes;
+    p.first_keys = m.first_keys;
+    p.prefix_lens = m.prefix_lens;
+    return launch_span(pool, plan, grid, p, stream);
 }
 
 kv_status paged_decode_step(kv_pool* pool, const void* k_new, const void* v_new, const void* q,

@@ -165,21 +165,37 @@ __device__ __forceinline__ void row_offsets(int (&dt)[NTT][2], int row0, int q_l
         for (int j = 0; j < 2; ++j) dt[nt][j] = q_len - 1 - (row0 + nt * 8 + 2 * c + j) % q_len;
 }
 
+// Which keys of a block a row sees, and what its raw score becomes (log2-domain logit, or
+// -inf for a key it does not see).  The causal rule: lim = ctx minus the block's first token
+// position (may exceed BS): token k of the block is a key for a row with causal offset dt
+// when k < lim - dt; tokens at or past lim are not in the cache at all and their values are
+// never used.
+template <int NTT>
+struct CausalRows {
+    int lim;
+    const int (&dt)[NTT][2];
+    float sl2;
+    __device__ __forceinline__ float logit(float s, int tok, int nt, int j) const
+    {
+        return tok < lim - dt[nt][j] ? s * sl2 : -INFINITY;
+    }
+    // values of tokens outside [value_lo, value_hi) of the block are never used
+    __device__ __forceinline__ int value_lo() const { return 0; }
+    __device__ __forceinline__ int value_hi() const { return lim; }
+};
+
 // One cache block (BS tokens of one kv head, K tile at tk, V tile at tv in
-// shared memory) folded into the warp's online-softmax state.  lim = ctx minus
-// the block's first token position (may exceed BS): token k of the block is a
-// key for a row with causal offset dt when k < lim - dt; tokens at or past
-// lim are not in the cache at all and their values are never used.
-template <bool FP8, int D, int BS, int NT>
-__device__ __forceinline__ void process_block(uint32_t tk, uint32_t tv, int lim,
-                                              const int (&dt)[NT / 8][2],
-                                              const uint32_t (&qf)[D / 16][NT / 8][2], float sl2,
-                                              WarpState<DecodeCfg<FP8, D, BS, NT>>& st, int lane)
+// shared memory) folded into the warp's online-softmax state, under the rule of `rows`.
+template <bool FP8, int D, int BS, int NT, class Rows>
+__device__ __forceinline__ void process_block_rows(uint32_t tk, uint32_t tv, const Rows& rows,
+                                                   const uint32_t (&qf)[D / 16][NT / 8][2],
+                                                   WarpState<DecodeCfg<FP8, D, BS, NT>>& st, int lane)
 {
     using C = DecodeCfg<FP8, D, BS, NT>;
     const int r = lane >> 2;
     const int c = lane & 3;
-    const int nvalid = min(BS, lim);
+    const int nvalid = min(BS, rows.value_hi());
+    const int nskip = rows.value_lo();
 
     // ---- scores S^T[tokens x heads] = K . Q^T
     float s[C::MT][C::NTT][4];
@@ -235,7 +251,7 @@ __device__ __forceinline__ void process_block(uint32_t tk, uint32_t tv, int lim,
 #pragma unroll
                 for (int hi = 0; hi < 2; ++hi) {
                     const int tok = mt * 16 + r + 8 * hi;
-                    const float x = tok < lim - dt[nt][j] ? s[mt][nt][2 * hi + j] * sl2 : -INFINITY;
+                    const float x = rows.logit(s[mt][nt][2 * hi + j], tok, nt, j);
                     s[mt][nt][2 * hi + j] = x;
                     mx = fmaxf(mx, x);
                 }
@@ -289,15 +305,16 @@ __device__ __forceinline__ void process_block(uint32_t tk, uint32_t tv, int lim,
         }
 
     // ---- O^T[d x heads] += V^T[d x tokens] . P^T[tokens x heads]
-    const bool partial = nvalid < BS;
+    const bool partial = nvalid < BS || nskip > 0;
+    const auto held = [&](int t) { return t < nvalid && t >= nskip; };
 #pragma unroll
     for (int mt = 0; mt < C::MT; ++mt) {
         const int t0 = mt * 16 + 2 * c;     // tokens of this thread: t0, t0+1, t0+8, t0+9
         if constexpr (!FP8) {
             uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;
             if (partial) {
-                mlo = (t0 < nvalid ? 0x0000ffffu : 0u) | (t0 + 1 < nvalid ? 0xffff0000u : 0u);
-                mhi = (t0 + 8 < nvalid ? 0x0000ffffu : 0u) | (t0 + 9 < nvalid ? 0xffff0000u : 0u);
+                mlo = (held(t0) ? 0x0000ffffu : 0u) | (held(t0 + 1) ? 0xffff0000u : 0u);
+                mhi = (held(t0 + 8) ? 0x0000ffffu : 0u) | (held(t0 + 9) ? 0xffff0000u : 0u);
             }
             const int quad = lane >> 3;     // 8x8 tile: (d half = quad & 1, token half = quad >> 1)
             const int tok = mt * 16 + (lane & 7) + (quad >> 1) * 8;
@@ -323,10 +340,10 @@ __device__ __forceinline__ void process_block(uint32_t tk, uint32_t tv, int lim,
             uint4 v3 = lds128(swz<1>(tv, t0 + 9, r));
             if (partial) {
                 const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                if (t0 >= nvalid) v0 = z;
-                if (t0 + 1 >= nvalid) v1 = z;
-                if (t0 + 8 >= nvalid) v2 = z;
-                if (t0 + 9 >= nvalid) v3 = z;
+                if (!held(t0)) v0 = z;
+                if (!held(t0 + 1)) v1 = z;
+                if (!held(t0 + 8)) v2 = z;
+                if (!held(t0 + 9)) v3 = z;
             }
             const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w};
             const uint32_t w1[4] = {v1.x, v1.y, v1.z, v1.w};
@@ -356,6 +373,15 @@ __device__ __forceinline__ void process_block(uint32_t tk, uint32_t tv, int lim,
             }
         }
     }
+}
+
+template <bool FP8, int D, int BS, int NT>
+__device__ __forceinline__ void process_block(uint32_t tk, uint32_t tv, int lim,
+                                              const int (&dt)[NT / 8][2],
+                                              const uint32_t (&qf)[D / 16][NT / 8][2], float sl2,
+                                              WarpState<DecodeCfg<FP8, D, BS, NT>>& st, int lane)
+{
+    process_block_rows<FP8, D, BS, NT>(tk, tv, CausalRows<NT / 8>{lim, dt, sl2}, qf, st, lane);
 }
 
 // The per-thread row sums of a warp summed over the 8 row groups sharing a column.

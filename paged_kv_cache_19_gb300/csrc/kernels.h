@@ -53,6 +53,17 @@ struct DecodeParams {
     unsigned long long consumer_wait_ns;
 };
 
+// Attention over a span of each sequence's keys (decode_span.cuh): the decode's parameters and
+// the rule of the rows.
+struct SpanParams {
+    DecodeParams d;
+    int window;               // keys a query sees back from its own position, itself included (0: all)
+    float cap_log2, cap_in;   // score cap * log2(e) and 2 / cap; 0 without a cap
+    const float* slopes;      // [q_heads] distance bias or null
+    const int32_t* first_keys;   // [batch] or null
+    const int32_t* prefix_lens;  // [batch] or null
+};
+
 struct AppendParams {
     const uint16_t* k_new;    // bf16 [num_tokens, kv_heads, head_dim]
     const uint16_t* v_new;
@@ -170,6 +181,14 @@ cudaError_t launch_decode_bf16(int head_dim, int block_size, int head_tile, dim3
 cudaError_t launch_decode_fp8(int head_dim, int block_size, int head_tile, dim3 grid,
                               const CUtensorMap& tk, const CUtensorMap& tv,
                               const DecodeParams& p, cudaStream_t s);
+cudaError_t prepare_span_bf16(int head_dim, int block_size, int head_tile);
+cudaError_t prepare_span_fp8(int head_dim, int block_size, int head_tile);
+cudaError_t launch_span_bf16(int head_dim, int block_size, int head_tile, dim3 grid,
+                             const CUtensorMap& tk, const CUtensorMap& tv, const SpanParams& p,
+                             cudaStream_t s);
+cudaError_t launch_span_fp8(int head_dim, int block_size, int head_tile, dim3 grid,
+                            const CUtensorMap& tk, const CUtensorMap& tv, const SpanParams& p,
+                            cudaStream_t s);
 // The decode kernel with one CTA per group of `heads` kv heads (decode_heads.cuh), `ctas`
 // CTAs per SM; the variants built are listed in decode_heads.cu.
 bool decode_heads_supported(bool fp8, int head_dim, int block_size, int head_tile, int heads,

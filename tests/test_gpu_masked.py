@@ -1,0 +1,232 @@
+"""paged_attention_masked against attention in 64 bits: capped scores, distance bias, windows,
+document starts and visible prefixes, over pools whose unseen blocks are poisoned or gone."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_19_gb300 as kp
+from attention_util import Cache
+from gpu_util import i32
+
+pytestmark = pytest.mark.gpu
+
+
+def hide(window=0, first=None, prefix=None):
+    def f(b, pos, t):
+        h = t > pos
+        if prefix is not None:
+            h &= t >= prefix[b]
+        if window:
+            h |= t <= pos - window
+        if first is not None:
+            h |= t < first[b]
+        return h
+    return f
+
+
+def run(c, split=0, lse=True, **kw):
+    out = torch.full_like(c.q, float("nan"))
+    l = torch.full(c.q.shape[:3], float("nan"), device="cuda") if lse else None  # noqa: E741
+    kp.paged_attention_masked(c.pool, c.q, c.tables, c.lens, c.scale, kv_split_tokens=split, out=out, lse=l, **kw)
+    return out, l
+
+
+def slopes_of(hq):
+    return torch.tensor(2.0 ** (-8.0 * np.arange(1, hq + 1) / hq), dtype=torch.float32)
+
+
+SHAPES = [
+    dict(hq=4, hk=4, d=64, bs=16, ctx=[1, 17, 64, 129]),
+    dict(hq=32, hk=8, d=128, bs=16, ctx=[300, 5, 1024, 16]),
+    dict(hq=8, hk=1, d=128, bs=32, ctx=[33, 2000]),
+    dict(hq=6, hk=2, d=64, bs=32, ctx=[1, 31, 32, 500], q_len=1),
+    dict(hq=16, hk=2, d=128, bs=16, ctx=[7, 40, 700], q_len=7),
+    dict(hq=4, hk=2, d=64, bs=16, ctx=[40, 333], q_len=33),
+    dict(hq=8, hk=4, d=128, bs=32, ctx=[3, 65, 900], q_len=3, fp8=True),
+    dict(hq=32, hk=32, d=128, bs=16, ctx=[100, 1], fp8=True),
+    dict(hq=4, hk=1, d=128, bs=16, ctx=[9, 1000], q_len=5, fp8=True),
+]
+RULES = ["none", "cap", "alibi", "window1", "window", "first", "prefix", "all"]
+
+
+@pytest.mark.parametrize("rule", RULES)
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "-".join(f"{k}{v}" for k, v in s.items()).replace(" ", ""))
+def test_matches_the_formula(shape, rule):
+    c = Cache(seed=len(shape) + len(rule), **shape)
+    r = np.random.default_rng(5)
+    kw, ref, first, prefix, window = {}, {}, None, None, 0
+    if rule in ("cap", "all"):
+        kw["softcap"] = ref["softcap"] = 2.0 if rule == "cap" else 30.0
+    if rule in ("alibi", "all"):
+        s = slopes_of(c.hq)
+        kw["alibi_slopes"], ref["slopes"] = s.cuda(), s.numpy()
+    if rule.startswith("window") or rule == "all":
+        kw["window"] = window = 1 if rule == "window1" else 37
+    if rule in ("first", "all"):
+        first = r.integers(0, c.ctx + 1)            # may leave rows without a key
+        kw["first_keys"] = i32(first)
+    if rule in ("prefix", "all"):
+        prefix = r.integers(0, c.ctx + 20)          # may reach past the context
+        kw["prefix_lens"] = i32(prefix)
+    want = c.reference(hide(window, first, prefix), **ref)
+    for split in (0, c.bs, 5 * c.bs):
+        c.check(*run(c, split, **kw), want)
+    assert c.pool.device_errors() == 0
+    c.pool.destroy()
+
+
+def test_no_rule_is_the_plain_attention():
+    """Within rounding of paged_decode_attention and paged_attention_multi_query (bit for bit with
+    the same chunks: the arithmetic is the same)."""
+    for q_len in (1, 4):
+        c = Cache(ctx=[50, 900, 4], hq=8, hk=2, d=128, bs=16, q_len=q_len)
+        out, lse = run(c, 128)
+        out2, lse2 = torch.empty_like(out), torch.empty_like(lse)
+        kp.paged_attention_multi_query(c.pool, c.q, c.tables, c.lens, c.scale, kv_split_tokens=128, out=out2, lse=lse2)
+        assert torch.equal(out, out2) and torch.equal(lse, lse2)
+        c.pool.destroy()
+
+
+def test_freed_blocks_before_a_window_are_not_looked_at():
+    c = Cache(ctx=[500, 90, 4], hq=8, hk=2, d=128, bs=16, q_len=2)
+    want = c.reference(hide(40))
+    tab = c.tab.copy()
+    raw = c.pool.raw_bytes()
+    for b in range(3):
+        lo = max(0, c.ctx[b] - 2 - 40 + 1) // 16
+        for j in range(lo):
+            for t in raw:
+                t[tab[b, j]] = 0xFF
+            tab[b, j] = [-1, 10 ** 6][j % 2]
+    c.tables = i32(tab)
+    c.check(*run(c, window=40), want)
+    assert c.pool.device_errors() == 0
+    c.pool.destroy()
+
+
+def test_nan_and_infinite_keys_and_values_behind_the_masks():
+    """Slots of a visible block that no row sees may hold anything."""
+    c = Cache(ctx=[61, 30], hq=4, hk=2, d=64, bs=32, q_len=1)
+    first = np.array([37, 29])
+    want = c.reference(hide(0, first))
+    k, v, _, _ = c.pool.tensors()
+    for b in range(2):
+        for t in range(first[b]):
+            at = c.tab[b, t // 32], t % 32
+            k[at] = [float("nan"), float("inf"), -float("inf")][t % 3]
+            v[at] = [float("inf"), float("nan"), -float("inf")][t % 3]
+    c.check(*run(c, first_keys=i32(first)), want)
+    c.pool.destroy()
+
+
+def test_large_and_small_caps_keep_small_scores():
+    """tanh near zero and saturated: a cap far above the scores changes nothing, one far below
+    them flattens all keys."""
+    c = Cache(ctx=[200], hq=4, hk=2, d=64, bs=16)
+    plain = c.reference()
+    c.check(*run(c, softcap=1e6), plain)
+    for cap in (1e-3, 0.7, 1e30):
+        c.check(*run(c, softcap=cap), c.reference(softcap=cap))
+    c.pool.destroy()
+
+
+def test_long_context_with_bias_and_every_split():
+    c = Cache(ctx=[20011, 3], hq=8, hk=1, d=128, bs=16, seed=9)
+    s = slopes_of(8)
+    want = c.reference(slopes=s.numpy())
+    for split in (0, 16, 4096):
+        c.check(*run(c, split, alibi_slopes=s.cuda()), want)
+    c.pool.destroy()
+
+
+def test_padded_batch_bad_lengths_and_bad_blocks():
+    """Context 0 gives 0 and -inf; lengths out of range are clamped, bad blocks skipped, both flagged."""
+    c = Cache(ctx=[40, 0, 33], hq=4, hk=2, d=64, bs=16)
+    out, lse = run(c, window=20)
+    assert c.pool.device_errors() == 0
+    c.check(out, lse, c.reference(hide(20)))
+    assert not out[1].any() and (lse[1] == -float("inf")).all()
+    c.lens = i32([40, -5, 1000])
+    run(c)
+    assert c.pool.device_errors() & kp.DEVERR_CONTEXT
+    c.lens = i32([40, 0, 33])
+    tab = c.tab.copy()
+    tab[0, 1] = -7
+    c.tables = i32(tab)
+    got = run(c)
+    assert c.pool.device_errors() == kp.DEVERR_BLOCK_ID
+    c.check(*got, c.reference(lambda b, pos, t: (t > pos) | ((b == 0) & (t // 16 == 1))))
+    c.pool.destroy()
+
+
+def test_workspace_is_reused_streams_and_graphs():
+    """One zeroed workspace over many calls, another stream, and a graph replayed with new lengths."""
+    c = Cache(ctx=[700, 90, 300], hq=8, hk=2, d=128, bs=16)
+    need = kp.paged_attention_masked_workspace_size(c.pool, 3, 8, 1, c.max_blocks, 200, 32)
+    assert need > 0
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    want = c.reference(hide(200))
+    for _ in range(3):
+        c.check(*run(c, 32, window=200, workspace=ws), want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = run(c, 32, window=200, workspace=ws)
+    torch.cuda.current_stream().wait_stream(s)
+    c.check(*got, want)
+    out = torch.empty_like(c.q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kp.paged_attention_masked(c.pool, c.q, c.tables, c.lens, c.scale, window=200, kv_split_tokens=32,
+                                  workspace=ws, out=out)
+    c.ctx = np.array([650, 16, 1])
+    c.lens.copy_(i32(c.ctx))
+    for _ in range(2):
+        g.replay()
+        c.check(out, None, c.reference(hide(200)))
+    assert c.pool.device_errors() == 0
+    c.pool.destroy()
+
+
+def test_window_shrinks_the_workspace():
+    c = Cache(ctx=[700], hq=8, hk=2, d=128, bs=16)
+    size = lambda w: kp.paged_attention_masked_workspace_size(c.pool, 1, 8, 1, c.max_blocks, w, 16)  # noqa: E731
+    assert size(17) < size(100) < size(0) == size(1 << 30) == size(44 * 16)
+    c.pool.destroy()
+
+
+def test_refusals():
+    c = Cache(ctx=[40, 30], hq=4, hk=2, d=64, bs=16)
+    before = c.q.clone()
+    for kw in (dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=float("inf")), dict(softcap=1e-45),
+               dict(window=-1), dict(split=7), dict(split=-16), dict(workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"), split=16)):
+        with pytest.raises(kp.KVError) as e:
+            run(c, **kw)
+        assert e.value.status == kp.KV_ERR_INVALID_ARG
+    for kw in (dict(alibi_slopes=torch.ones(3, device="cuda")), dict(first_keys=i32([1])), dict(prefix_lens=i32([1, 2, 3])),
+               dict(alibi_slopes=torch.ones(4, dtype=torch.float64, device="cuda"))):
+        with pytest.raises(ValueError):
+            run(c, **kw)
+    with pytest.raises(ValueError):
+        kp.paged_attention_masked(c.pool, c.q, c.tables[:1], c.lens, c.scale)
+    with pytest.raises(kp.KVError):
+        kp.paged_attention_masked(c.pool, c.q, c.tables, c.lens, float("nan"))
+    with pytest.raises(kp.KVError):
+        kp.paged_attention_masked(c.pool, c.q[:, :3].contiguous(), c.tables, c.lens, c.scale)
+    assert torch.equal(c.q, before) and c.pool.device_errors() == 0
+    empty = kp.paged_attention_masked(c.pool, c.q[:0], c.tables[:0], c.lens[:0], c.scale, window=3)
+    assert empty.shape[0] == 0
+    c.pool.destroy()
+
+
+def test_a_stage_that_never_lands_times_out():
+    c = Cache(ctx=[900], hq=4, hk=1, d=128, bs=16)
+    kp.kv_debug_decode_stall(3, 20_000_000)
+    try:
+        run(c, 256, window=500)
+        torch.cuda.synchronize()
+    finally:
+        kp.kv_debug_decode_stall(-1, 0)
+    assert c.pool.device_errors() & kp.DEVERR_TIMEOUT
+    c.check(*run(c, 256, window=500), c.reference(hide(500)))
+    c.pool.destroy()
