@@ -117,6 +117,21 @@ kv_status kv_bm_build_tables(const kv_block_manager* bm, const int64_t* seqs, in
                              int max_blocks, int32_t* block_tables, int32_t* context_lens);
 
 /*
+ * Groups of the listed sequences that hold the same blocks at their start, for
+ * paged_shared_prefix_attention: order [batch] gets a permutation of 0 .. batch - 1
+ * (sequences of a group next to each other, groups by their first sequence in the
+ * list), group_offsets [batch + 1] and group_blocks [batch] the *n_groups groups
+ * over that order.  Sequences are grouped by the block at table entry
+ * min_blocks - 1 (min_blocks >= 1: fewer common blocks are not worth a group); a
+ * group's block count is the length of the start that all of its sequences have in
+ * common, counting only blocks that every sequence has filled.  The other sequences
+ * form groups of one with 0 blocks.  KV_ERR_INVALID_ARG if a sequence is unknown.
+ */
+kv_status kv_bm_prefix_groups(const kv_block_manager* bm, const int64_t* seqs, int batch,
+                              int min_blocks, int32_t* order, int32_t* group_offsets,
+                              int32_t* group_blocks, int* n_groups);
+
+/*
  * Device: copies whole blocks of the pool (K and V, every slot and kv head),
  * copies[i].src -> copies[i].dst for i < n, on the stream.  copies is a DEVICE
  * array of n kv_block_copy.  Ids outside the pool are skipped and flagged

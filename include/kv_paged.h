@@ -69,6 +69,8 @@ typedef enum kv_dtype {
 #define KV_DEVERR_SEQ      0x4u  /* an appended token named a sequence outside [0, batch) */
 #define KV_DEVERR_POSITION 0x8u  /* an appended token's position was < 0 or past the table */
 #define KV_DEVERR_TIMEOUT  0x10u /* a pipeline wait gave up after its time limit (about 2 s) */
+#define KV_DEVERR_GROUP    0x20u /* group offsets out of order or outside the batch, or a shared block
+                                    count outside [0, max_blocks]: computed without sharing */
 
 typedef struct kv_pool kv_pool;  /* opaque; owned by the library */
 
@@ -392,6 +394,45 @@ kv_status paged_attention_masked(const kv_pool* pool, const void* q, int q_heads
 kv_status paged_attention_masked_workspace_size(const kv_pool* pool, int batch, int q_heads,
                                                 int q_len, int max_blocks, int window,
                                                 int kv_split_tokens, size_t* bytes);
+
+/*
+ * paged_shared_prefix_attention -- paged_attention_multi_query of a batch whose
+ * sequences share leading cache blocks (samples of one prompt, requests behind
+ * one system prompt: the shared blocks of kv_bm_fork and kv_bm_match_prefix),
+ * the shared part computed once for all members of a group: its K/V blocks are
+ * read once, against the query rows of all members together, and the result is
+ * merged by log-sum-exp with each member's attention over its own blocks
+ * (learn.mohebi.ai lesson 12, section 6).  Same result up to rounding.
+ *   The batch is ordered by group: group g is the sequences group_offsets[g] ..
+ *   group_offsets[g + 1] - 1, and the first group_blocks[g] entries of their block
+ *   tables are the same blocks, all of whose slots are cached (the entries of the
+ *   group's first sequence are the ones read).  kv_bm_prefix_groups makes both
+ *   arrays.  group_offsets: int32 [n_groups + 1], not decreasing, in [0, batch];
+ *   group_blocks: int32 [n_groups], in [0, max_blocks].  Sequences outside every
+ *   group, groups of one, and groups with 0 shared blocks share nothing; a
+ *   context may end inside its group's shared blocks (0 included).  Offsets that
+ *   break the rule (KV_DEVERR_GROUP): nothing is shared; a block count that
+ *   does (KV_DEVERR_GROUP): that group shares nothing.  The results are right
+ *   either way.
+ *   n_groups == 0 is allowed (nothing is shared; the arrays may be NULL).
+ *   kv_split_tokens: the chunk of the members' own parts, which begin behind
+ *   the shared blocks.  workspace: at least paged_shared_prefix_workspace_size()
+ *   bytes, zero-filled before its first use; calls that share one must not
+ *   overlap.  Everything else as in paged_attention_multi_query.  Two kernel
+ *   launches (one when n_groups is 0 or the batch is 1).
+ */
+kv_status paged_shared_prefix_attention(const kv_pool* pool, const void* q, int q_heads, int q_len,
+                                        const int32_t* block_tables, int max_blocks,
+                                        const int32_t* context_lens, int batch,
+                                        const int32_t* group_offsets, const int32_t* group_blocks,
+                                        int n_groups, float scale, int kv_split_tokens,
+                                        void* workspace, size_t workspace_bytes, void* out,
+                                        float* lse_out, void* stream);
+
+/* Workspace bytes of paged_shared_prefix_attention for these sizes. */
+kv_status paged_shared_prefix_workspace_size(const kv_pool* pool, int batch, int q_heads, int q_len,
+                                             int max_blocks, int n_groups, int kv_split_tokens,
+                                             size_t* bytes);
 
 /*
  * paged_decode_step -- one decode step of every sequence of the batch: the

@@ -22,12 +22,14 @@ __all__ = [
     "paged_merge_attention_states",
     "paged_attention_multi_query",
     "paged_decode_step",
+    "paged_shared_prefix_attention", "paged_shared_prefix_workspace_size",
     "paged_attention_masked", "paged_attention_masked_workspace_size",
     "paged_multi_query_workspace_size", "library_path", "load_library", "BlockManager",
     "kv_copy_blocks", "BM_FIFO", "BM_LIFO", "BM_PREFIX_CACHING", "kv_mla_pool_create",
     "paged_mla_decode_plan", "paged_mla_workspace_size", "paged_mla_decode_attention",
     "paged_mla_decode_step",
     "DEVERR_BLOCK_ID", "DEVERR_CONTEXT", "DEVERR_SEQ", "DEVERR_POSITION", "DEVERR_TIMEOUT",
+    "DEVERR_GROUP",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -45,6 +47,7 @@ DEVERR_CONTEXT = 0x2
 DEVERR_SEQ = 0x4
 DEVERR_POSITION = 0x8
 DEVERR_TIMEOUT = 0x10
+DEVERR_GROUP = 0x20
 _DTYPES = {"bf16": 0, "fp8_e4m3": 1}
 BM_FIFO = 0x0
 BM_LIFO = 0x1
@@ -113,6 +116,9 @@ def load_library():
             "paged_attention_masked": ([P, P, I, I, P, I, P, I, ctypes.c_float,
                                         ctypes.POINTER(_AttentionMask), I, P, S, P, P, P], I),
             "paged_attention_masked_workspace_size": ([P, I, I, I, I, I, I, ctypes.POINTER(S)], I),
+            "paged_shared_prefix_attention": ([P, P, I, I, P, I, P, I, P, P, I, ctypes.c_float, I, P, S,
+                                               P, P, P], I),
+            "paged_shared_prefix_workspace_size": ([P, I, I, I, I, I, I, ctypes.POINTER(S)], I),
             "paged_decode_step": ([P, P, P, P, I, I, P, I, P, I, ctypes.c_float, I, P, S, P, P, P],
                                   I),
             "kv_bm_create": ([I, I, I, ctypes.POINTER(P)], I),
@@ -126,6 +132,7 @@ def load_library():
             "kv_bm_sequence_info": ([P, L, ctypes.POINTER(I), ctypes.POINTER(I)], I),
             "kv_bm_block_refcount": ([P, ctypes.c_int32, ctypes.POINTER(I)], I),
             "kv_bm_build_tables": ([P, P, I, I, P, P], I),
+            "kv_bm_prefix_groups": ([P, P, I, I, P, P, P, ctypes.POINTER(I)], I),
             "kv_copy_blocks": ([P, P, I, P], I),
             "kv_mla_pool_create": ([I, I, I, I, I, ctypes.POINTER(P)], I),
             "paged_mla_decode_plan": ([P, I, I, I, I, ctypes.POINTER(I), ctypes.POINTER(I)], I),
@@ -556,6 +563,47 @@ def paged_attention_masked(pool: Pool, q, block_tables, context_lens, scale: flo
     return out
 
 
+def paged_shared_prefix_workspace_size(pool: Pool, batch: int, q_heads: int, q_len: int, max_blocks: int,
+                                       n_groups: int, kv_split_tokens: int = 0) -> int:
+    lib = load_library()
+    n = ctypes.c_size_t()
+    _check(lib.paged_shared_prefix_workspace_size(pool.handle, int(batch), int(q_heads), int(q_len),
+                                                  int(max_blocks), int(n_groups), int(kv_split_tokens),
+                                                  ctypes.byref(n)),
+           "paged_shared_prefix_workspace_size")
+    return n.value
+
+
+def paged_shared_prefix_attention(pool: Pool, q, block_tables, context_lens, group_offsets, group_blocks,
+                                  scale: float, kv_split_tokens: int = 0, workspace=None, out=None,
+                                  lse=None, stream=None):
+    """Attention of the new tokens of a batch ordered by groups that share leading blocks: group g
+    is the sequences group_offsets[g] .. group_offsets[g + 1] - 1 (int32 [G + 1]) and shares the
+    first group_blocks[g] entries of their tables (int32 [G]); BlockManager.prefix_groups makes
+    both.  q bf16 [B, Hq, d] or [B, Hq, q_len, d].  Returns out (shaped like q)."""
+    lib = load_library()
+    if out is None:
+        out = torch.empty_like(q)
+    batch, heads, q_len = _queries(pool, q, block_tables, context_lens, out, lse)
+    _need(group_offsets, torch.int32, "group_offsets")
+    _need(group_blocks, torch.int32, "group_blocks")
+    n_groups = group_blocks.numel()
+    if group_offsets.numel() != n_groups + 1:
+        raise ValueError("group_offsets must hold one entry more than group_blocks")
+    max_blocks = block_tables.shape[1]
+    if workspace is None:
+        need = paged_shared_prefix_workspace_size(pool, batch, heads, q_len, max_blocks, n_groups, kv_split_tokens)
+        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device) if need else None
+    _need(workspace, torch.uint8, "workspace")
+    _check(lib.paged_shared_prefix_attention(
+        pool.handle, q.data_ptr(), heads, q_len, block_tables.data_ptr(), max_blocks,
+        context_lens.data_ptr(), batch, group_offsets.data_ptr(), group_blocks.data_ptr(), n_groups,
+        float(scale), int(kv_split_tokens), _ptr(workspace),
+        0 if workspace is None else workspace.numel(), out.data_ptr(), _ptr(lse), _stream(stream)),
+        "paged_shared_prefix_attention")
+    return out
+
+
 def paged_decode_step(pool: Pool, k_new, v_new, q, block_tables, context_lens,
                       scale: float, kv_split_tokens: int = 0, workspace=None,
                       out=None, lse=None, stream=None):
@@ -689,6 +737,21 @@ class BlockManager:
                                             int(max_blocks), tables.data_ptr(), lens.data_ptr()),
                "kv_bm_build_tables")
         return tables, lens
+
+    def prefix_groups(self, seqs, min_blocks: int = 1):
+        """(order, group_offsets, group_blocks): host int32 tensors that sort the sequences by the
+        blocks they share at their start, for paged_shared_prefix_attention."""
+        batch = len(seqs)
+        ids = (ctypes.c_int64 * max(batch, 1))(*[int(s) for s in seqs])
+        order = torch.empty(batch, dtype=torch.int32)
+        offsets = torch.zeros(batch + 1, dtype=torch.int32)
+        blocks = torch.empty(max(batch, 1), dtype=torch.int32)
+        n = ctypes.c_int()
+        _check(self._lib.kv_bm_prefix_groups(self._h, ctypes.cast(ids, ctypes.c_void_p), batch,
+                                             int(min_blocks), order.data_ptr(), offsets.data_ptr(),
+                                             blocks.data_ptr(), ctypes.byref(n)),
+               "kv_bm_prefix_groups")
+        return order, offsets[:n.value + 1].clone(), blocks[:n.value].clone()
 
     def block_table(self, seq: int):
         """The sequence's block ids, in order."""

@@ -35,6 +35,7 @@ struct kv_pool {
                             // per box (the wide tcgen05 decode)
     CUtensorMap tmh;        // latent pools with blocks of 64: one 128-byte piece of 32 slots
                             // per box (the narrow tcgen05 decode)
+    CUtensorMap tmpk, tmpv; // K and V pools in octets of slots (the shared prefix pass)
     int has_tc;
     int num_sms;
     int mla;                // 1: latent pool (one cached vector per token, no V half)
@@ -113,6 +114,31 @@ kv_status encode_pool_map(const kv_pool* p, uint8_t* base, CUtensorMap* map, int
                                                                           : row / 128), 1,
                                static_cast<cuuint32_t>(slots_per_box > 0 ? slots_per_box
                                                                          : p->block_size), 1};
+    const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
+    const CUtensorMapDataType dt = p->dtype == KV_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                             : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    CUresult r = fn(map, dt, 5, base, dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? KV_OK : KV_ERR_CUDA;
+}
+
+// Tile map of one pool half for the shared prefix pass: dims (innermost first) = 128-byte row
+// piece, slot of an octet, pieces per token row, octet of slots (of all blocks), kv head; a box
+// is one block of one kv head, written as octets of [piece][8 slots][128 bytes] with the 128-byte
+// swizzle -- 8-row groups of the tensor cores' operand layout one after another.
+kv_status encode_octet_map(const kv_pool* p, uint8_t* base, CUtensorMap* map)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return KV_ERR_CUDA;
+    const cuuint64_t row = static_cast<cuuint64_t>(p->head_dim) * p->elem;
+    const cuuint64_t token = row * p->kv_heads;
+    const cuuint64_t dims[5] = {128 / p->elem, 8, row / 128,
+                                static_cast<cuuint64_t>(p->num_blocks) * (p->block_size / 8),
+                                static_cast<cuuint64_t>(p->kv_heads)};
+    const cuuint64_t strides[4] = {token, 128, 8 * token, row};
+    const cuuint32_t box[5] = {static_cast<cuuint32_t>(128 / p->elem), 8, static_cast<cuuint32_t>(row / 128),
+                               static_cast<cuuint32_t>(p->block_size / 8), 1};
     const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
     const CUtensorMapDataType dt = p->dtype == KV_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                              : CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -286,6 +312,26 @@ size_t workspace_bytes_for(const kv_pool* pl, int batch, const Plan& p)
     return workspace_layout(pl, batch, p).total;
 }
 
+// The shared prefix pass's part of a workspace (behind the plan's own, on a kAlign boundary):
+// run entries, (max, sum) pairs, partial outputs.  Pieces: one per run and one per range border
+// of the grid (one CTA per SM).
+struct PrefixLayout {
+    size_t runs, piece_ml, piece_o, total;
+    long long pieces;
+};
+
+PrefixLayout prefix_layout(const kv_pool* pl, int batch, const Plan& p, int n_groups)
+{
+    PrefixLayout w{0, 0, 0, 0, 0};
+    if (n_groups == 0 || batch < 2) return w;
+    const long long runs = kvp::prefix_run_slots(batch, pl->kv_heads, p.rows, n_groups);
+    w.pieces = runs + pl->num_sms;
+    w.piece_ml = round_up(static_cast<size_t>(runs) * sizeof(int2), kAlign);
+    w.piece_o = w.piece_ml + round_up(static_cast<size_t>(w.pieces) * 256 * sizeof(float2), kAlign);
+    w.total = w.piece_o + static_cast<size_t>(w.pieces) * 256 * pl->head_dim * sizeof(float);
+    return w;
+}
+
 kv_status check_device(const kv_pool* pl)
 {
     int dev = -1;
@@ -378,6 +424,8 @@ kv_status kv_pool_create(int num_blocks, int block_size, int kv_heads, int head_
         st = KV_ERR_CUDA;
     if (st == KV_OK) st = encode_pool_map(p, p->k, &p->tmk);
     if (st == KV_OK) st = encode_pool_map(p, p->v, &p->tmv);
+    if (st == KV_OK) st = encode_octet_map(p, p->k, &p->tmpk);
+    if (st == KV_OK) st = encode_octet_map(p, p->v, &p->tmpv);
     if (st == KV_OK) {
         const bool fp8 = dtype == KV_DTYPE_FP8_E4M3;
         for (int nt : {8, 16}) {
@@ -389,6 +437,7 @@ kv_status kv_pool_create(int num_blocks, int block_size, int kv_heads, int head_
             if (e != cudaSuccess) st = KV_ERR_CUDA;
         }
         if (kvp::prepare_decode_heads(fp8, head_dim, block_size) != cudaSuccess) st = KV_ERR_CUDA;
+        if (kvp::prepare_prefix(fp8, head_dim, block_size) != cudaSuccess) st = KV_ERR_CUDA;
     }
     if (st == KV_OK && cudaDeviceSynchronize() != cudaSuccess) st = KV_ERR_CUDA;
     if (st != KV_OK) {
@@ -756,10 +805,11 @@ kv_status launch_decode(const kv_pool* pool, const Plan& plan, dim3 grid, const 
     return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }
 
-kv_status launch_span(const kv_pool* pool, const Plan& plan, dim3 grid, const kvp::SpanParams& p, void* stream)
+kv_status launch_span(const kv_pool* pool, const Plan& plan, dim3 grid, kvp::SpanRule rule, const kvp::SpanParams& p,
+                      void* stream)
 {
     const auto launch = pool->dtype == KV_DTYPE_BF16 ? kvp::launch_span_bf16 : kvp::launch_span_fp8;
-    return launch(pool->head_dim, pool->block_size, plan.head_tile, grid, pool->tmk, pool->tmv, p,
+    return launch(rule, pool->head_dim, pool->block_size, plan.head_tile, grid, pool->tmk, pool->tmv, p,
                   static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? KV_OK
                : KV_ERR_CUDA;
@@ -825,7 +875,76 @@ kv_status paged_attention_masked(const kv_pool* pool, const void* q, int q_heads
     p.slopes = m.alibi_slopes;
     p.first_keys = m.first_keys;
     p.prefix_lens = m.prefix_lens;
-    return launch_span(pool, plan, grid, p, stream);
+    p.shared = {};
+    const int rule = (m.softcap > 0.f ? kvp::SPAN_CAP : 0) | (m.alibi_slopes != nullptr ? kvp::SPAN_BIAS : 0);
+    return launch_span(pool, plan, grid, static_cast<kvp::SpanRule>(rule), p, stream);
+}
+
+kv_status paged_shared_prefix_workspace_size(const kv_pool* pool, int batch, int q_heads, int q_len,
+                                             int max_blocks, int n_groups, int kv_split_tokens,
+                                             size_t* bytes)
+{
+    if (bytes == nullptr || n_groups < 0) return KV_ERR_INVALID_ARG;
+    Plan p;
+    kv_status st = make_span_plan(pool, batch, q_heads, q_len, max_blocks, max_blocks, kv_split_tokens, &p);
+    if (st != KV_OK) return st;
+    if (pool->mla) return KV_ERR_INVALID_ARG;
+    const PrefixLayout l = prefix_layout(pool, batch, p, n_groups);
+    if (l.pieces > (1 << 30)) return KV_ERR_UNSUPPORTED;
+    const size_t own = workspace_bytes_for(pool, batch, p);
+    *bytes = l.total > 0 ? round_up(own, kAlign) + l.total : own;
+    return KV_OK;
+}
+
+kv_status paged_shared_prefix_attention(const kv_pool* pool, const void* q, int q_heads, int q_len,
+                                        const int32_t* block_tables, int max_blocks,
+                                        const int32_t* context_lens, int batch,
+                                        const int32_t* group_offsets, const int32_t* group_blocks,
+                                        int n_groups, float scale, int kv_split_tokens,
+                                        void* workspace, size_t workspace_bytes, void* out,
+                                        float* lse_out, void* stream)
+{
+    if (n_groups < 0 || (n_groups > 0 && (group_offsets == nullptr || group_blocks == nullptr)) ||
+        !aligned(group_offsets, 4) || !aligned(group_blocks, 4))
+        return KV_ERR_INVALID_ARG;
+    Plan plan;
+    kv_status st = make_span_plan(pool, batch, q_heads, q_len, max_blocks, max_blocks, kv_split_tokens, &plan);
+    if (st != KV_OK) return st;
+    if (pool->mla) return KV_ERR_INVALID_ARG;
+    const PrefixLayout l = prefix_layout(pool, batch, plan, n_groups);
+    if (l.pieces > (1 << 30)) return KV_ERR_UNSUPPORTED;
+    kvp::SpanParams p = {};
+    dim3 grid;
+    st = fill_decode_launch(pool, plan, q, q_heads, q_len, block_tables, max_blocks, context_lens, batch, scale,
+                            workspace, workspace_bytes, l.total, out, lse_out, &p.d, &grid);
+    if (st != KV_OK || batch == 0) return st;
+    if (l.total == 0) return launch_span(pool, plan, grid, kvp::SPAN_MASK, p, stream);   // nobody to share with
+    kvp::PrefixParams& s = p.shared;
+    uint8_t* ws = static_cast<uint8_t*>(workspace) + round_up(workspace_bytes_for(pool, batch, plan), kAlign);
+    s.q = p.d.q;
+    s.tables = block_tables;
+    s.ctx = context_lens;
+    s.group_offsets = group_offsets;
+    s.group_blocks = group_blocks;
+    s.k_scale = pool->k_scale;
+    s.v_scale = pool->v_scale;
+    s.runs = reinterpret_cast<int2*>(ws + l.runs);
+    s.piece_ml = reinterpret_cast<float2*>(ws + l.piece_ml);
+    s.piece_o = reinterpret_cast<float*>(ws + l.piece_o);
+    s.err = pool->err;
+    s.batch = batch;
+    s.kv_heads = pool->kv_heads;
+    s.q_len = q_len;
+    s.rows = plan.rows;
+    s.max_blocks = max_blocks;
+    s.num_blocks = pool->num_blocks;
+    s.n_groups = n_groups;
+    s.pieces = static_cast<int>(l.pieces);
+    s.scale_log2 = p.d.scale_log2;
+    if (kvp::launch_prefix(pool->dtype == KV_DTYPE_FP8_E4M3, pool->head_dim, pool->block_size, pool->num_sms, pool->tmpk,
+                           pool->tmpv, s, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return KV_ERR_CUDA;
+    return launch_span(pool, plan, grid, kvp::SPAN_SUFFIX, p, stream);
 }
 
 kv_status paged_decode_step(kv_pool* pool, const void* k_new, const void* v_new, const void* q,

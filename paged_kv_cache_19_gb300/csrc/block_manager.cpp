@@ -361,4 +361,59 @@ kv_status kv_bm_build_tables(const kv_block_manager* bm, const int64_t* seqs, in
     return KV_OK;
 }
 
+kv_status kv_bm_prefix_groups(const kv_block_manager* bm, const int64_t* seqs, int batch,
+                              int min_blocks, int32_t* order, int32_t* group_offsets,
+                              int32_t* group_blocks, int* n_groups)
+{
+    if (bm == nullptr || batch < 0 || min_blocks < 1 || n_groups == nullptr || group_offsets == nullptr ||
+        (batch > 0 && (seqs == nullptr || order == nullptr || group_blocks == nullptr)))
+        return KV_ERR_INVALID_ARG;
+    std::lock_guard<std::mutex> lock(bm->mu);
+    try {
+        std::vector<const Seq*> of(batch);
+        for (int i = 0; i < batch; ++i) {
+            auto it = bm->seqs.find(seqs[i]);
+            if (it == bm->seqs.end()) return KV_ERR_INVALID_ARG;
+            of[i] = &it->second;
+        }
+        // A block is held at one place of a table only by sequences whose starts are the same
+        // blocks up to it, so the block at entry min_blocks - 1 names the group; what the
+        // members have in common is compared all the same.
+        std::unordered_map<int32_t, int> group_of;
+        std::vector<std::vector<int32_t>> members;
+        for (int i = 0; i < batch; ++i) {
+            const int64_t filled = of[i]->len / bm->block_size;
+            if (filled >= min_blocks) {
+                const auto at = group_of.emplace(of[i]->blocks[min_blocks - 1], static_cast<int>(members.size()));
+                if (!at.second) {
+                    members[at.first->second].push_back(i);
+                    continue;
+                }
+            }
+            members.push_back({i});
+        }
+        int n = 0;
+        for (size_t g = 0; g < members.size(); ++g) {
+            const Seq& first = *of[members[g][0]];
+            int64_t common = members[g].size() < 2 ? 0 : first.len / bm->block_size;
+            group_offsets[g] = n;
+            for (int32_t i : members[g]) {
+                const Seq& s = *of[i];
+                const int64_t filled = s.len / bm->block_size;
+                if (common > filled) common = filled;
+                int64_t same = 0;
+                while (same < common && s.blocks[same] == first.blocks[same]) ++same;
+                common = same;
+                order[n++] = i;
+            }
+            group_blocks[g] = static_cast<int32_t>(common);
+        }
+        group_offsets[members.size()] = n;
+        *n_groups = static_cast<int>(members.size());
+    } catch (...) {
+        return KV_ERR_OUT_OF_MEMORY;
+    }
+    return KV_OK;
+}
+
 }  // extern "C"

@@ -13,12 +13,17 @@
 // sees -- chunk j covers blocks [first + j S, first + (j + 1) S) -- and the rule of a row
 // (SpanRows) is applied to the raw scores before the softmax.
 //
+// The suffix form (SPAN_SUFFIX, paged_shared_prefix_attention) starts a sequence's keys behind
+// the blocks that its group shares and takes the pieces that the shared pass left for its rows
+// (prefix_groups.cuh) as further chunks of the merge.
+//
 // It stays bound by the K/V bytes of the visible blocks.  The cap costs one ex2 and one
 // reciprocal per score (capped_tanh), the bias one add and one multiply; both are template
 // flags, so a plain mask pays for neither.
 #pragma once
 
 #include "decode_common.cuh"
+#include "prefix_groups.cuh"
 
 namespace kvp {
 
@@ -35,8 +40,10 @@ __device__ __forceinline__ float capped_tanh(float y)
 }
 
 // The rule of the rows of a thread's accumulator columns, positions absolute.
-template <int NTT, bool CAP, bool BIAS>
+template <int NTT, int RULE>
 struct SpanRows {
+    static constexpr bool CAP = RULE == SPAN_CAP || RULE == SPAN_CAP_BIAS;
+    static constexpr bool BIAS = RULE == SPAN_BIAS || RULE == SPAN_CAP_BIAS;
     int lo[NTT][2], hi[NTT][2];       // keys [lo, hi)
     float slope[NTT][2];              // log2 units per token of distance
     int pos[NTT][2];
@@ -55,15 +62,67 @@ struct SpanRows {
     __device__ __forceinline__ int value_hi() const { return tile_hi - base; }
 };
 
+// The pieces of a shared pass that hold query row `r` (of the `rows` of a kv head) of a sequence:
+// entry e has its (max, sum) at ml(e) and its normalised output numbers d0 .. d0 + 3 at o(e, d0).
+template <int D>
+struct RowPieces {
+    const float2* ml0;
+    const float* o0;
+    int n = 0;
+    bool both = false;                // the two slots of a piece hold the same rows
+    __device__ __forceinline__ void find(const PrefixParams& p, int g, int b, int kvh, int r)
+    {
+        const PrefixGroup gr = load_prefix_group(p, g);
+        const int grow = (b - gr.off) * p.rows + r;
+        const int pair = grow / PFX_PAIR, at = grow - pair * PFX_PAIR;
+        const int pairs = prefix_pairs(p, gr);
+        const int2 run = __ldcg(p.runs + prefix_run_base(p, g, gr) + kvh * pairs + pair);
+        // (a shared pass that gave up may have left this run's entry unwritten)
+        if (run.x < 0 || run.y < 0 || run.x > p.pieces - run.y) return;
+        both = gr.n * p.rows - pair * PFX_PAIR <= PFX_TILE;
+        const size_t slot = static_cast<size_t>(run.x) * 2 + at / PFX_TILE;
+        ml0 = p.piece_ml + slot * PFX_TILE + at % PFX_TILE;
+        o0 = p.piece_o + slot * (PFX_TILE * D) + at % PFX_TILE * 4;
+        n = both ? 2 * run.y : run.y;
+    }
+    __device__ __forceinline__ size_t slot(int e) const { return both ? e : 2 * e; }
+    __device__ __forceinline__ float2 ml(int e) const { return __ldcg(ml0 + slot(e) * PFX_TILE); }
+    __device__ __forceinline__ float4 o(int e, int d0) const
+    {
+        return __ldcg(reinterpret_cast<const float4*>(o0 + slot(e) * (PFX_TILE * D) + d0 * PFX_TILE));
+    }
+};
+
+// Adds the pieces of a row to acc (numbers d0 ..) and the weight W, against the maximum M.
+template <class C, int D>
+__device__ __forceinline__ void add_pieces(const RowPieces<D>& pc, int d0, float M, float (&acc)[C::E], float& W)
+{
+#pragma unroll 4
+    for (int e = 0; e < pc.n; ++e) {
+        const float2 v = pc.ml(e);
+        if (!(v.y > 0.f)) continue;                  // a piece this row sees nothing of
+        const float w = v.y * fast_exp2(v.x - M);
+        W += w;
+#pragma unroll
+        for (int k = 0; k < C::E; k += 4) {
+            const float4 x = pc.o(e, d0 + k);
+            acc[k] += w * x.x;
+            acc[k + 1] += w * x.y;
+            acc[k + 2] += w * x.z;
+            acc[k + 3] += w * x.w;
+        }
+    }
+}
+
 template <bool FP8, int D, int BS, int NT>
 struct SpanCfg : DecodeCfg<FP8, D, BS, NT> {
     using C = DecodeCfg<FP8, D, BS, NT>;
-    static constexpr int SMEM = 1024 + C::NSTAGE * C::STAGE + C::NSTAGE * (8 + 8 + 4) + 16;
+    static constexpr int SMEM = 1024 + C::NSTAGE * C::STAGE + C::NSTAGE * (8 + 8 + 4) + 16;   // ring, barriers, ids, flags
     static constexpr int MINB = NT == 8 ? 3 : 2;    // CTAs per SM: 16-row tiles keep twice the state
     static_assert(C::RED_BYTES <= C::NSTAGE * C::STAGE, "epilogue buffer reuses the stages");
 };
 
-template <bool FP8, int D, int BS, int NT, bool CAP, bool BIAS>
+template <bool FP8, int D, int BS, int NT, int RULE>
 __global__ void __launch_bounds__(DecodeCfg<FP8, D, BS, NT>::THREADS, SpanCfg<FP8, D, BS, NT>::MINB)
 paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                   const SpanParams sp)
@@ -77,6 +136,8 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     uint64_t* empty = full + C::NSTAGE;
     int* stage_blk = reinterpret_cast<int*>(empty + C::NSTAGE);
     int* merge_flag = stage_blk + C::NSTAGE;
+    int* group_slot = merge_flag + 1;                  // the suffix form: the sequence's group
+    constexpr bool SUFFIX = RULE == SPAN_SUFFIX;
 
     const int b = blockIdx.y;
     const int kvh = blockIdx.x / p.head_groups;
@@ -93,12 +154,29 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             mbar_init(smem_u32(empty + i), 1);
         }
         fence_mbar_init();
+        if constexpr (SUFFIX) *group_slot = -1;
     }
     grid_dependency_wait();                          // inputs of the preceding kernel are ready
 
     int ctx = __ldg(p.ctx + b);
-    const int first = sp.first_keys != nullptr ? max(0, __ldg(sp.first_keys + b)) : 0;
-    const int prefix = sp.prefix_lens != nullptr ? __ldg(sp.prefix_lens + b) : 0;
+    int first = 0, prefix = 0;
+    int group = -1;                                  // the sequence's group, if it shares blocks
+    if constexpr (SUFFIX) {
+        __syncthreads();
+        bool ok = true;
+        for (int g = threadIdx.x; g < sp.shared.n_groups; g += C::THREADS) {
+            ok = ok && prefix_offsets_ok(sp.shared, g);
+            if (__ldg(sp.shared.group_offsets + g) <= b && b < __ldg(sp.shared.group_offsets + g + 1)) *group_slot = g;
+        }
+        if (__syncthreads_and(ok)) group = *group_slot;   // bad offsets: nothing is shared
+        if (group >= 0) {
+            first = load_prefix_group(sp.shared, group).blocks * BS;
+            if (first == 0) group = -1;
+        }
+    } else {
+        if (sp.first_keys != nullptr) first = max(0, __ldg(sp.first_keys + b));
+        if (sp.prefix_lens != nullptr) prefix = __ldg(sp.prefix_lens + b);
+    }
     uint32_t qf[C::KS][C::NTT][2];
     float sl2 = 0.f;
     if (warp < C::NCW)
@@ -114,7 +192,7 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     const int visible = min(prefix, ctx);
     const auto key_lo = [&](int i) {
         const int pos = ctx - p.q_len + i;
-        return sp.window > 0 ? max(first, pos - sp.window + 1) : first;
+        return !SUFFIX && sp.window > 0 ? max(first, pos - sp.window + 1) : first;
     };
     const auto key_hi = [&](int i) { return max(ctx - p.q_len + i + 1, visible); };
     // tokens of the tile's rows: a run, or all of them where the tile spans two heads
@@ -203,7 +281,7 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     }
 
     // ------------------------------------------------------------ consumer warps
-    SpanRows<C::NTT, CAP, BIAS> rows;
+    SpanRows<C::NTT, RULE> rows;
     rows.sl2 = sl2;
     rows.cap_in = sp.cap_in;
     rows.cap_log2 = sp.cap_log2;
@@ -219,7 +297,7 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             rows.lo[nt][j] = key_lo(i);
             rows.hi[nt][j] = local < nh ? key_hi(i) : 0;      // padding rows see nothing
             rows.pos[nt][j] = ctx - p.q_len + i;
-            rows.slope[nt][j] = BIAS && local < nh
+            rows.slope[nt][j] = rows.BIAS && local < nh
                                     ? __ldg(sp.slopes + kvh * p.group + head) * 1.4426950408889634f
                                     : 0.f;
         }
@@ -260,6 +338,26 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         float acc[C::E], M, L;
         combine_warps<C>(red, head, d0, FP8 ? __ldg(p.v_scale + kvh) : 1.f, acc, M, L);
         if (nsplit == 1) {
+            if constexpr (SUFFIX) {
+                RowPieces<D> pc;
+                if (group >= 0) pc.find(sp.shared, group, b, kvh, hg * NT + head);
+                if (pc.n > 0) {
+                    float top = L > 0.f ? M : -INFINITY;
+                    for (int e = 0; e < pc.n; ++e) {
+                        const float2 v = pc.ml(e);
+                        if (v.y > 0.f) top = fmaxf(top, v.x);
+                    }
+                    float W = L > 0.f ? L * fast_exp2(M - top) : 0.f;
+#pragma unroll
+                    for (int e = 0; e < C::E; ++e) acc[e] *= W;
+                    add_pieces<C, D>(pc, d0, top, acc, W);
+                    const float inv = W > 0.f ? 1.f / W : 0.f;
+#pragma unroll
+                    for (int e = 0; e < C::E; ++e) acc[e] *= inv;
+                    M = top;
+                    L = W;
+                }
+            }
             uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + bh * D + d0);
 #pragma unroll
             for (int e = 0; e < C::E; e += 2) dst[e / 2] = pack_bf16x2(acc[e], acc[e + 1]);
@@ -290,6 +388,14 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     if (head < nh) {
         const float* ml = p.part_ml + bh * p.max_splits * 2;
         float M = -INFINITY;
+        RowPieces<D> pc;
+        if constexpr (SUFFIX) {
+            if (group >= 0) pc.find(sp.shared, group, b, kvh, hg * NT + head);
+            for (int e = 0; e < pc.n; ++e) {
+                const float2 v = pc.ml(e);
+                if (v.y > 0.f) M = fmaxf(M, v.x);
+            }
+        }
         for (int j = 0; j < nsplit; ++j) {
             if (__ldcg(ml + 2 * j + 1) > 0.f) M = fmaxf(M, __ldcg(ml + 2 * j));
         }
@@ -313,6 +419,7 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 acc[e + 3] += wj * v.w;
             }
         }
+        if constexpr (SUFFIX) add_pieces<C, D>(pc, d0, M, acc, W);
         const float inv = W > 0.f ? 1.f / W : 0.f;
         uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + bh * D + d0);
 #pragma unroll
@@ -329,26 +436,30 @@ cudaError_t prepare_span_variant()
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     SpanCfg<FP8, D, BS, NT>::SMEM);
     };
-    cudaError_t e = raise(paged_decode_span<FP8, D, BS, NT, false, false>);
-    if (e == cudaSuccess) e = raise(paged_decode_span<FP8, D, BS, NT, true, false>);
-    if (e == cudaSuccess) e = raise(paged_decode_span<FP8, D, BS, NT, false, true>);
-    if (e == cudaSuccess) e = raise(paged_decode_span<FP8, D, BS, NT, true, true>);
+    cudaError_t e = raise(paged_decode_span<FP8, D, BS, NT, SPAN_MASK>);
+    if (e == cudaSuccess) e = raise(paged_decode_span<FP8, D, BS, NT, SPAN_CAP>);
+    if (e == cudaSuccess) e = raise(paged_decode_span<FP8, D, BS, NT, SPAN_BIAS>);
+    if (e == cudaSuccess) e = raise(paged_decode_span<FP8, D, BS, NT, SPAN_CAP_BIAS>);
+    if (e == cudaSuccess) e = raise(paged_decode_span<FP8, D, BS, NT, SPAN_SUFFIX>);
     return e;
 }
 
 template <bool FP8, int D, int BS, int NT>
-cudaError_t launch_span_variant(dim3 grid, const CUtensorMap& tk, const CUtensorMap& tv,
+cudaError_t launch_span_variant(SpanRule rule, dim3 grid, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const SpanParams& p, cudaStream_t s)
 {
-    const bool capped = p.cap_log2 > 0.f, biased = p.slopes != nullptr;
     const auto go = [&](auto kernel) {
         return launch_dependent(kernel, grid, dim3(DecodeCfg<FP8, D, BS, NT>::THREADS),
                                 SpanCfg<FP8, D, BS, NT>::SMEM, s, tk, tv, p);
     };
-    if (capped && biased) return go(paged_decode_span<FP8, D, BS, NT, true, true>);
-    if (capped) return go(paged_decode_span<FP8, D, BS, NT, true, false>);
-    if (biased) return go(paged_decode_span<FP8, D, BS, NT, false, true>);
-    return go(paged_decode_span<FP8, D, BS, NT, false, false>);
+    switch (rule) {
+    case SPAN_MASK: return go(paged_decode_span<FP8, D, BS, NT, SPAN_MASK>);
+    case SPAN_CAP: return go(paged_decode_span<FP8, D, BS, NT, SPAN_CAP>);
+    case SPAN_BIAS: return go(paged_decode_span<FP8, D, BS, NT, SPAN_BIAS>);
+    case SPAN_CAP_BIAS: return go(paged_decode_span<FP8, D, BS, NT, SPAN_CAP_BIAS>);
+    case SPAN_SUFFIX: return go(paged_decode_span<FP8, D, BS, NT, SPAN_SUFFIX>);
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace kvp

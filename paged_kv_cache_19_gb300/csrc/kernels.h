@@ -53,6 +53,34 @@ struct DecodeParams {
     unsigned long long consumer_wait_ns;
 };
 
+// The shared pass of paged_shared_prefix_attention (prefix_groups.cuh, decode_prefix.cu).
+struct PrefixParams {
+    const uint16_t* q;        // bf16 [batch, q_heads, q_len, head_dim]
+    const int32_t* tables;    // [batch, max_blocks]
+    const int32_t* ctx;       // [batch]
+    const int32_t* group_offsets;   // [n_groups + 1]
+    const int32_t* group_blocks;    // [n_groups]
+    const float* k_scale;     // [kv_heads] (fp8 cache)
+    const float* v_scale;
+    int2* runs;               // per run slot: first piece, pieces
+    float2* piece_ml;         // [piece][2][128] (max, sum), log2 units
+    float* piece_o;           // [piece][2][head_dim / 4][128][4], normalised
+    uint32_t* err;
+    int batch, kv_heads, q_len, rows, max_blocks, num_blocks, n_groups;
+    int pieces;               // pieces the workspace holds
+    float scale_log2;
+};
+// Run slots and pieces the shared pass can use, for a grid of `ctas` (its workspace).
+inline long long prefix_run_slots(int batch, int kv_heads, int rows, int n_groups)
+{
+    const long long by_rows = static_cast<long long>(batch) * rows / 256;
+    const long long sharing = n_groups < batch / 2 ? n_groups : batch / 2;
+    return kv_heads * (by_rows + sharing + 1);
+}
+cudaError_t prepare_prefix(bool fp8, int head_dim, int block_size);
+cudaError_t launch_prefix(bool fp8, int head_dim, int block_size, int ctas, const CUtensorMap& tk,
+                          const CUtensorMap& tv, const PrefixParams& p, cudaStream_t s);
+
 // Attention over a span of each sequence's keys (decode_span.cuh): the decode's parameters and
 // the rule of the rows.
 struct SpanParams {
@@ -62,7 +90,10 @@ struct SpanParams {
     const float* slopes;      // [q_heads] distance bias or null
     const int32_t* first_keys;   // [batch] or null
     const int32_t* prefix_lens;  // [batch] or null
+    PrefixParams shared;      // the form behind a shared pass: its groups and partial results
 };
+// The rule of the rows: a template argument of the span kernel.
+enum SpanRule { SPAN_MASK = 0, SPAN_CAP = 1, SPAN_BIAS = 2, SPAN_CAP_BIAS = 3, SPAN_SUFFIX = 4 };
 
 struct AppendParams {
     const uint16_t* k_new;    // bf16 [num_tokens, kv_heads, head_dim]
@@ -183,10 +214,10 @@ cudaError_t launch_decode_fp8(int head_dim, int block_size, int head_tile, dim3 
                               const DecodeParams& p, cudaStream_t s);
 cudaError_t prepare_span_bf16(int head_dim, int block_size, int head_tile);
 cudaError_t prepare_span_fp8(int head_dim, int block_size, int head_tile);
-cudaError_t launch_span_bf16(int head_dim, int block_size, int head_tile, dim3 grid,
+cudaError_t launch_span_bf16(SpanRule rule, int head_dim, int block_size, int head_tile, dim3 grid,
                              const CUtensorMap& tk, const CUtensorMap& tv, const SpanParams& p,
                              cudaStream_t s);
-cudaError_t launch_span_fp8(int head_dim, int block_size, int head_tile, dim3 grid,
+cudaError_t launch_span_fp8(SpanRule rule, int head_dim, int block_size, int head_tile, dim3 grid,
                             const CUtensorMap& tk, const CUtensorMap& tv, const SpanParams& p,
                             cudaStream_t s);
 // The decode kernel with one CTA per group of `heads` kv heads (decode_heads.cuh), `ctas`

@@ -1,0 +1,60 @@
+// prefix_groups.cuh -- the groups of sequences that share leading cache blocks, as the two
+// kernels of paged_shared_prefix_attention see them: which group a sequence is in, the work
+// units of the shared pass, and where its partial results lie.
+//
+// Group g holds the sequences [off_g, off_g+1) and shares the first blocks_g blocks of each.  Its
+// query rows for one kv head are the members' rows one after another (member m's row r is group
+// row m * rows + r); they are cut into pairs of 128-row tiles (256 rows).  A run is one
+// (group, kv head, pair), its units the 128-token tiles of the prefix, in the order
+// (group, kv head, pair, tile); CTA c of G takes the units [U c / G, U (c+1) / G).
+#pragma once
+
+#include "device_common.cuh"
+#include "kernels.h"
+
+namespace kvp {
+
+constexpr int PFX_TILE = 128;              // tokens of a unit, rows of a row tile
+constexpr int PFX_PAIR = 2 * PFX_TILE;     // rows of a run
+
+struct PrefixGroup {
+    int off, n;                            // members
+    int blocks;                            // shared blocks; 0: computed without sharing
+};
+
+// Group g, its block count checked; a single sequence has nobody to share with.
+__device__ __forceinline__ PrefixGroup load_prefix_group(const PrefixParams& p, int g)
+{
+    PrefixGroup gr;
+    gr.off = __ldg(p.group_offsets + g);
+    gr.n = __ldg(p.group_offsets + g + 1) - gr.off;
+    const int blocks = __ldg(p.group_blocks + g);
+    gr.blocks = gr.n >= 2 && blocks > 0 && blocks <= p.max_blocks ? blocks : 0;
+    return gr;
+}
+
+// Whether the offsets of group g are in order and inside the batch.
+__device__ __forceinline__ bool prefix_offsets_ok(const PrefixParams& p, int g)
+{
+    const int a = __ldg(p.group_offsets + g), b = __ldg(p.group_offsets + g + 1);
+    return 0 <= a && a <= b && b <= p.batch;
+}
+
+__device__ __forceinline__ int prefix_pairs(const PrefixParams& p, const PrefixGroup& gr)
+{
+    return (gr.n * p.rows + PFX_PAIR - 1) / PFX_PAIR;
+}
+
+// Index of a sharing group's first run among all runs, with gaps: it grows by at least the
+// group's pairs from one sharing group to the next (two members or more each), so no sum over
+// the groups is needed to find it.  Less than prefix_run_slots().
+__device__ __forceinline__ int prefix_run_base(const PrefixParams& p, int g, const PrefixGroup& gr)
+{
+    return p.kv_heads * (gr.off * p.rows / PFX_PAIR + min(gr.off / 2, g));
+}
+
+// Numbers of a piece: [2 slots][D / 4][128 rows][4] fp32 outputs, [2 slots][128 rows] (max, sum).
+// A run of more than 128 rows has row tile s in slot s; one of fewer has the same rows in both
+// slots, each over every other token tile.
+
+}  // namespace kvp

@@ -31,6 +31,12 @@ __host__ __device__ constexpr uint32_t tc_idesc_bf16(int m, int n, int a_mn, int
            (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+// The same with f16 A and B.
+__host__ __device__ constexpr uint32_t tc_idesc_f16(int m, int n, int a_mn, int b_mn)
+{
+    return tc_idesc_bf16(m, n, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+
 // Warp-wide: allocate `ncols` tensor-memory columns, address written to smem.
 __device__ __forceinline__ void tc_alloc(uint32_t smem_slot, uint32_t ncols)
 {

@@ -1,0 +1,97 @@
+"""CPU checks of the norm-rotation-append, masked and shared-prefix calls: declared, exported,
+and refused on the host; groups of sequences that share blocks, from the block manager."""
+import ctypes
+import os
+
+import pytest
+
+import paged_kv_cache_19_gb300 as kp
+from paged_kv_cache_19_gb300 import build as cuda_build
+
+HEADERS = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    cuda_build.build()
+    return kp.load_library()
+
+
+def test_declared_exported_and_bound(lib):
+    text = "".join(open(os.path.join(HEADERS, f)).read() for f in os.listdir(HEADERS))
+    for name in ("paged_norm_rope_append", "paged_attention_masked", "paged_attention_masked_workspace_size",
+                 "paged_shared_prefix_attention", "paged_shared_prefix_workspace_size"):
+        assert f"kv_status {name}(" in text and hasattr(lib, name) and callable(getattr(kp, name)) and name in kp.__all__
+    assert "kv_status kv_bm_prefix_groups(" in text and "KV_DEVERR_GROUP    0x20u" in text and kp.DEVERR_GROUP == 0x20
+
+
+def test_a_null_pool_is_refused(lib):
+    bad = kp.KV_ERR_INVALID_ARG
+    n = ctypes.c_size_t()
+    assert lib.paged_norm_rope_append(None, 16, 64, 16, 64, 16, 64, 1, 1, None, None, 0.0, None, 0, 0, 0, None, None, 16, 1,
+                                      16, 1, 1, 16, None) == bad
+    assert lib.paged_attention_masked(None, 16, 1, 1, 16, 1, 16, 1, 1.0, None, 0, None, 0, 16, None, None) == bad
+    assert lib.paged_attention_masked_workspace_size(None, 1, 1, 1, 1, 0, 0, ctypes.byref(n)) == bad
+    assert lib.paged_shared_prefix_attention(None, 16, 1, 1, 16, 1, 16, 1, None, None, 0, 1.0, 0, None, 0, 16, None,
+                                             None) == bad
+    assert lib.paged_shared_prefix_workspace_size(None, 1, 1, 1, 1, 0, 0, ctypes.byref(n)) == bad
+    assert lib.paged_shared_prefix_workspace_size(None, 1, 1, 1, 1, 0, 0, None) == bad
+
+
+def test_host_tensors_are_refused():
+    import torch
+    with pytest.raises(ValueError):
+        kp._rows(torch.zeros(2, 4, 64, dtype=torch.bfloat16), 4, 64, "q")
+
+
+def groups(bm, seqs, **kw):
+    order, off, blk = (t.tolist() for t in bm.prefix_groups(seqs, **kw))
+    assert sorted(order) == list(range(len(seqs))) and off[0] == 0 and off[-1] == len(seqs) and len(off) == len(blk) + 1
+    return [([seqs[i] for i in order[off[g]:off[g + 1]]], blk[g]) for g in range(len(blk))]
+
+
+def test_groups_of_forks_and_cached_prompts():
+    bm = kp.BlockManager(64, 4, prefix_caching=True)
+    prompt = list(range(11))
+    bm.add_sequence(1)
+    bm.append_slots(1, 11, prompt)                    # two full blocks and three tokens
+    bm.fork(1, 2)
+    bm.add_sequence(3)
+    bm.append_slots(3, 9, [7] * 9)
+    bm.add_sequence(4)                                # the same prompt through the prefix cache
+    assert bm.match_prefix(4, prompt) == 8
+    bm.append_slots(4, 3, prompt[8:])
+    bm.add_sequence(5)                                # one block in common
+    assert bm.match_prefix(5, prompt[:4] + [99] * 6) == 4
+    bm.append_slots(5, 6, [99] * 6)
+    bm.add_sequence(6)                                # empty
+    assert groups(bm, [3, 1, 6, 2, 4, 5]) == [([3], 0), ([1, 2, 4, 5], 1), ([6], 0)]
+    assert groups(bm, [3, 1, 6, 2, 4, 5], min_blocks=2) == [([3], 0), ([1, 2, 4], 2), ([6], 0), ([5], 0)]
+    assert groups(bm, [3, 1, 6, 2, 4, 5], min_blocks=3) == [([s], 0) for s in (3, 1, 6, 2, 4, 5)]
+    # the partly filled last block of the forks is shared too, but not full: it never counts,
+    # also when it is full in one of them
+    bm.append_slots(2, 1, [11])
+    assert groups(bm, [2, 1]) == [([2, 1], 2)]
+    assert groups(bm, []) == []
+    bm.close()
+
+
+def test_the_same_sequence_twice_is_a_group():
+    bm = kp.BlockManager(8, 4)
+    bm.add_sequence(1)
+    bm.append_slots(1, 8)
+    assert groups(bm, [1, 1]) == [([1, 1], 2)]
+    bm.close()
+
+
+def test_groups_refusals(lib):
+    bm = kp.BlockManager(8, 4)
+    bm.add_sequence(1)
+    with pytest.raises(kp.KVError):
+        bm.prefix_groups([1, 2])
+    with pytest.raises(kp.KVError):
+        bm.prefix_groups([1], min_blocks=0)
+    n = ctypes.c_int()
+    assert lib.kv_bm_prefix_groups(None, None, 0, 1, None, None, None, ctypes.byref(n)) == kp.KV_ERR_INVALID_ARG
+    assert lib.kv_bm_prefix_groups(bm._h, None, 1, 1, None, None, None, ctypes.byref(n)) == kp.KV_ERR_INVALID_ARG
+    bm.close()
