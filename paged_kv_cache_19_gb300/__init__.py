@@ -174,9 +174,11 @@ def _need(t, dtype, name):
 
 
 class _CudaBytes:
-    """Exposes a device byte range to torch through __cuda_array_interface__."""
+    """Exposes a device byte range to torch through __cuda_array_interface__.  The tensor made
+    from it keeps this object, and with it the owner of the memory, alive."""
 
-    def __init__(self, ptr: int, shape):
+    def __init__(self, ptr: int, shape, owner):
+        self._owner = owner
         self.__cuda_array_interface__ = {"shape": tuple(shape), "typestr": "|u1",
                                          "data": (ptr, False), "version": 3, "strides": None}
 
@@ -202,17 +204,17 @@ class Pool:
     def tensors(self):
         """Torch views (no copy) of the pool: K, V as raw bytes [num_blocks, bs, Hkv, d*elem]
         viewed as bf16 or float8_e4m3fn (V is None for a latent pool), and the float32
-        scales [Hkv]."""
+        scales [Hkv].  A view keeps the pool alive; destroy() frees the memory under it."""
         lib = load_library()
         k, v, ks, vs = (ctypes.c_void_p() for _ in range(4))
         _check(lib.kv_pool_tensors(self.handle, ctypes.byref(k), ctypes.byref(v), ctypes.byref(ks),
                                    ctypes.byref(vs)), "kv_pool_tensors")
         dev = torch.device("cuda", self.device)
         shape = (self.num_blocks, self.block_size, self.kv_heads, self.head_dim * self.elem_bytes)
-        kt = torch.as_tensor(_CudaBytes(k.value, shape), device=dev)
-        vt = torch.as_tensor(_CudaBytes(v.value, shape), device=dev) if v.value else None
-        st = torch.as_tensor(_CudaBytes(ks.value, (self.kv_heads * 4,)), device=dev).view(torch.float32)
-        sv = torch.as_tensor(_CudaBytes(vs.value, (self.kv_heads * 4,)), device=dev).view(torch.float32)
+        kt = torch.as_tensor(_CudaBytes(k.value, shape, self), device=dev)
+        vt = torch.as_tensor(_CudaBytes(v.value, shape, self), device=dev) if v.value else None
+        st = torch.as_tensor(_CudaBytes(ks.value, (self.kv_heads * 4,), self), device=dev).view(torch.float32)
+        sv = torch.as_tensor(_CudaBytes(vs.value, (self.kv_heads * 4,), self), device=dev).view(torch.float32)
         cache = torch.float8_e4m3fn if self.dtype == "fp8_e4m3" else torch.bfloat16
         return kt.view(cache), None if vt is None else vt.view(cache), st, sv
 
