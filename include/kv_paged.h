@@ -379,9 +379,15 @@ typedef struct kv_attention_mask {
  *   that fell out of a window may have been freed and reused.
  *   mask: HOST struct, copied by the call; NULL = no change.  softcap >= 0 with a
  *   finite 2 / softcap, window >= 0; slopes finite (not checked).
- *   Shapes, tables, split, workspace (zero-filled before its first use), outputs
- *   and errors as in paged_attention_multi_query; the chunks of a sequence begin
- *   at the first block its queries see.
+ *   kv_split_tokens: the work of a batch is cut into equal ranges, one per CTA
+ *     that the GPU holds at a time; this is the least a range covers, in tokens of
+ *     a group of kv heads and a tile of query rows (0 = automatic; else a positive multiple
+ *     of block_size).  The result does not depend on it up to rounding.
+ *   workspace: at least paged_attention_masked_workspace_size() bytes, never 0,
+ *     zero-filled before its first use; every call leaves its counters at zero
+ *     again (after KV_DEVERR_TIMEOUT, zero it before reuse).  Calls that share one
+ *     must not overlap.  One kernel launch per call.
+ *   Shapes, tables, outputs and errors as in paged_attention_multi_query.
  */
 kv_status paged_attention_masked(const kv_pool* pool, const void* q, int q_heads, int q_len,
                                  const int32_t* block_tables, int max_blocks,
@@ -415,8 +421,8 @@ kv_status paged_attention_masked_workspace_size(const kv_pool* pool, int batch, 
  *   does (KV_DEVERR_GROUP): that group shares nothing.  The results are right
  *   either way.
  *   n_groups == 0 is allowed (nothing is shared; the arrays may be NULL).
- *   kv_split_tokens: the chunk of the members' own parts, which begin behind
- *   the shared blocks.  workspace: at least paged_shared_prefix_workspace_size()
+ *   kv_split_tokens: as in paged_attention_masked, for the members' own parts.
+ *   workspace: at least paged_shared_prefix_workspace_size()
  *   bytes, zero-filled before its first use; calls that share one must not
  *   overlap.  Everything else as in paged_attention_multi_query.  Two kernel
  *   launches (one when n_groups is 0 or the batch is 1).

@@ -35,6 +35,7 @@ struct kv_pool {
                             // per box (the wide tcgen05 decode)
     CUtensorMap tmh;        // latent pools with blocks of 64: one 128-byte piece of 32 slots
                             // per box (the narrow tcgen05 decode)
+    CUtensorMap tmsk, tmsv; // K and V pools in boxes of 16 slots (the span kernel)
     CUtensorMap tmpk, tmpv; // K and V pools in octets of slots (the shared prefix pass)
     int has_tc;
     int num_sms;
@@ -237,29 +238,39 @@ kv_status make_plan(const kv_pool* pl, int batch, int q_heads, int q_len, int ma
     return KV_OK;
 }
 
-// Split plan of the span kernel, whose tiles see at most `span_blocks` blocks of a sequence:
-// one CTA per kv head and row tile, and chunks about a sixth of what one SM would take, at
-// least 16 blocks.
+// Plan of the span kernel, whose tiles see at most `span_blocks` blocks of a sequence: units of
+// (sequence, group of kv heads, row tile), and a grid of the CTAs that are resident together, or
+// fewer where ranges of the least length cover everything.
+struct SpanPlan {
+    int rows, head_tile, head_groups, heads, least, ctas;
+    long long units, parts;         // parts: states of four warps, per unit and per range border
+};
+
+// Least positions of a CTA's range with the automatic choice.
+constexpr int kSpanLeast = 4 + kvp::SPAN_PAD;
+
 kv_status make_span_plan(const kv_pool* pl, int batch, int q_heads, int q_len, int max_blocks,
-                         int span_blocks, int split_tokens, Plan* out)
+                         int span_blocks, int split_tokens, SpanPlan* out)
 {
-    Plan p;
-    kv_status st = make_plan(pl, batch, q_heads, q_len, max_blocks, split_tokens, &p);
-    if (st != KV_OK) return st;
-    p.cta_heads = 1;
-    if (split_tokens > 0) {
-        p.split_blocks = split_tokens / pl->block_size;
-    } else {
-        const long long units = static_cast<long long>(batch > 0 ? batch : 1) * pl->kv_heads * p.head_groups;
-        const long long target = static_cast<long long>(pl->num_sms > 0 ? pl->num_sms : 148) * 6;
-        long long sb = (units * span_blocks + target - 1) / target;
-        if (sb < 16) sb = 16;
-        if (sb > 192) sb = 192;
-        p.split_blocks = static_cast<int>(sb);
-    }
-    if (p.split_blocks > span_blocks) p.split_blocks = span_blocks;
-    p.max_splits = (span_blocks + p.split_blocks - 1) / p.split_blocks;
-    if (p.max_splits > 65535) return KV_ERR_UNSUPPORTED;      // grid z limit
+    if (pl == nullptr || pl->mla || batch < 0 || q_heads <= 0 || q_len <= 0 || max_blocks <= 0 || split_tokens < 0)
+        return KV_ERR_INVALID_ARG;
+    if (q_heads % pl->kv_heads != 0 || split_tokens % pl->block_size != 0) return KV_ERR_INVALID_ARG;
+    if (static_cast<long long>(max_blocks) * pl->block_size > std::numeric_limits<int>::max())
+        return KV_ERR_INVALID_ARG;
+    if (static_cast<long long>(q_heads / pl->kv_heads) * q_len > 4096) return KV_ERR_UNSUPPORTED;
+    SpanPlan p;
+    p.rows = q_heads / pl->kv_heads * q_len;
+    p.head_tile = kvp::head_tile_for_group(p.rows);
+    p.head_groups = (p.rows + p.head_tile - 1) / p.head_tile;
+    p.heads = pl->kv_heads % 4 == 0 ? 4 : pl->kv_heads % 2 == 0 ? 2 : 1;
+    p.units = static_cast<long long>(batch) * (pl->kv_heads / p.heads) * p.head_groups;
+    if (p.units > (1 << 28)) return KV_ERR_UNSUPPORTED;
+    p.least = split_tokens > 0 ? split_tokens / 16 : kSpanLeast;
+    const long long subs = static_cast<long long>(span_blocks) * (pl->block_size / 16) + kvp::SPAN_PAD;
+    const long long most = (p.units * subs + p.least - 1) / p.least;
+    const long long resident = static_cast<long long>(pl->num_sms) * kvp::SPAN_CTAS;
+    p.ctas = static_cast<int>(most < resident ? most : resident);
+    p.parts = 4 * (p.units + p.ctas);
     *out = p;
     return KV_OK;
 }
@@ -280,7 +291,7 @@ int masked_span_blocks(const kv_pool* pl, int q_len, int max_blocks, int window)
 }
 
 kv_status make_masked_plan(const kv_pool* pl, int batch, int q_heads, int q_len, int max_blocks,
-                           int window, int split_tokens, Plan* out)
+                           int window, int split_tokens, SpanPlan* out)
 {
     if (pl == nullptr || window < 0 || q_len <= 0 || max_blocks <= 0) return KV_ERR_INVALID_ARG;
     window = effective_window(pl, window, max_blocks);
@@ -312,22 +323,38 @@ size_t workspace_bytes_for(const kv_pool* pl, int batch, const Plan& p)
     return workspace_layout(pl, batch, p).total;
 }
 
-// The shared prefix pass's part of a workspace (behind the plan's own, on a kAlign boundary):
-// run entries, (max, sum) pairs, partial outputs.  Pieces: one per run and one per range border
-// of the grid (one CTA per SM).
+// Workspace of the span kernel: tickets, (max, sum) pairs, partial outputs.
+struct SpanLayout {
+    size_t part_ml, part_o, total;
+};
+
+SpanLayout span_layout(const kv_pool* pl, const SpanPlan& p)
+{
+    SpanLayout w;
+    const size_t rows = static_cast<size_t>(p.parts) * p.head_tile;
+    w.part_ml = round_up(static_cast<size_t>(p.units) * p.heads * sizeof(int), kAlign);
+    w.part_o = w.part_ml + round_up(rows * 2 * sizeof(float), kAlign);
+    w.total = w.part_o + round_up(rows * pl->head_dim * sizeof(float), kAlign);
+    return w;
+}
+
+// The shared prefix pass's part of a workspace (behind the span kernel's): the sequences' shared
+// parts, run entries, log-sum-exps, partial outputs.  Pieces: one per run and one per range
+// border of the grid (one CTA per SM).
 struct PrefixLayout {
-    size_t runs, piece_ml, piece_o, total;
+    size_t runs, piece_lse, piece_o, total;
     long long pieces;
 };
 
-PrefixLayout prefix_layout(const kv_pool* pl, int batch, const Plan& p, int n_groups)
+PrefixLayout prefix_layout(const kv_pool* pl, int batch, const SpanPlan& p, int n_groups)
 {
     PrefixLayout w{0, 0, 0, 0, 0};
     if (n_groups == 0 || batch < 2) return w;
     const long long runs = kvp::prefix_run_slots(batch, pl->kv_heads, p.rows, n_groups);
     w.pieces = runs + pl->num_sms;
-    w.piece_ml = round_up(static_cast<size_t>(runs) * sizeof(int2), kAlign);
-    w.piece_o = w.piece_ml + round_up(static_cast<size_t>(w.pieces) * 256 * sizeof(float2), kAlign);
+    w.runs = round_up(static_cast<size_t>(batch) * sizeof(int2), kAlign);
+    w.piece_lse = w.runs + round_up(static_cast<size_t>(runs) * sizeof(int2), kAlign);
+    w.piece_o = w.piece_lse + static_cast<size_t>(w.pieces) * 256 * sizeof(float4);
     w.total = w.piece_o + static_cast<size_t>(w.pieces) * 256 * pl->head_dim * sizeof(float);
     return w;
 }
@@ -424,6 +451,8 @@ kv_status kv_pool_create(int num_blocks, int block_size, int kv_heads, int head_
         st = KV_ERR_CUDA;
     if (st == KV_OK) st = encode_pool_map(p, p->k, &p->tmk);
     if (st == KV_OK) st = encode_pool_map(p, p->v, &p->tmv);
+    if (st == KV_OK) st = encode_pool_map(p, p->k, &p->tmsk, 16);
+    if (st == KV_OK) st = encode_pool_map(p, p->v, &p->tmsv, 16);
     if (st == KV_OK) st = encode_octet_map(p, p->k, &p->tmpk);
     if (st == KV_OK) st = encode_octet_map(p, p->v, &p->tmpv);
     if (st == KV_OK) {
@@ -432,8 +461,9 @@ kv_status kv_pool_create(int num_blocks, int block_size, int kv_heads, int head_
             cudaError_t e = fp8 ? kvp::prepare_decode_fp8(head_dim, block_size, nt)
                                 : kvp::prepare_decode_bf16(head_dim, block_size, nt);
             if (e == cudaSuccess)
-                e = fp8 ? kvp::prepare_span_fp8(head_dim, block_size, nt)
-                        : kvp::prepare_span_bf16(head_dim, block_size, nt);
+                for (int hc : {1, 2, 4})
+                    if (e == cudaSuccess)
+                        e = fp8 ? kvp::prepare_span_fp8(head_dim, nt, hc) : kvp::prepare_span_bf16(head_dim, nt, hc);
             if (e != cudaSuccess) st = KV_ERR_CUDA;
         }
         if (kvp::prepare_decode_heads(fp8, head_dim, block_size) != cudaSuccess) st = KV_ERR_CUDA;
@@ -705,15 +735,17 @@ kv_status paged_decode_workspace_size(const kv_pool* pool, int batch, int q_head
 
 namespace {
 
-// Validates a decode call of a given plan and fills its kernel parameters and grid (nothing
-// launched).  extra_workspace: bytes the call needs beside the plan's own.
-kv_status fill_decode_launch(const kv_pool* pool, const Plan& plan, const void* q, int q_heads,
-                             int q_len, const int32_t* block_tables, int max_blocks,
-                             const int32_t* context_lens, int batch, float scale, void* workspace,
-                             size_t workspace_bytes, size_t extra_workspace, void* out,
-                             float* lse_out, kvp::DecodeParams* pp, dim3* grid)
+// Validates a decode call and fills its kernel parameters and grid (nothing launched).
+kv_status make_decode_launch(const kv_pool* pool, const void* q, int q_heads, int q_len,
+                             const int32_t* block_tables, int max_blocks,
+                             const int32_t* context_lens, int batch, float scale,
+                             int kv_split_tokens, void* workspace, size_t workspace_bytes,
+                             void* out, float* lse_out, Plan* plan_out, kvp::DecodeParams* pp,
+                             dim3* grid)
 {
-    kv_status st;
+    Plan plan;
+    kv_status st = make_plan(pool, batch, q_heads, q_len, max_blocks, kv_split_tokens, &plan);
+    if (st != KV_OK) return st;
     if (pool->mla) return KV_ERR_INVALID_ARG;        // latent pools: paged_mla_decode_attention
     if (batch == 0) return KV_OK;
     if (q == nullptr || block_tables == nullptr || context_lens == nullptr || out == nullptr)
@@ -725,8 +757,7 @@ kv_status fill_decode_launch(const kv_pool* pool, const Plan& plan, const void* 
     if (batch > 65535 || static_cast<long long>(pool->kv_heads) * plan.head_groups > 65535)
         return KV_ERR_UNSUPPORTED;                  // grid x / y limits
     const size_t need = workspace_bytes_for(pool, batch, plan);
-    const size_t whole = extra_workspace > 0 ? round_up(need, kAlign) + extra_workspace : need;
-    if (whole > 0 && (workspace == nullptr || workspace_bytes < whole)) return KV_ERR_INVALID_ARG;
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KV_ERR_INVALID_ARG;
     st = check_device(pool);
     if (st != KV_OK) return st;
 
@@ -766,24 +797,8 @@ kv_status fill_decode_launch(const kv_pool* pool, const Plan& plan, const void* 
     // chunk-major grid: x = (kv head group, row tile), y = sequence, z = chunk
     *grid = dim3(static_cast<unsigned>(pool->kv_heads / plan.cta_heads * plan.head_groups),
                  static_cast<unsigned>(batch), static_cast<unsigned>(plan.max_splits));
+    *plan_out = plan;
     return KV_OK;
-}
-
-// Validates a decode call and fills its kernel parameters and grid (nothing launched).
-kv_status make_decode_launch(const kv_pool* pool, const void* q, int q_heads, int q_len,
-                             const int32_t* block_tables, int max_blocks,
-                             const int32_t* context_lens, int batch, float scale,
-                             int kv_split_tokens, void* workspace, size_t workspace_bytes,
-                             void* out, float* lse_out, Plan* plan_out, kvp::DecodeParams* pp,
-                             dim3* grid)
-{
-    Plan plan;
-    kv_status st = make_plan(pool, batch, q_heads, q_len, max_blocks, kv_split_tokens, &plan);
-    if (st != KV_OK) return st;
-    st = fill_decode_launch(pool, plan, q, q_heads, q_len, block_tables, max_blocks, context_lens,
-                            batch, scale, workspace, workspace_bytes, 0, out, lse_out, pp, grid);
-    if (st == KV_OK) *plan_out = plan;
-    return st;
 }
 
 kv_status launch_decode(const kv_pool* pool, const Plan& plan, dim3 grid, const kvp::DecodeParams& p,
@@ -805,11 +820,60 @@ kv_status launch_decode(const kv_pool* pool, const Plan& plan, dim3 grid, const 
     return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }
 
-kv_status launch_span(const kv_pool* pool, const Plan& plan, dim3 grid, kvp::SpanRule rule, const kvp::SpanParams& p,
+// Validates a call of the span kernel and fills its decode parameters (nothing launched).
+// extra: workspace bytes the call needs behind the kernel's own.
+kv_status make_span_launch(const kv_pool* pool, const SpanPlan& plan, const void* q, int q_heads, int q_len,
+                           const int32_t* block_tables, int max_blocks, const int32_t* context_lens, int batch,
+                           float scale, void* workspace, size_t workspace_bytes, size_t extra, void* out,
+                           float* lse_out, kvp::SpanParams* sp)
+{
+    if (!std::isfinite(scale)) return KV_ERR_INVALID_ARG;
+    if (batch == 0) return KV_OK;
+    if (q == nullptr || block_tables == nullptr || context_lens == nullptr || out == nullptr || workspace == nullptr)
+        return KV_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
+        !aligned(lse_out, 4) || !aligned(workspace, 16))
+        return KV_ERR_INVALID_ARG;
+    const SpanLayout wl = span_layout(pool, plan);
+    if (workspace_bytes < wl.total + extra) return KV_ERR_INVALID_ARG;
+    kv_status st = check_device(pool);
+    if (st != KV_OK) return st;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    kvp::DecodeParams& p = sp->d;
+    p = {};
+    p.q = static_cast<const uint16_t*>(q);
+    p.tables = block_tables;
+    p.ctx = context_lens;
+    p.k_scale = pool->k_scale;
+    p.v_scale = pool->v_scale;
+    p.out = static_cast<uint16_t*>(out);
+    p.lse = lse_out;
+    p.tickets = reinterpret_cast<int*>(ws);
+    p.part_ml = reinterpret_cast<float*>(ws + wl.part_ml);
+    p.part_o = reinterpret_cast<float*>(ws + wl.part_o);
+    p.err = pool->err;
+    p.batch = batch;
+    p.q_heads = q_heads;
+    p.kv_heads = pool->kv_heads;
+    p.group = q_heads / pool->kv_heads;
+    p.head_groups = plan.head_groups;
+    p.q_len = q_len;
+    p.rows = plan.rows;
+    p.max_blocks = max_blocks;
+    p.num_blocks = pool->num_blocks;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.stop_stage = g_stop_stage.load(std::memory_order_relaxed);
+    p.consumer_wait_ns = g_consumer_wait_ns.load(std::memory_order_relaxed);
+    sp->block_size = pool->block_size;
+    sp->least = plan.least;
+    return KV_OK;
+}
+
+kv_status launch_span(const kv_pool* pool, const SpanPlan& plan, kvp::SpanRule rule, const kvp::SpanParams& p,
                       void* stream)
 {
     const auto launch = pool->dtype == KV_DTYPE_BF16 ? kvp::launch_span_bf16 : kvp::launch_span_fp8;
-    return launch(rule, pool->head_dim, pool->block_size, plan.head_tile, grid, pool->tmk, pool->tmv, p,
+    return launch(rule, pool->head_dim, plan.head_tile, plan.heads, plan.ctas, pool->tmsk, pool->tmsv, p,
                   static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? KV_OK
                : KV_ERR_CUDA;
@@ -841,11 +905,10 @@ kv_status paged_attention_masked_workspace_size(const kv_pool* pool, int batch, 
                                                 int kv_split_tokens, size_t* bytes)
 {
     if (bytes == nullptr) return KV_ERR_INVALID_ARG;
-    Plan p;
+    SpanPlan p;
     kv_status st = make_masked_plan(pool, batch, q_heads, q_len, max_blocks, window, kv_split_tokens, &p);
-    if (st != KV_OK) return st;
-    *bytes = workspace_bytes_for(pool, batch, p);
-    return KV_OK;
+    if (st == KV_OK) *bytes = span_layout(pool, p).total;
+    return st;
 }
 
 kv_status paged_attention_masked(const kv_pool* pool, const void* q, int q_heads, int q_len,
@@ -861,13 +924,12 @@ kv_status paged_attention_masked(const kv_pool* pool, const void* q, int q_heads
         return KV_ERR_INVALID_ARG;
     if (!aligned(m.alibi_slopes, 4) || !aligned(m.first_keys, 4) || !aligned(m.prefix_lens, 4))
         return KV_ERR_INVALID_ARG;
-    Plan plan;
+    SpanPlan plan;
     kv_status st = make_masked_plan(pool, batch, q_heads, q_len, max_blocks, m.window, kv_split_tokens, &plan);
     if (st != KV_OK) return st;
-    kvp::SpanParams p;
-    dim3 grid;
-    st = fill_decode_launch(pool, plan, q, q_heads, q_len, block_tables, max_blocks, context_lens, batch, scale,
-                            workspace, workspace_bytes, 0, out, lse_out, &p.d, &grid);
+    kvp::SpanParams p = {};
+    st = make_span_launch(pool, plan, q, q_heads, q_len, block_tables, max_blocks, context_lens, batch, scale,
+                          workspace, workspace_bytes, 0, out, lse_out, &p);
     if (st != KV_OK || batch == 0) return st;
     p.window = effective_window(pool, m.window, max_blocks);
     p.cap_log2 = m.softcap * 1.4426950408889634f;
@@ -875,9 +937,8 @@ kv_status paged_attention_masked(const kv_pool* pool, const void* q, int q_heads
     p.slopes = m.alibi_slopes;
     p.first_keys = m.first_keys;
     p.prefix_lens = m.prefix_lens;
-    p.shared = {};
     const int rule = (m.softcap > 0.f ? kvp::SPAN_CAP : 0) | (m.alibi_slopes != nullptr ? kvp::SPAN_BIAS : 0);
-    return launch_span(pool, plan, grid, static_cast<kvp::SpanRule>(rule), p, stream);
+    return launch_span(pool, plan, static_cast<kvp::SpanRule>(rule), p, stream);
 }
 
 kv_status paged_shared_prefix_workspace_size(const kv_pool* pool, int batch, int q_heads, int q_len,
@@ -885,14 +946,12 @@ kv_status paged_shared_prefix_workspace_size(const kv_pool* pool, int batch, int
                                              size_t* bytes)
 {
     if (bytes == nullptr || n_groups < 0) return KV_ERR_INVALID_ARG;
-    Plan p;
+    SpanPlan p;
     kv_status st = make_span_plan(pool, batch, q_heads, q_len, max_blocks, max_blocks, kv_split_tokens, &p);
     if (st != KV_OK) return st;
-    if (pool->mla) return KV_ERR_INVALID_ARG;
     const PrefixLayout l = prefix_layout(pool, batch, p, n_groups);
     if (l.pieces > (1 << 30)) return KV_ERR_UNSUPPORTED;
-    const size_t own = workspace_bytes_for(pool, batch, p);
-    *bytes = l.total > 0 ? round_up(own, kAlign) + l.total : own;
+    *bytes = span_layout(pool, p).total + l.total;
     return KV_OK;
 }
 
@@ -907,20 +966,18 @@ kv_status paged_shared_prefix_attention(const kv_pool* pool, const void* q, int 
     if (n_groups < 0 || (n_groups > 0 && (group_offsets == nullptr || group_blocks == nullptr)) ||
         !aligned(group_offsets, 4) || !aligned(group_blocks, 4))
         return KV_ERR_INVALID_ARG;
-    Plan plan;
+    SpanPlan plan;
     kv_status st = make_span_plan(pool, batch, q_heads, q_len, max_blocks, max_blocks, kv_split_tokens, &plan);
     if (st != KV_OK) return st;
-    if (pool->mla) return KV_ERR_INVALID_ARG;
     const PrefixLayout l = prefix_layout(pool, batch, plan, n_groups);
     if (l.pieces > (1 << 30)) return KV_ERR_UNSUPPORTED;
     kvp::SpanParams p = {};
-    dim3 grid;
-    st = fill_decode_launch(pool, plan, q, q_heads, q_len, block_tables, max_blocks, context_lens, batch, scale,
-                            workspace, workspace_bytes, l.total, out, lse_out, &p.d, &grid);
+    st = make_span_launch(pool, plan, q, q_heads, q_len, block_tables, max_blocks, context_lens, batch, scale,
+                          workspace, workspace_bytes, l.total, out, lse_out, &p);
     if (st != KV_OK || batch == 0) return st;
-    if (l.total == 0) return launch_span(pool, plan, grid, kvp::SPAN_MASK, p, stream);   // nobody to share with
+    if (l.total == 0) return launch_span(pool, plan, kvp::SPAN_MASK, p, stream);   // nobody to share with
     kvp::PrefixParams& s = p.shared;
-    uint8_t* ws = static_cast<uint8_t*>(workspace) + round_up(workspace_bytes_for(pool, batch, plan), kAlign);
+    uint8_t* ws = static_cast<uint8_t*>(workspace) + span_layout(pool, plan).total;
     s.q = p.d.q;
     s.tables = block_tables;
     s.ctx = context_lens;
@@ -928,8 +985,9 @@ kv_status paged_shared_prefix_attention(const kv_pool* pool, const void* q, int 
     s.group_blocks = group_blocks;
     s.k_scale = pool->k_scale;
     s.v_scale = pool->v_scale;
+    s.seqs = reinterpret_cast<int2*>(ws);
     s.runs = reinterpret_cast<int2*>(ws + l.runs);
-    s.piece_ml = reinterpret_cast<float2*>(ws + l.piece_ml);
+    s.piece_lse = reinterpret_cast<float4*>(ws + l.piece_lse);
     s.piece_o = reinterpret_cast<float*>(ws + l.piece_o);
     s.err = pool->err;
     s.batch = batch;
@@ -944,7 +1002,7 @@ kv_status paged_shared_prefix_attention(const kv_pool* pool, const void* q, int 
     if (kvp::launch_prefix(pool->dtype == KV_DTYPE_FP8_E4M3, pool->head_dim, pool->block_size, pool->num_sms, pool->tmpk,
                            pool->tmpv, s, static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return KV_ERR_CUDA;
-    return launch_span(pool, plan, grid, kvp::SPAN_SUFFIX, p, stream);
+    return launch_span(pool, plan, kvp::SPAN_SUFFIX, p, stream);
 }
 
 kv_status paged_decode_step(kv_pool* pool, const void* k_new, const void* v_new, const void* q,

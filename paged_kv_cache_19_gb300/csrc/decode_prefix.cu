@@ -79,7 +79,12 @@ struct PfxCtl {
     long long base;                                 // first unit of group0
     int group0, ctas;                               // group that holds lo; CTAs with units
     long long scan[32];
-    float q_up[2][PFX_TILE];                        // fp8: undoes a row's power-of-two scale
+    uint64_t x_full, x_free;                        // team 1's state handed over, read
+    union {
+        float q_up[2][PFX_TILE];                    // fp8: undoes a row's power-of-two scale (read at an
+                                                    // item's start)
+        float2 x_ml[PFX_TILE];                      // team 1's maxima and sums (written at its end)
+    };
 };
 
 // A run of one CTA: tiles tile0 .. tile0 + n - 1 of (group, kv head, pair).
@@ -153,6 +158,14 @@ __device__ __forceinline__ bool pfx_wait(uint32_t bar, uint32_t parity, volatile
     }
 }
 
+// Eight floats, one 32-byte sector.
+__device__ __forceinline__ void store_sector(float* dst, const float* x)
+{
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+                 "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ void pfx_give_up(const PrefixParams& p, volatile int* abort_flag)
 {
     if (!*abort_flag) atomicOr(p.err, KV_DEVERR_TIMEOUT);
@@ -197,6 +210,8 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             mbar_init(smem_u32(&ctl->o_full[s]), 1);
         }
         mbar_init(smem_u32(&ctl->mma_done), 1);
+        mbar_init(smem_u32(&ctl->x_full), 4);
+        mbar_init(smem_u32(&ctl->x_free), 4);
         ctl->abort_flag = 0;
         fence_mbar_init();
     }
@@ -230,6 +245,14 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         long long units = 0;
         for (int w = 0; w < C::THREADS / 32; ++w) units += ctl->scan[w];
         if (!all) units = 0;
+        // the sequences' shared parts, for the suffix kernel
+        for (int g = all ? blockIdx.x : p.n_groups; g < p.n_groups; g += gridDim.x) {
+            const PrefixGroup gr = load_prefix_group(p, g);
+            for (int m = tid; m < gr.n; m += C::THREADS) p.seqs[gr.off + m] = make_int2(gr.blocks * BS, g);
+        }
+        const int in0 = all ? __ldg(p.group_offsets) : p.batch, in1 = all ? __ldg(p.group_offsets + p.n_groups) : p.batch;
+        for (int b = blockIdx.x * C::THREADS + tid; b < p.batch; b += gridDim.x * C::THREADS)
+            if (b < in0 || b >= in1) p.seqs[b] = make_int2(0, -1);
         const int ctas = units < gridDim.x ? static_cast<int>(units) : static_cast<int>(gridDim.x);
         const int c = blockIdx.x;
         const long long lo = c < ctas ? units * c / ctas : 0;
@@ -446,6 +469,7 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         bool ok = true;
         int kt = 0;                                 // K tiles of the items before
         uint32_t seen = 0;                          // score tiles of this slot waited for
+        int swaps = 0;                              // items whose slots were merged
         for (int k = 0; walk.next(p, BS, it); ++k) {
             // ---- this warp's 32 rows of q into shared memory (K-major, 128-byte swizzle);
             // the score MMAs of the item before are complete (o_full)
@@ -603,26 +627,70 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             if (!ok) break;
             tc_fence_after();
 
-            // ---- epilogue: this row's piece, normalised; thread = row, so that each store of a
-            // warp is 512 contiguous bytes
-            const size_t piece = (static_cast<size_t>(blockIdx.x) + it.run) * 2 + s;
-            const float inv = l > 0.f ? (FP8 ? __ldg(p.v_scale + it.kvh) : 1.f) / l : 0.f;
-            if (row < rows) p.piece_ml[piece * PFX_TILE + row] = make_float2(m_ref, l);
-            if (!idle && (!it.both || s < it.n)) {  // the slot had a tile at all
-                float4* dst = reinterpret_cast<float4*>(p.piece_o + piece * (PFX_TILE * D)) + row;
+            // ---- epilogue: the pair's rows of the piece, normalised.  Where the slots took alternate
+            // tiles of the same rows, team 1 hands its state over through the rows' shared memory
+            // (idle: every score MMA of the item is complete), [number][row], and team 0 merges.
+            float m_out = m_ref, l_out = l, keep = 1.f, add = 0.f;
+            const bool handed = it.both && it.n > 1;
+            float* xo = reinterpret_cast<float*>(qsm);
+            if (handed) {
+                const uint32_t ph = static_cast<uint32_t>(swaps) & 1u;
+                ++swaps;
+                ok = all_ok(pfx_wait(smem_u32(&ctl->o_full[s ^ 1]), static_cast<uint32_t>(k) & 1u, abort_flag));
+                if (ok && s == 1 && !idle) {
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t r[32];
+                        tc_ld32(tm_o + c * 32, r);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) xo[(c * 32 + j) * PFX_TILE + row] = __uint_as_float(r[j]);
+                    }
+                    ctl->x_ml[row] = make_float2(m_ref, l);
+                }
+                __syncwarp();
+                if (ok && s == 1 && lane == 0) mbar_arrive(smem_u32(&ctl->x_full));
+                if (ok && s == 0) ok = all_ok(pfx_wait(smem_u32(&ctl->x_full), ph, abort_flag));
+                if (!ok) break;
+                if (s == 0) {
+                    const float2 o = ctl->x_ml[row];
+                    m_out = o.y > 0.f ? (l > 0.f ? fmaxf(m_ref, o.x) : o.x) : m_ref;
+                    keep = l > 0.f ? fast_exp2(m_ref - m_out) : 0.f;
+                    add = o.y > 0.f ? fast_exp2(o.x - m_out) : 0.f;
+                    l_out = l * keep + o.y * add;
+                }
+            }
+            if (!idle && !(it.both && s == 1)) {
+                const float inv = l_out > 0.f ? (FP8 ? __ldg(p.v_scale + it.kvh) : 1.f) / l_out : 0.f;
+                keep *= inv;
+                add *= inv;
+                const size_t at = (static_cast<size_t>(blockIdx.x) + it.run) * PFX_PAIR + s * PFX_TILE + row;
+                if (row < rows)
+                    p.piece_lse[at] = make_float4(l_out > 0.f ? m_out + __log2f(l_out) : -INFINITY, 0.f, 0.f, 0.f);
+                float* dst = p.piece_o + at * D;
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t r[32];
                     tc_ld32(tm_o + c * 32, r);
                     tc_wait_ld();
+                    float x[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        x[j] = __uint_as_float(r[j]) * keep;
+                        if (add != 0.f) x[j] += xo[(c * 32 + j) * PFX_TILE + row] * add;
+                    }
                     if (row < rows) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            dst[(c * 8 + j) * PFX_TILE] =
-                                make_float4(__uint_as_float(r[4 * j]) * inv, __uint_as_float(r[4 * j + 1]) * inv,
-                                            __uint_as_float(r[4 * j + 2]) * inv, __uint_as_float(r[4 * j + 3]) * inv);
+                        for (int j = 0; j < 32; j += 8) store_sector(dst + c * 32 + j, x + j);
                     }
                 }
+            }
+            if (handed) {
+                // the rows' memory is free for the next item's once team 0 has read it
+                __syncwarp();
+                if (s == 0 && lane == 0) mbar_arrive(smem_u32(&ctl->x_free));
+                ok = all_ok(pfx_wait(smem_u32(&ctl->x_free), static_cast<uint32_t>(swaps - 1) & 1u, abort_flag));
+                if (!ok) break;
             }
             if (it.tile0 == 0 && tid == 0) {
                 // the run's pieces: one per CTA from this one to the one of its last tile

@@ -7,19 +7,32 @@
 //   score  x = scale q . K[t];  x <- cap tanh(x / cap);  x <- x - slope_h |p - t|
 //   out = softmax over those keys of x, times V;  a row that sees no key gives 0 and lse = -inf
 // (the sliding window, the cap, the distance bias, the document start and the visible prefix
-// are each optional).  It is the decode kernel's structure (decode_kernel.cuh: one producer
-// warp, a ring of TMA stages, four consumer warps, chunks merged by the last CTA of a unit)
-// with two differences: a tile of query rows starts at the first block that one of its rows
-// sees -- chunk j covers blocks [first + j S, first + (j + 1) S) -- and the rule of a row
-// (SpanRows) is applied to the raw scores before the softmax.
+// are each optional).  The suffix form (SPAN_SUFFIX, paged_shared_prefix_attention) starts a
+// sequence's keys behind the blocks that its group shares and takes the pieces that the shared
+// pass left for its rows (prefix_groups.cuh) into the merge.
 //
-// The suffix form (SPAN_SUFFIX, paged_shared_prefix_attention) starts a sequence's keys behind
-// the blocks that its group shares and takes the pieces that the shared pass left for its rows
-// (prefix_groups.cuh) as further chunks of the merge.
-//
-// It stays bound by the K/V bytes of the visible blocks.  The cap costs one ex2 and one
-// reciprocal per score (capped_tanh), the bias one add and one multiply; both are template
-// flags, so a plain mask pays for neither.
+// A unit is (sequence, group of HC kv heads, tile of query rows) with the 16-token sub-blocks its
+// rows see.  Windows, document starts and shared parts make the units of a batch short and unequal,
+// so the grid is persistent -- the CTAs that are resident together -- and the units' sub-blocks,
+// each unit preceded by SPAN_PAD positions for what starting and finishing it costs, are cut into
+// equal contiguous ranges, one per CTA.
+//   * One producer warp walks the CTA's range, hands every unit on through a queue in shared memory
+//     and streams what it needs through a ring of stages: the query rows, then its sub-blocks, HC
+//     heads at a time (5-D TMA tensor loads), then the pieces of the shared pass (bulk copies).  It
+//     runs ahead over unit borders, so the consumers read nothing from global memory themselves and
+//     find the next unit's lengths and data there.
+//   * Four consumer warps, 4 / HC per kv head, fold their head's tile of a sub-block (every
+//     (4 / HC)-th one) into an online-softmax state in registers (decode_common.cuh,
+//     process_block_rows under the rule of SpanRows).  With four heads a warp owns its rows and
+//     finishes a unit by itself.
+// Where several warps hold parts of the same rows -- a unit cut by a range border, or several warps
+// per head -- each leaves its fp32 state in the accumulators' layout, and the warp that finishes
+// last merges them in order (a ticket per unit and head, zero between calls).
+// SPAN_FIGURES
+// Bound by the K/V bytes of the visible blocks.  The cap costs one ex2 and one reciprocal per
+// score (capped_tanh), the bias one add and one multiply; both are template flags, so a plain
+// mask pays for neither.  Every wait is bounded (WAIT_LIMIT_NS); a warp whose wait runs out sets
+// KV_DEVERR_TIMEOUT and leaves, and the producer waits for its copies in flight.
 #pragma once
 
 #include "decode_common.cuh"
@@ -62,402 +75,702 @@ struct SpanRows {
     __device__ __forceinline__ int value_hi() const { return tile_hi - base; }
 };
 
-// The pieces of a shared pass that hold query row `r` (of the `rows` of a kv head) of a sequence:
-// entry e has its (max, sum) at ml(e) and its normalised output numbers d0 .. d0 + 3 at o(e, d0).
-template <int D>
-struct RowPieces {
-    const float2* ml0;
-    const float* o0;
-    int n = 0;
-    bool both = false;                // the two slots of a piece hold the same rows
-    __device__ __forceinline__ void find(const PrefixParams& p, int g, int b, int kvh, int r)
+constexpr int SPAN_TOK = 16;          // tokens of a sub-block
+
+// The keys of one sequence.
+template <int RULE>
+struct SpanSeq {
+    int ctx, first, visible, group;   // group: whose shared pass holds the keys before first, or -1
+    __device__ __forceinline__ void load(const SpanParams& sp, int b, bool flag)
     {
-        const PrefixGroup gr = load_prefix_group(p, g);
-        const int grow = (b - gr.off) * p.rows + r;
-        const int pair = grow / PFX_PAIR, at = grow - pair * PFX_PAIR;
-        const int pairs = prefix_pairs(p, gr);
-        const int2 run = __ldcg(p.runs + prefix_run_base(p, g, gr) + kvh * pairs + pair);
-        // (a shared pass that gave up may have left this run's entry unwritten)
-        if (run.x < 0 || run.y < 0 || run.x > p.pieces - run.y) return;
-        both = gr.n * p.rows - pair * PFX_PAIR <= PFX_TILE;
-        const size_t slot = static_cast<size_t>(run.x) * 2 + at / PFX_TILE;
-        ml0 = p.piece_ml + slot * PFX_TILE + at % PFX_TILE;
-        o0 = p.piece_o + slot * (PFX_TILE * D) + at % PFX_TILE * 4;
-        n = both ? 2 * run.y : run.y;
-    }
-    __device__ __forceinline__ size_t slot(int e) const { return both ? e : 2 * e; }
-    __device__ __forceinline__ float2 ml(int e) const { return __ldcg(ml0 + slot(e) * PFX_TILE); }
-    __device__ __forceinline__ float4 o(int e, int d0) const
-    {
-        return __ldcg(reinterpret_cast<const float4*>(o0 + slot(e) * (PFX_TILE * D) + d0 * PFX_TILE));
-    }
-};
-
-// Adds the pieces of a row to acc (numbers d0 ..) and the weight W, against the maximum M.
-template <class C, int D>
-__device__ __forceinline__ void add_pieces(const RowPieces<D>& pc, int d0, float M, float (&acc)[C::E], float& W)
-{
-#pragma unroll 4
-    for (int e = 0; e < pc.n; ++e) {
-        const float2 v = pc.ml(e);
-        if (!(v.y > 0.f)) continue;                  // a piece this row sees nothing of
-        const float w = v.y * fast_exp2(v.x - M);
-        W += w;
-#pragma unroll
-        for (int k = 0; k < C::E; k += 4) {
-            const float4 x = pc.o(e, d0 + k);
-            acc[k] += w * x.x;
-            acc[k + 1] += w * x.y;
-            acc[k + 2] += w * x.z;
-            acc[k + 3] += w * x.w;
+        const DecodeParams& p = sp.d;
+        ctx = __ldg(p.ctx + b);
+        first = visible = 0;
+        group = -1;
+        if constexpr (RULE == SPAN_SUFFIX) {
+            const int2 s = __ldcg(sp.shared.seqs + b);
+            first = max(0, s.x);
+            group = s.x > 0 ? s.y : -1;
+        } else {
+            if (sp.first_keys != nullptr) first = max(0, __ldg(sp.first_keys + b));
+            if (sp.prefix_lens != nullptr) visible = __ldg(sp.prefix_lens + b);
         }
-    }
-}
-
-template <bool FP8, int D, int BS, int NT>
-struct SpanCfg : DecodeCfg<FP8, D, BS, NT> {
-    using C = DecodeCfg<FP8, D, BS, NT>;
-    static constexpr int SMEM = 1024 + C::NSTAGE * C::STAGE + C::NSTAGE * (8 + 8 + 4) + 16;   // ring, barriers, ids, flags
-    static constexpr int MINB = NT == 8 ? 3 : 2;    // CTAs per SM: 16-row tiles keep twice the state
-    static_assert(C::RED_BYTES <= C::NSTAGE * C::STAGE, "epilogue buffer reuses the stages");
-};
-
-template <bool FP8, int D, int BS, int NT, int RULE>
-__global__ void __launch_bounds__(DecodeCfg<FP8, D, BS, NT>::THREADS, SpanCfg<FP8, D, BS, NT>::MINB)
-paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                  const SpanParams sp)
-{
-    using C = DecodeCfg<FP8, D, BS, NT>;
-    const DecodeParams& p = sp.d;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::NSTAGE * C::STAGE);
-    uint64_t* empty = full + C::NSTAGE;
-    int* stage_blk = reinterpret_cast<int*>(empty + C::NSTAGE);
-    int* merge_flag = stage_blk + C::NSTAGE;
-    int* group_slot = merge_flag + 1;                  // the suffix form: the sequence's group
-    constexpr bool SUFFIX = RULE == SPAN_SUFFIX;
-
-    const int b = blockIdx.y;
-    const int kvh = blockIdx.x / p.head_groups;
-    const int hg = blockIdx.x - kvh * p.head_groups;
-    const int split = blockIdx.z;
-    const int warp = threadIdx.x >> 5;
-    const int lane = threadIdx.x & 31;
-    const int nh = min(NT, p.rows - hg * NT);          // real rows in this tile
-    const size_t row0 = (static_cast<size_t>(b) * p.kv_heads + kvh) * p.rows + hg * NT;
-
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < C::NSTAGE; ++i) {
-            mbar_init(smem_u32(full + i), 1);
-            mbar_init(smem_u32(empty + i), 1);
+        const int cap = p.max_blocks * sp.block_size;
+        if (ctx < 0 || ctx > cap || (ctx > 0 && ctx < p.q_len)) {
+            // out of range (clamped), or fewer cached tokens than new queries (kept: the queries
+            // at negative positions see nothing but the visible prefix)
+            if (flag) atomicOr(p.err, KV_DEVERR_CONTEXT);
+            ctx = ctx < 0 ? 0 : (ctx > cap ? cap : ctx);
         }
-        fence_mbar_init();
-        if constexpr (SUFFIX) *group_slot = -1;
-    }
-    grid_dependency_wait();                          // inputs of the preceding kernel are ready
-
-    int ctx = __ldg(p.ctx + b);
-    int first = 0, prefix = 0;
-    int group = -1;                                  // the sequence's group, if it shares blocks
-    if constexpr (SUFFIX) {
-        __syncthreads();
-        bool ok = true;
-        for (int g = threadIdx.x; g < sp.shared.n_groups; g += C::THREADS) {
-            ok = ok && prefix_offsets_ok(sp.shared, g);
-            if (__ldg(sp.shared.group_offsets + g) <= b && b < __ldg(sp.shared.group_offsets + g + 1)) *group_slot = g;
-        }
-        if (__syncthreads_and(ok)) group = *group_slot;   // bad offsets: nothing is shared
-        if (group >= 0) {
-            first = load_prefix_group(sp.shared, group).blocks * BS;
-            if (first == 0) group = -1;
-        }
-    } else {
-        if (sp.first_keys != nullptr) first = max(0, __ldg(sp.first_keys + b));
-        if (sp.prefix_lens != nullptr) prefix = __ldg(sp.prefix_lens + b);
-    }
-    uint32_t qf[C::KS][C::NTT][2];
-    float sl2 = 0.f;
-    if (warp < C::NCW)
-        sl2 = load_q_frags<FP8, D, BS, NT>(qf, p.q + row0 * D, nh, lane, p.scale_log2, p.k_scale, kvh);
-    const int cap = p.max_blocks * BS;
-    if (ctx < 0 || ctx > cap || (ctx > 0 && ctx < p.q_len)) {
-        // out of range (clamped), or fewer cached tokens than new queries (kept: the queries
-        // at negative positions see nothing but the visible prefix)
-        if (threadIdx.x == 0 && split == 0 && blockIdx.x == 0) atomicOr(p.err, KV_DEVERR_CONTEXT);
-        ctx = ctx < 0 ? 0 : (ctx > cap ? cap : ctx);
+        visible = min(visible, ctx);
     }
     // keys of query token i: both ends grow with i
-    const int visible = min(prefix, ctx);
-    const auto key_lo = [&](int i) {
-        const int pos = ctx - p.q_len + i;
-        return !SUFFIX && sp.window > 0 ? max(first, pos - sp.window + 1) : first;
-    };
-    const auto key_hi = [&](int i) { return max(ctx - p.q_len + i + 1, visible); };
-    // tokens of the tile's rows: a run, or all of them where the tile spans two heads
-    const int i0 = (hg * NT) % p.q_len;
-    const bool wraps = i0 + nh > p.q_len;
-    const int tile_lo = key_lo(wraps ? 0 : i0);
-    const int tile_hi = key_hi(wraps ? p.q_len - 1 : i0 + nh - 1);
-    const int blk_first = tile_lo / BS;
-    const int nblk = tile_hi > tile_lo ? (tile_hi + BS - 1) / BS - blk_first : 0;
-    const int nsplit = nblk > 0 ? (nblk + p.split_blocks - 1) / p.split_blocks : 1;
-    const int blk0 = blk_first + split * p.split_blocks;
-    const int nb = max(0, min(nblk - split * p.split_blocks, p.split_blocks));
-    __syncthreads();                                 // barriers initialised
-    if (split >= nsplit) {                           // this tile has fewer chunks
-        grid_dependents_launch();
-        return;
+    __device__ __forceinline__ int key_lo(const SpanParams& sp, int i) const
+    {
+        if (RULE == SPAN_SUFFIX || sp.window <= 0) return first;
+        return max(first, ctx - sp.d.q_len + i - sp.window + 1);
     }
-
-    // ------------------------------------------------------------ producer warp
-    if (warp == C::NCW) {
-        if (lane == 0) {
-            prefetch_tensormap(&tmk);
-            prefetch_tensormap(&tmv);
-        }
-        const int32_t* trow = p.tables + static_cast<size_t>(b) * p.max_blocks + blk0;
-        int issued = 0;
-        bool ok = true;
-        for (int base = 0; base < nb && ok; base += 32) {
-            const int j = base + lane;
-            int id = -1;
-            if (j < nb) {
-                id = __ldg(trow + j);
-                if (id < 0 || id >= p.num_blocks) {
-                    atomicOr(p.err, KV_DEVERR_BLOCK_ID);
-                    id = -1;                          // skipped: never addressed
-                }
-            }
-            const int cnt = min(32, nb - base);
-            for (int k = 0; k < cnt; ++k) {
-                const int blk = __shfl_sync(FULL_MASK, id, k);
-                const int it = base + k;
-                if (it == p.stop_stage) {                // test hook: the rest never lands
-                    ok = false;
-                    break;
-                }
-                const int st = it % C::NSTAGE;
-                const uint32_t ph = static_cast<uint32_t>(it / C::NSTAGE) & 1u;
-                int good = 1;
-                if (lane == 0) {
-                    if (!mbar_wait_bounded(smem_u32(empty + st), ph ^ 1u)) {
-                        atomicOr(p.err, KV_DEVERR_TIMEOUT);
-                        good = 0;
-                    } else {
-                        stage_blk[st] = blk;
-                        const uint32_t fb = smem_u32(full + st);
-                        if (blk >= 0) {
-                            const uint32_t dst = smem_u32(smem + st * C::STAGE);
-                            mbar_arrive_expect_tx(fb, C::STAGE);
-                            tma_load_5d(dst, &tmk, 0, 0, kvh, 0, blk, fb);
-                            tma_load_5d(dst + C::TILE, &tmv, 0, 0, kvh, 0, blk, fb);
-                        } else {
-                            mbar_arrive(fb);
-                        }
-                    }
-                }
-                good = __shfl_sync(FULL_MASK, good, 0);
-                if (!good) {
-                    ok = false;
-                    break;
-                }
-                issued = it + 1;
-            }
-        }
-        grid_dependents_launch();                    // every load of this CTA is issued
-        // Drain: the CTA must not exit while a copy into its shared memory is in flight.
-        if (lane == 0) {
-            for (int it = max(0, issued - C::NSTAGE); it < issued; ++it) {
-                if (!mbar_wait_bounded(smem_u32(full + (it % C::NSTAGE)),
-                                       static_cast<uint32_t>(it / C::NSTAGE) & 1u)) {
-                    atomicOr(p.err, KV_DEVERR_TIMEOUT);
-                    break;
-                }
-            }
-        }
-        return;
+    __device__ __forceinline__ int key_hi(const SpanParams& sp, int i) const
+    {
+        return max(ctx - sp.d.q_len + i + 1, visible);
     }
+    // keys that some row of tile hg sees; the tile's tokens are a run, or all of them where it
+    // spans two heads
+    __device__ __forceinline__ void tile_keys(const SpanParams& sp, int hg, int nt, int& lo, int& hi) const
+    {
+        const DecodeParams& p = sp.d;
+        const int i0 = (hg * nt) % p.q_len;
+        const int nh = min(nt, p.rows - hg * nt);
+        const bool wraps = i0 + nh > p.q_len;
+        lo = key_lo(sp, wraps ? 0 : i0);
+        hi = key_hi(sp, wraps ? p.q_len - 1 : i0 + nh - 1);
+    }
+    // its sub-blocks: [sub, sub + return value)
+    __device__ __forceinline__ int tile_subs(const SpanParams& sp, int hg, int nt, int& sub) const
+    {
+        int lo, hi;
+        tile_keys(sp, hg, nt, lo, hi);
+        sub = lo / SPAN_TOK;
+        return hi > lo ? (hi + SPAN_TOK - 1) / SPAN_TOK - sub : 0;
+    }
+};
 
-    // ------------------------------------------------------------ consumer warps
-    SpanRows<C::NTT, RULE> rows;
-    rows.sl2 = sl2;
-    rows.cap_in = sp.cap_in;
-    rows.cap_log2 = sp.cap_log2;
-    rows.tile_lo = tile_lo;
-    rows.tile_hi = tile_hi;
+// A CTA's range of positions [lo, hi), and where it begins.
+struct SpanRange {
+    long long lo, hi;
+    long long base;                   // position of sequence b0's first unit
+    int b0;
+};
+
+// A run of sub-blocks of one unit.
+template <int RULE>
+struct SpanItem {
+    SpanSeq<RULE> seq;
+    int b, kg, hg, unit;              // sequence, group of kv heads, row tile; -1: no more items
+    int sub0, n;                      // sub-blocks [sub0, sub0 + n) of the sequence
+    int split, nsplit;                // which of the unit's pieces this is
+    int range0;                       // range of its first piece
+};
+
+// Walks the units of a CTA's range.
+template <int RULE, int NT, int HC>
+struct SpanWalk {
+    SpanSeq<RULE> seq;
+    long long lo, hi, total, at;      // at: position of the current unit
+    int b, kg, hg, ranges;
+    bool pending;                     // the sequence of the next unit is not loaded yet
+
+    __device__ __forceinline__ void init(const SpanParams& sp, const SpanRange& r, long long all, int n_ranges)
+    {
+        lo = r.lo;
+        hi = r.hi;
+        total = all;
+        ranges = n_ranges;
+        at = hi;                      // an empty range has no base and no first sequence
+        b = kg = hg = 0;
+        pending = false;
+        if (lo >= hi) return;
+        at = r.base;
+        b = r.b0;
+        seq.load(sp, b, false);
+        // whole groups of kv heads before the range
+        long long per = 0;
+        int sub;
+        for (int t = 0; t < sp.d.head_groups; ++t) per += seq.tile_subs(sp, t, NT, sub) + SPAN_PAD;
+        kg = static_cast<int>((lo - at) / per);
+        at += kg * per;
+    }
+    __device__ __forceinline__ int range_of(long long pos) const
+    {
+        return static_cast<int>(((pos + 1) * ranges - 1) / total);
+    }
+    __device__ __forceinline__ bool next(const SpanParams& sp, SpanItem<RULE>& it)
+    {
+        while (at < hi) {
+            if (pending) {
+                seq.load(sp, b, false);
+                pending = false;
+            }
+            int sub;
+            const int n = seq.tile_subs(sp, hg, NT, sub);
+            const long long first = at + SPAN_PAD, end = first + n;
+            const long long a = max(lo, first), z = min(hi, end);
+            const bool mine = n > 0 ? a < z : at >= lo;
+            if (mine) {
+                it.seq = seq;
+                it.b = b;
+                it.kg = kg;
+                it.hg = hg;
+                it.unit = (b * (sp.d.kv_heads / HC) + kg) * sp.d.head_groups + hg;
+                it.split = 0;
+                it.nsplit = 1;
+                it.range0 = static_cast<int>(blockIdx.x);      // with unit: an index of its own
+                it.sub0 = sub;
+                it.n = n;
+                if (n > 0 && (first < lo || end > hi)) {
+                    it.range0 = range_of(first);
+                    it.nsplit = range_of(end - 1) - it.range0 + 1;
+                    it.split = static_cast<int>(blockIdx.x) - it.range0;
+                    it.sub0 = sub + static_cast<int>(a - first);
+                    it.n = static_cast<int>(z - a);
+                }
+            }
+            at = end;
+            if (++hg == sp.d.head_groups) {
+                hg = 0;
+                if (++kg == sp.d.kv_heads / HC) {
+                    kg = 0;
+                    ++b;
+                    pending = true;
+                }
+            }
+            if (mine) return true;
+        }
+        return false;
+    }
+};
+
+// Kinds of a stage, in the low bits of its tag.
+constexpr int TAG_SKIP = 0;           // a sub-block of an invalid block: nothing landed
+constexpr int TAG_KV = 1;             // a sub-block
+constexpr int TAG_Q = 2;              // the unit's query rows
+constexpr int TAG_PIECE = 3;          // rows [a, b) of a piece: a, b in bits 8 .., 16 ..; the heads that
+constexpr int TAG_LAST = 4;           // have it in bits 24 ..
+                                      // LAST: the unit ends with this stage
+
+// Rows of a tile whose pieces lie next to each other: at most three segments, cut where the group's
+// rows pass into another row tile of the shared pass and at the rows a stage holds.
+template <int NT, int RPS>
+struct PieceRows {
+    int row0, nh;                     // the tile's first row in its group, its rows
+    __device__ __forceinline__ int end(int a) const
+    {
+        return min(nh, min(a + RPS, PFX_TILE - (row0 + a) % PFX_TILE + a));
+    }
+};
+
+// Rows [a, b) of a piece -- normalised outputs o [row][D] and log-sum-exps (log2 units, 4 floats
+// apart; -inf: the row saw nothing) in shared memory -- folded into the state as one more block;
+// out_scale: the factor that takes its outputs to the state's units.
+template <bool FP8, int D, int NT>
+__device__ __forceinline__ void fold_piece(const float* o, const float* lse, int a, int b, float out_scale,
+                                           WarpState<DecodeCfg<FP8, D, SPAN_TOK, NT>>& st, int lane)
+{
+    using C = DecodeCfg<FP8, D, SPAN_TOK, NT>;
+    const int r = lane >> 2;
 #pragma unroll
     for (int nt = 0; nt < C::NTT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int local = nt * 8 + 2 * (lane & 3) + j;
-            const int r = hg * NT + local;
-            const int head = r / p.q_len, i = r - head * p.q_len;
-            rows.lo[nt][j] = key_lo(i);
-            rows.hi[nt][j] = local < nh ? key_hi(i) : 0;      // padding rows see nothing
-            rows.pos[nt][j] = ctx - p.q_len + i;
-            rows.slope[nt][j] = rows.BIAS && local < nh
-                                    ? __ldg(sp.slopes + kvh * p.group + head) * 1.4426950408889634f
-                                    : 0.f;
-        }
-    WarpState<C> st;
-    reset_state(st);
-    const unsigned long long wait_ns = p.consumer_wait_ns ? p.consumer_wait_ns : WAIT_LIMIT_NS;
-    for (int it = warp; it < nb; it += C::NCW) {
-        const int s = it % C::NSTAGE;
-        const uint32_t ph = static_cast<uint32_t>(it / C::NSTAGE) & 1u;
-        const bool arrived = mbar_wait_bounded(smem_u32(full + s), ph, wait_ns);
-        if (!__all_sync(FULL_MASK, arrived)) {
-            if (lane == 0) atomicOr(p.err, KV_DEVERR_TIMEOUT);
-            break;
-        }
-        const int blk = stage_blk[s];
-        if (blk >= 0) {
-            const uint32_t tk = smem_u32(smem + s * C::STAGE);
-            rows.base = (blk0 + it) * BS;
-            process_block_rows<FP8, D, BS, NT>(tk, tk + C::TILE, rows, qf, st, lane);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(empty + s));
-    }
-
-    // ------------------------------------------------------------ epilogue
-    grid_dependents_launch();
-    reduce_row_sums(st);
-    named_barrier_sync(1, C::NCW * 32);     // every consumer is done with the stages
-    float* red = reinterpret_cast<float*>(smem);
-    stash_state<FP8>(red, st, warp, lane);
-    named_barrier_sync(1, C::NCW * 32);
-
-    const int t = threadIdx.x;
-    const int head = (t * C::E) / D;
-    const int d0 = (t * C::E) % D;
-    const size_t bh = row0 + head;                   // global query row
-    if (head < nh) {
-        float acc[C::E], M, L;
-        combine_warps<C>(red, head, d0, FP8 ? __ldg(p.v_scale + kvh) : 1.f, acc, M, L);
-        if (nsplit == 1) {
-            if constexpr (SUFFIX) {
-                RowPieces<D> pc;
-                if (group >= 0) pc.find(sp.shared, group, b, kvh, hg * NT + head);
-                if (pc.n > 0) {
-                    float top = L > 0.f ? M : -INFINITY;
-                    for (int e = 0; e < pc.n; ++e) {
-                        const float2 v = pc.ml(e);
-                        if (v.y > 0.f) top = fmaxf(top, v.x);
-                    }
-                    float W = L > 0.f ? L * fast_exp2(M - top) : 0.f;
+            const int row = nt * 8 + 2 * (lane & 3) + j;
+            if (row < a || row >= b) continue;
+            const float s = lse[(row - a) * 4];
+            if (!(s > -INFINITY)) continue;
+            const float m = fmaxf(st.m[nt][j], s);
+            const float f = fast_exp2(st.m[nt][j] - m), w = fast_exp2(s - m);
+            st.m[nt][j] = m;
+            st.l[nt][j] = st.l[nt][j] * f + (r == 0 ? w : 0.f);     // the lanes' sums are added up at the end
+            const float g = w * out_scale;
+            const float* x = o + (row - a) * D + (FP8 ? 16 * r : r);
 #pragma unroll
-                    for (int e = 0; e < C::E; ++e) acc[e] *= W;
-                    add_pieces<C, D>(pc, d0, top, acc, W);
-                    const float inv = W > 0.f ? 1.f / W : 0.f;
+            for (int ms = 0; ms < C::KS; ++ms)
 #pragma unroll
-                    for (int e = 0; e < C::E; ++e) acc[e] *= inv;
-                    M = top;
-                    L = W;
+                for (int hi = 0; hi < 2; ++hi) {
+                    float& y = st.o[ms][nt][2 * hi + j];
+                    y = y * f + g * x[FP8 ? 2 * ms + hi : 16 * ms + 8 * hi];
                 }
-            }
-            uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + bh * D + d0);
-#pragma unroll
-            for (int e = 0; e < C::E; e += 2) dst[e / 2] = pack_bf16x2(acc[e], acc[e + 1]);
-            if (p.lse != nullptr && d0 == 0) p.lse[bh] = lse_from(M, L);
-        } else {
-            float* dst = p.part_o + (bh * p.max_splits + split) * D + d0;
-#pragma unroll
-            for (int e = 0; e < C::E; ++e) dst[e] = acc[e];
-            if (d0 == 0) {
-                p.part_ml[(bh * p.max_splits + split) * 2 + 0] = M;
-                p.part_ml[(bh * p.max_splits + split) * 2 + 1] = L;
-            }
-            __threadfence();                        // partial visible before the ticket
         }
-    }
-    if (nsplit == 1) return;
-
-    // ---- ticket: the last chunk of this unit to finish merges all chunks
-    named_barrier_sync(1, C::NCW * 32);
-    int* ticket = p.tickets + (static_cast<size_t>(b) * p.kv_heads + kvh) * p.head_groups + hg;
-    if (t == 0) {
-        const int last = atomicAdd(ticket, 1) == nsplit - 1;
-        if (last) __threadfence();
-        *merge_flag = last;
-    }
-    named_barrier_sync(1, C::NCW * 32);
-    if (!*merge_flag) return;
-    if (head < nh) {
-        const float* ml = p.part_ml + bh * p.max_splits * 2;
-        float M = -INFINITY;
-        RowPieces<D> pc;
-        if constexpr (SUFFIX) {
-            if (group >= 0) pc.find(sp.shared, group, b, kvh, hg * NT + head);
-            for (int e = 0; e < pc.n; ++e) {
-                const float2 v = pc.ml(e);
-                if (v.y > 0.f) M = fmaxf(M, v.x);
-            }
-        }
-        for (int j = 0; j < nsplit; ++j) {
-            if (__ldcg(ml + 2 * j + 1) > 0.f) M = fmaxf(M, __ldcg(ml + 2 * j));
-        }
-        float acc[C::E];
-#pragma unroll
-        for (int e = 0; e < C::E; ++e) acc[e] = 0.f;
-        float W = 0.f;
-        const float* ob = p.part_o + bh * p.max_splits * D + d0;
-        for (int j = 0; j < nsplit; ++j) {
-            const float lj = __ldcg(ml + 2 * j + 1);
-            if (!(lj > 0.f)) continue;               // a chunk this row sees nothing of
-            const float wj = lj * fast_exp2(__ldcg(ml + 2 * j) - M);
-            W += wj;
-            const float* oj = ob + static_cast<size_t>(j) * D;
-#pragma unroll
-            for (int e = 0; e < C::E; e += 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(oj + e));
-                acc[e] += wj * v.x;
-                acc[e + 1] += wj * v.y;
-                acc[e + 2] += wj * v.z;
-                acc[e + 3] += wj * v.w;
-            }
-        }
-        if constexpr (SUFFIX) add_pieces<C, D>(pc, d0, M, acc, W);
-        const float inv = W > 0.f ? 1.f / W : 0.f;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + bh * D + d0);
-#pragma unroll
-        for (int e = 0; e < C::E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-        if (p.lse != nullptr && d0 == 0) p.lse[bh] = lse_from(M, W);
-    }
-    if (t == 0) *ticket = 0;                        // ready for the next call
 }
 
-template <bool FP8, int D, int BS, int NT>
+template <bool FP8, int D, int NT, int HC>
+struct SpanCfg : DecodeCfg<FP8, D, SPAN_TOK, NT> {
+    using C = DecodeCfg<FP8, D, SPAN_TOK, NT>;
+    static constexpr int NCW = 4;                   // consumer warps
+    static constexpr int WPH = NCW / HC;            // of one kv head
+    static constexpr int THREADS = (NCW + 1) * 32;
+    static constexpr int MINB = SPAN_CTAS;          // CTAs per SM
+    static constexpr int HSTAGE = HC * C::STAGE;    // K tiles of the heads, then V tiles; or the query
+                                                    // rows of the heads; or a piece's rows of each head
+    static constexpr int RPS = C::STAGE / (D * 4) < NT ? C::STAGE / (D * 4) : NT;   // rows of a piece stage
+    static constexpr int LSE = HC * RPS * 16;       // and their log-sum-exps, 16 bytes a row
+    static constexpr int CTL = 2048;                // barriers, items
+    static constexpr int BUDGET = 228 * 1024 / MINB - 1024 /* reserved */ - 1024 /* alignment */ - CTL;
+    static constexpr int NST = BUDGET / (HSTAGE + LSE) < 16 ? BUDGET / (HSTAGE + LSE) : 16;
+    static constexpr int SMEM = 1024 + NST * (HSTAGE + LSE) + CTL;
+    static constexpr int QUEUE = 8;                 // items handed on ahead
+    static constexpr int REGS4 = C::KS * C::NTT;    // groups of four accumulators of a thread
+    static_assert(NST >= 3 && SMEM <= 227 * 1024, "a ring of three stages at least");
+};
+
+template <bool FP8, int D, int NT, int HC, int RULE>
+__global__ void __launch_bounds__(SpanCfg<FP8, D, NT, HC>::THREADS, SpanCfg<FP8, D, NT, HC>::MINB)
+paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                  const SpanParams sp)
+{
+    using C = DecodeCfg<FP8, D, SPAN_TOK, NT>;
+    using S = SpanCfg<FP8, D, NT, HC>;
+    constexpr int NST = S::NST, THREADS = S::THREADS, NCW = S::NCW, WPH = S::WPH, QUEUE = S::QUEUE;
+    constexpr bool SUFFIX = RULE == SPAN_SUFFIX;
+    const DecodeParams& p = sp.d;
+    struct Ctl {
+        uint64_t full[NST], empty[NST];
+        uint64_t item_full[QUEUE], item_empty[QUEUE];
+        SpanRange range;
+        long long scan[THREADS / 32];
+        int tag[NST];                                // what the stage holds
+        SpanItem<RULE> queue[QUEUE];
+    };
+    static_assert(sizeof(Ctl) <= S::CTL, "control block");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* lse_sm = smem + NST * S::HSTAGE;
+    Ctl* ctl = reinterpret_cast<Ctl*>(lse_sm + NST * S::LSE);
+
+    const int tid = threadIdx.x;
+    const int warp = tid >> 5;
+    const int lane = tid & 31;
+    const int r = lane >> 2, c = lane & 3;           // accumulator row and column pair of the lane
+
+    if (tid == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(smem_u32(&ctl->full[i]), 1);
+            mbar_init(smem_u32(&ctl->empty[i]), NCW);
+        }
+        for (int i = 0; i < QUEUE; ++i) {
+            mbar_init(smem_u32(&ctl->item_full[i]), 1);
+            mbar_init(smem_u32(&ctl->item_empty[i]), NCW);
+        }
+        fence_mbar_init();
+        prefetch_tensormap(&tmk);
+        prefetch_tensormap(&tmv);
+    }
+    grid_dependency_wait();                          // inputs of the preceding kernel are ready
+    grid_dependents_launch();                        // this grid is resident: the next may launch
+
+    // ---- this CTA's range: the positions of all sequences, then the one it begins in.  A round
+    // takes one sequence per thread; more than THREADS of them are gone through twice.
+    long long total = 0;
+    int ranges;
+    {
+        const auto positions = [&](int b) {
+            long long w = 0;
+            if (b < p.batch) {
+                SpanSeq<RULE> s;
+                s.load(sp, b, blockIdx.x == 0);
+                int sub;
+                for (int t = 0; t < p.head_groups; ++t) w += s.tile_subs(sp, t, NT, sub) + SPAN_PAD;
+                w *= p.kv_heads / HC;
+            }
+            return w;
+        };
+        long long w = 0, sum = 0;
+        for (int b = tid; b < p.batch; b += THREADS) sum += w = positions(b);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
+        if (lane == 0) ctl->scan[warp] = sum;
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < THREADS / 32; ++v) total += ctl->scan[v];
+        const long long most = (total + sp.least - 1) / sp.least;       // ranges of `least` positions or more
+        ranges = most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
+        const int k = blockIdx.x;
+        const long long lo = k < ranges ? total * k / ranges : total;
+        const long long hi = k < ranges ? total * (k + 1) / ranges : total;
+        long long before = 0;
+        for (int b0 = 0; lo < hi && b0 < p.batch && before <= lo; b0 += THREADS) {
+            if (p.batch > THREADS) w = positions(b0 + tid);
+            long long x = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(FULL_MASK, x, o);
+                if (lane >= o) x += y;
+            }
+            __syncthreads();                         // the sums before this round are read
+            if (lane == 31) ctl->scan[warp] = x;
+            __syncthreads();
+            long long base = before + x - w;
+#pragma unroll
+            for (int v = 0; v < THREADS / 32; ++v) {
+                if (v < warp) base += ctl->scan[v];
+                before += ctl->scan[v];
+            }
+            if (base <= lo && lo < base + w) {
+                ctl->range.base = base;
+                ctl->range.b0 = b0 + tid;
+            }
+        }
+        if (tid == 0) {
+            ctl->range.lo = lo;
+            ctl->range.hi = hi;
+        }
+        __syncthreads();
+    }
+
+    // ------------------------------------------------------------ producer warp
+    if (warp == NCW) {
+        SpanWalk<RULE, NT, HC> walk;
+        walk.init(sp, ctl->range, total, ranges);
+        const int per_block = sp.block_size / SPAN_TOK;                 // 1 or 2
+        // lane i < 2 HC loads the K (i < HC) or V tile of kv head kg * HC + i % HC
+        const int my_h = lane % HC;
+        const CUtensorMap* my_map = lane < HC ? &tmk : &tmv;
+        const uint32_t my_off = static_cast<uint32_t>((lane < HC ? 0 : HC * C::TILE) + my_h * C::TILE);
+        int ids = -1, ids_b = -1, ids_at = 0;        // table entries ids_at .. ids_at + 31 of sequence ids_b
+        int n = 0;                                   // stages issued
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            SpanItem<RULE> it;
+            const bool more = walk.next(sp, it);
+            if (!more) it.b = -1;
+            const int slot = k % QUEUE;
+            ok = all_ok(mbar_wait_bounded(smem_u32(&ctl->item_empty[slot]), (static_cast<uint32_t>(k / QUEUE) & 1u) ^ 1u));
+            if (!ok) break;
+            if (lane == 0) {
+                ctl->queue[slot] = it;
+                mbar_arrive(smem_u32(&ctl->item_full[slot]));
+            }
+            __syncwarp();
+            if (!more) break;
+            // arms the next stage (tag, bytes to land); false: no more stages
+            const auto arm = [&](int tag, uint32_t bytes) {
+                if (n == p.stop_stage) return false; // test hook: the rest never lands
+                const int st = n % NST;
+                if (!all_ok(mbar_wait_bounded(smem_u32(&ctl->empty[st]), (static_cast<uint32_t>(n / NST) & 1u) ^ 1u)))
+                    return false;
+                if (lane == 0) {
+                    ctl->tag[st] = tag;
+                    if (bytes > 0)
+                        mbar_arrive_expect_tx(smem_u32(&ctl->full[st]), bytes);
+                    else
+                        mbar_arrive(smem_u32(&ctl->full[st]));
+                }
+                __syncwarp();                        // armed before any of the stage's bytes can land
+                return true;
+            };
+            const auto stage = [&]() { return smem_u32(smem + n % NST * S::HSTAGE); };
+            const auto bar = [&]() { return smem_u32(&ctl->full[n % NST]); };
+
+            // the shared pass's pieces of the unit's rows: per segment, lane h of the first HC holds
+            // the first piece and the count of head h; the unit's first CTA takes them
+            constexpr int SEGS = 3;
+            const int nh = min(NT, p.rows - it.hg * NT);
+            PieceRows<NT, S::RPS> pr{0, 0};
+            int2 run[SEGS];
+            int pieces = 0;                          // stages of pieces
+            if (SUFFIX && it.seq.group >= 0 && it.split == 0) {
+                const PrefixGroup gr = load_prefix_group(sp.shared, it.seq.group);
+                const int pairs = prefix_pairs(sp.shared, gr);
+                const int base = prefix_run_base(sp.shared, it.seq.group, gr);
+                pr = PieceRows<NT, S::RPS>{(it.b - gr.off) * p.rows + it.hg * NT, nh};
+                int a = 0;
+#pragma unroll
+                for (int g = 0; g < SEGS; ++g) {
+                    run[g] = make_int2(0, 0);
+                    if (a < nh && lane < HC) {
+                        run[g] = __ldcg(sp.shared.runs + base + (it.kg * HC + lane) * pairs + (pr.row0 + a) / PFX_PAIR);
+                        // (a shared pass that gave up may have left this run's entry unwritten)
+                        if (run[g].x < 0 || run[g].y < 0 || run[g].x > sp.shared.pieces - run[g].y) run[g].y = 0;
+                    }
+                    if (a < nh) a = pr.end(a);
+                }
+            }
+            const auto count = [&](int g) {          // stages of segment g: the most any head has
+                int y = run[g].y;
+#pragma unroll
+                for (int o = HC / 2; o >= 1; o >>= 1) y = max(y, __shfl_xor_sync(FULL_MASK, y, o));
+                return __shfl_sync(FULL_MASK, y, 0);
+            };
+            const auto count_pieces = [&]() {
+                if (SUFFIX && pr.nh > 0) {
+#pragma unroll
+                    for (int g = 0; g < SEGS; ++g) pieces += count(g);
+                }
+            };
+
+            // ---- the query rows
+            if (it.n == 0) count_pieces();
+            ok = arm(TAG_Q | (it.n == 0 && pieces == 0 ? TAG_LAST : 0), static_cast<uint32_t>(HC * nh * D * 2));
+            if (!ok) break;
+            if (lane < HC) {
+                const size_t row = (static_cast<size_t>(it.b) * p.kv_heads + it.kg * HC + lane) * p.rows + it.hg * NT;
+                bulk_load(stage() + lane * (NT * D * 2), p.q + row * D, static_cast<uint32_t>(nh * D * 2), bar());
+            }
+            ++n;
+            // ---- the sub-blocks
+            for (int i = 0; i < it.n; ++i) {
+                const int sub = it.sub0 + i;
+                const int entry = per_block == 2 ? sub >> 1 : sub;
+                if (ids_b != it.b || entry < ids_at || entry >= ids_at + 32) {
+                    ids_b = it.b;
+                    ids_at = entry;
+                    const int j = entry + lane;
+                    ids = j < p.max_blocks ? __ldg(p.tables + static_cast<size_t>(it.b) * p.max_blocks + j) : -1;
+                }
+                const int blk = __shfl_sync(FULL_MASK, ids, entry - ids_at);
+                const bool good = blk >= 0 && blk < p.num_blocks;
+                if (!good && lane == 0) atomicOr(p.err, KV_DEVERR_BLOCK_ID);    // skipped: never addressed
+                if (i + 1 == it.n) count_pieces();
+                ok = arm((good ? TAG_KV : TAG_SKIP) | (i + 1 == it.n && pieces == 0 ? TAG_LAST : 0),
+                         good ? static_cast<uint32_t>(S::HSTAGE) : 0u);
+                if (!ok) break;
+                if (good && lane < 2 * HC)
+                    tma_load_5d(stage() + my_off, my_map, 0, 0, it.kg * HC + my_h,
+                                per_block == 2 ? (sub & 1) * SPAN_TOK : 0, blk, bar());
+                ++n;
+            }
+            if (!ok || pieces == 0) continue;
+            // ---- the pieces
+            int a = 0, done = 0;
+#pragma unroll
+            for (int g = 0; g < SEGS; ++g) {
+                if (a >= nh || !ok) continue;
+                const int e1 = pr.end(a), most = count(g);
+                const int slot_rows = (pr.row0 + a) % PFX_PAIR;
+                for (int e = 0; e < most; ++e) {
+                    const uint32_t have = __ballot_sync(FULL_MASK, lane < HC && e < run[g].y);
+                    const uint32_t rows = static_cast<uint32_t>(e1 - a);
+                    ok = arm(TAG_PIECE | (a << 8) | (e1 << 16) | static_cast<int>(have << 24) | (++done == pieces ? TAG_LAST : 0),
+                             static_cast<uint32_t>(__popc(have)) * rows * (D * 4 + 16));
+                    if (!ok) break;
+                    if (have >> lane & 1u) {
+                        const size_t at = static_cast<size_t>(run[g].x + e) * PFX_PAIR + slot_rows;
+                        bulk_load(stage() + lane * C::STAGE, sp.shared.piece_o + at * D, rows * (D * 4), bar());
+                        bulk_load(smem_u32(lse_sm + n % NST * S::LSE) + lane * (S::RPS * 16), sp.shared.piece_lse + at,
+                                  rows * 16, bar());
+                    }
+                    ++n;
+                }
+                a = e1;
+            }
+        }
+        if (!ok && lane == 0 && n != p.stop_stage) atomicOr(p.err, KV_DEVERR_TIMEOUT);
+        // Drain: the CTA must not exit while a copy into its shared memory is in flight.
+        for (int i = max(0, n - NST); i < n; ++i)
+            if (!mbar_wait_bounded(smem_u32(&ctl->full[i % NST]), static_cast<uint32_t>(i / NST) & 1u)) break;
+        return;
+    }
+
+    // ------------------------------------------------------------ consumer warps
+    const unsigned long long wait_ns = p.consumer_wait_ns ? p.consumer_wait_ns : WAIT_LIMIT_NS;
+    const int h = warp / WPH;                        // head of the group
+    int taken = 0;                                   // stages of the items before
+    bool ok = true;
+    for (int k = 0;; ++k) {
+        ok = all_ok(mbar_wait_bounded(smem_u32(&ctl->item_full[k % QUEUE]), static_cast<uint32_t>(k / QUEUE) & 1u));
+        if (!ok) break;
+        const SpanItem<RULE> it = ctl->queue[k % QUEUE];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->item_empty[k % QUEUE]));
+        if (it.b < 0) break;
+        const int b = it.b, kvh = it.kg * HC + h;
+        const int nh = min(NT, p.rows - it.hg * NT);                    // real rows in this tile
+        const size_t row0 = (static_cast<size_t>(b) * p.kv_heads + kvh) * p.rows + it.hg * NT;
+        uint32_t qf[C::KS][C::NTT][2];
+        SpanRows<C::NTT, RULE> rows;
+        rows.cap_in = sp.cap_in;
+        rows.cap_log2 = sp.cap_log2;
+        it.seq.tile_keys(sp, it.hg, NT, rows.tile_lo, rows.tile_hi);
+#pragma unroll
+        for (int nt = 0; nt < C::NTT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int local = nt * 8 + 2 * c + j;
+                const int rr = it.hg * NT + local;
+                const int head = rr / p.q_len, i = rr - head * p.q_len;
+                rows.lo[nt][j] = it.seq.key_lo(sp, i);
+                rows.hi[nt][j] = local < nh ? it.seq.key_hi(sp, i) : 0;        // padding rows see nothing
+                rows.pos[nt][j] = it.seq.ctx - p.q_len + i;
+                rows.slope[nt][j] = rows.BIAS && local < nh
+                                        ? __ldg(sp.slopes + kvh * p.group + head) * 1.4426950408889634f
+                                        : 0.f;
+            }
+        WarpState<C> st;
+        reset_state(st);
+        // every warp waits for every stage in order, also for those that another warp of its head
+        // folds: a wait by parity is only unambiguous for the next phase
+        int sub = it.sub0, turn = 0;
+        for (bool last = false; !last; ++taken) {
+            const int s = taken % NST;
+            ok = all_ok(mbar_wait_bounded(smem_u32(&ctl->full[s]), static_cast<uint32_t>(taken / NST) & 1u, wait_ns));
+            if (!ok) break;
+            const int tag = ctl->tag[s];
+            const uint8_t* st_sm = smem + s * S::HSTAGE;
+            last = tag & TAG_LAST;
+            if ((tag & 3) == TAG_Q) {
+                rows.sl2 = load_q_frags<FP8, D, SPAN_TOK, NT>(
+                    qf, reinterpret_cast<const uint16_t*>(st_sm + h * (NT * D * 2)), nh, lane, p.scale_log2, p.k_scale, kvh);
+            } else {
+                const bool mine = WPH == 1 || turn % WPH == warp % WPH;
+                ++turn;
+                if ((tag & 3) == TAG_KV && mine) {
+                    const uint32_t tk = smem_u32(st_sm) + h * C::TILE;
+                    rows.base = sub * SPAN_TOK;
+                    process_block_rows<FP8, D, SPAN_TOK, NT>(tk, tk + HC * C::TILE, rows, qf, st, lane);
+                }
+                if (SUFFIX && (tag & 3) == TAG_PIECE && mine && (tag >> (24 + h) & 1))
+                    fold_piece<FP8, D, NT>(reinterpret_cast<const float*>(st_sm + h * C::STAGE),
+                                           reinterpret_cast<const float*>(lse_sm + s * S::LSE + h * (S::RPS * 16)),
+                                           tag >> 8 & 0xff, tag >> 16 & 0xff,
+                                           FP8 ? 1.f / __ldg(p.v_scale + kvh) : 1.f, st, lane);
+                ++sub;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->empty[s]));
+        }
+        if (!ok) break;
+
+        // -------------------------------------------------------- the unit's end
+        reduce_row_sums(st);
+        const int parts = it.nsplit * WPH;           // warps that hold parts of these rows
+        if (parts > 1) {
+            // part e of the head: warp e % WPH of the unit's piece e / WPH
+            const size_t part0 = (static_cast<size_t>(it.range0) + it.unit) * NCW + h * WPH;
+            const auto part = [&](int e) { return part0 + e / WPH * NCW + e % WPH; };
+            const size_t own = part(it.split * WPH + warp % WPH);
+            float4* mine = reinterpret_cast<float4*>(p.part_o) + own * (S::REGS4 * 32) + lane;
+#pragma unroll
+            for (int ms = 0; ms < C::KS; ++ms)
+#pragma unroll
+                for (int nt = 0; nt < C::NTT; ++nt)
+                    mine[(ms * C::NTT + nt) * 32] =
+                        make_float4(st.o[ms][nt][0], st.o[ms][nt][1], st.o[ms][nt][2], st.o[ms][nt][3]);
+            float2* ml = reinterpret_cast<float2*>(p.part_ml);
+            if (r == 0) {
+#pragma unroll
+                for (int nt = 0; nt < C::NTT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        ml[own * NT + nt * 8 + 2 * c + j] = make_float2(st.m[nt][j], st.l[nt][j]);
+            }
+            __threadfence();                         // partial visible before the ticket
+            __syncwarp();
+            int last = 0;
+            if (lane == 0) {
+                int* ticket = p.tickets + static_cast<size_t>(it.unit) * HC + h;
+                last = atomicAdd(ticket, 1) == parts - 1;
+                if (last) {
+                    *ticket = 0;                     // ready for the next call
+                    __threadfence();
+                }
+            }
+            last = __shfl_sync(FULL_MASK, last, 0);
+            if (!last) continue;
+            __threadfence();
+            // all partials in order (this warp's own among them), so the bits do not depend on
+            // which warp is last
+            reset_state(st);
+#pragma unroll 1
+            for (int e = 0; e < parts; ++e) {
+                const size_t at = part(e);
+                float f[C::NTT][2], g[C::NTT][2];
+#pragma unroll
+                for (int nt = 0; nt < C::NTT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float2 v = __ldcg(ml + at * NT + nt * 8 + 2 * c + j);
+                        const float m = v.y > 0.f ? fmaxf(st.m[nt][j], v.x) : st.m[nt][j];
+                        f[nt][j] = m > -INFINITY ? fast_exp2(st.m[nt][j] - m) : 1.f;
+                        g[nt][j] = v.y > 0.f ? fast_exp2(v.x - m) : 0.f;
+                        st.m[nt][j] = m;
+                        st.l[nt][j] = st.l[nt][j] * f[nt][j] + g[nt][j] * v.y;
+                    }
+                const float4* other = reinterpret_cast<const float4*>(p.part_o) + at * (S::REGS4 * 32) + lane;
+#pragma unroll
+                for (int ms = 0; ms < C::KS; ++ms)
+#pragma unroll
+                    for (int nt = 0; nt < C::NTT; ++nt) {
+                        const float4 x = __ldcg(other + (ms * C::NTT + nt) * 32);
+                        st.o[ms][nt][0] = st.o[ms][nt][0] * f[nt][0] + x.x * g[nt][0];
+                        st.o[ms][nt][1] = st.o[ms][nt][1] * f[nt][1] + x.y * g[nt][1];
+                        st.o[ms][nt][2] = st.o[ms][nt][2] * f[nt][0] + x.z * g[nt][0];
+                        st.o[ms][nt][3] = st.o[ms][nt][3] * f[nt][1] + x.w * g[nt][1];
+                    }
+            }
+        }
+        if constexpr (FP8) {
+            const float vs = __ldg(p.v_scale + kvh);
+#pragma unroll
+            for (int ms = 0; ms < C::KS; ++ms)
+#pragma unroll
+                for (int nt = 0; nt < C::NTT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) st.o[ms][nt][e] *= vs;
+        }
+        // ---- normalise and store
+#pragma unroll
+        for (int nt = 0; nt < C::NTT; ++nt) {
+            const float inv[2] = {st.l[nt][0] > 0.f ? 1.f / st.l[nt][0] : 0.f,
+                                  st.l[nt][1] > 0.f ? 1.f / st.l[nt][1] : 0.f};
+            const int mine = nt * 8 + 2 * c;         // the lane's two rows
+            if constexpr (FP8) {
+                // numbers 16 r .. 16 r + 15 of both rows
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int ms = 0; ms < C::KS; ++ms)
+                        w[ms] = pack_bf16x2(st.o[ms][nt][j] * inv[j], st.o[ms][nt][2 + j] * inv[j]);
+                    if (mine + j < nh) {
+                        uint4* dst = reinterpret_cast<uint4*>(p.out + (row0 + mine + j) * D + 16 * r);
+                        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
+                }
+            } else {
+                // numbers 16 ms + r and 16 ms + r + 8 of both rows: lanes r and r ^ 1 exchange, so
+                // that an even r holds a pair of the first row and an odd one of the second
+                const int row = mine + (r & 1);
+                uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (row0 + row) * D + (r & 6));
+#pragma unroll
+                for (int ms = 0; ms < C::KS; ++ms)
+#pragma unroll
+                    for (int hi = 0; hi < 2; ++hi) {
+                        const float a = st.o[ms][nt][2 * hi] * inv[0], d = st.o[ms][nt][2 * hi + 1] * inv[1];
+                        const float got = __shfl_xor_sync(FULL_MASK, r & 1 ? a : d, 4);
+                        const uint32_t w = r & 1 ? pack_bf16x2(got, d) : pack_bf16x2(a, got);
+                        if (row < nh) dst[ms * 8 + hi * 4] = w;
+                    }
+            }
+            if (p.lse != nullptr && r == 0) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (mine + j < nh) p.lse[row0 + mine + j] = lse_from(st.m[nt][j], st.l[nt][j]);
+            }
+        }
+    }
+    if (!ok && lane == 0) atomicOr(p.err, KV_DEVERR_TIMEOUT);
+}
+
+template <bool FP8, int D, int NT, int HC>
 cudaError_t prepare_span_variant()
 {
+    using S = SpanCfg<FP8, D, NT, HC>;
     const auto raise = [](auto kernel) {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    SpanCfg<FP8, D, BS, NT>::SMEM);
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     };
-    cudaError_t e = raise(paged_decode_span<FP8, D, BS, NT, SPAN_MASK>);
-    if (e == cudaSuccess) e = raise(paged_decode_span<FP8, D, BS, NT, SPAN_CAP>);
-    if (e == cudaSuccess) e = raise(paged_decode_span<FP8, D, BS, NT, SPAN_BIAS>);
-    if (e == cudaSuccess) e = raise(paged_decode_span<FP8, D, BS, NT, SPAN_CAP_BIAS>);
-    if (e == cudaSuccess) e = raise(paged_decode_span<FP8, D, BS, NT, SPAN_SUFFIX>);
+    cudaError_t e = raise(paged_decode_span<FP8, D, NT, HC, SPAN_MASK>);
+    if (e == cudaSuccess) e = raise(paged_decode_span<FP8, D, NT, HC, SPAN_CAP>);
+    if (e == cudaSuccess) e = raise(paged_decode_span<FP8, D, NT, HC, SPAN_BIAS>);
+    if (e == cudaSuccess) e = raise(paged_decode_span<FP8, D, NT, HC, SPAN_CAP_BIAS>);
+    if (e == cudaSuccess) e = raise(paged_decode_span<FP8, D, NT, HC, SPAN_SUFFIX>);
     return e;
 }
 
-template <bool FP8, int D, int BS, int NT>
-cudaError_t launch_span_variant(SpanRule rule, dim3 grid, const CUtensorMap& tk, const CUtensorMap& tv,
+template <bool FP8, int D, int NT, int HC>
+cudaError_t launch_span_variant(SpanRule rule, int ctas, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const SpanParams& p, cudaStream_t s)
 {
+    using S = SpanCfg<FP8, D, NT, HC>;
     const auto go = [&](auto kernel) {
-        return launch_dependent(kernel, grid, dim3(DecodeCfg<FP8, D, BS, NT>::THREADS),
-                                SpanCfg<FP8, D, BS, NT>::SMEM, s, tk, tv, p);
+        return launch_dependent(kernel, dim3(static_cast<unsigned>(ctas)), dim3(S::THREADS), S::SMEM, s, tk, tv, p);
     };
     switch (rule) {
-    case SPAN_MASK: return go(paged_decode_span<FP8, D, BS, NT, SPAN_MASK>);
-    case SPAN_CAP: return go(paged_decode_span<FP8, D, BS, NT, SPAN_CAP>);
-    case SPAN_BIAS: return go(paged_decode_span<FP8, D, BS, NT, SPAN_BIAS>);
-    case SPAN_CAP_BIAS: return go(paged_decode_span<FP8, D, BS, NT, SPAN_CAP_BIAS>);
-    case SPAN_SUFFIX: return go(paged_decode_span<FP8, D, BS, NT, SPAN_SUFFIX>);
+    case SPAN_MASK: return go(paged_decode_span<FP8, D, NT, HC, SPAN_MASK>);
+    case SPAN_CAP: return go(paged_decode_span<FP8, D, NT, HC, SPAN_CAP>);
+    case SPAN_BIAS: return go(paged_decode_span<FP8, D, NT, HC, SPAN_BIAS>);
+    case SPAN_CAP_BIAS: return go(paged_decode_span<FP8, D, NT, HC, SPAN_CAP_BIAS>);
+    case SPAN_SUFFIX: return go(paged_decode_span<FP8, D, NT, HC, SPAN_SUFFIX>);
     }
     return cudaErrorInvalidValue;
 }

@@ -3,25 +3,24 @@
 
 namespace kvp {
 
-#define KVP_SPAN_FP8_VARIANTS(X) X(128, 16, 8) X(128, 16, 16) X(128, 32, 8) X(128, 32, 16)
+#define KVP_SPAN_FP8_VARIANTS(X) \
+    X(128, 8, 1) X(128, 8, 2) X(128, 8, 4) X(128, 16, 1) X(128, 16, 2) X(128, 16, 4)
 
-cudaError_t launch_span_fp8(SpanRule rule, int head_dim, int block_size, int head_tile, dim3 grid,
-                            const CUtensorMap& tk, const CUtensorMap& tv, const SpanParams& p,
-                            cudaStream_t s)
+cudaError_t launch_span_fp8(SpanRule rule, int head_dim, int head_tile, int heads, int ctas, const CUtensorMap& tk,
+                             const CUtensorMap& tv, const SpanParams& p, cudaStream_t s)
 {
-#define KVP_CASE(D_, BS_, NT_) \
-    if (head_dim == D_ && block_size == BS_ && head_tile == NT_) \
-        return launch_span_variant<true, D_, BS_, NT_>(rule, grid, tk, tv, p, s);
+#define KVP_CASE(D_, NT_, HC_) \
+    if (head_dim == D_ && head_tile == NT_ && heads == HC_) \
+        return launch_span_variant<true, D_, NT_, HC_>(rule, ctas, tk, tv, p, s);
     KVP_SPAN_FP8_VARIANTS(KVP_CASE)
 #undef KVP_CASE
     return cudaErrorInvalidValue;
 }
 
-cudaError_t prepare_span_fp8(int head_dim, int block_size, int head_tile)
+cudaError_t prepare_span_fp8(int head_dim, int head_tile, int heads)
 {
-#define KVP_CASE(D_, BS_, NT_) \
-    if (head_dim == D_ && block_size == BS_ && head_tile == NT_) \
-        return prepare_span_variant<true, D_, BS_, NT_>();
+#define KVP_CASE(D_, NT_, HC_) \
+    if (head_dim == D_ && head_tile == NT_ && heads == HC_) return prepare_span_variant<true, D_, NT_, HC_>();
     KVP_SPAN_FP8_VARIANTS(KVP_CASE)
 #undef KVP_CASE
     return cudaErrorInvalidValue;

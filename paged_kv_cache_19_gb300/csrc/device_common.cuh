@@ -148,6 +148,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// Contiguous bulk load global -> shared (both 16-byte aligned, a multiple of 16 bytes), completion
+// counted in bytes on the mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 // L2 prefetch of `bytes` (a multiple of 16) contiguous bytes of global memory.
 __device__ __forceinline__ void prefetch_l2_bulk(const void* src, uint32_t bytes)
 {

@@ -62,9 +62,10 @@ struct PrefixParams {
     const int32_t* group_blocks;    // [n_groups]
     const float* k_scale;     // [kv_heads] (fp8 cache)
     const float* v_scale;
+    int2* seqs;               // [batch]: tokens of the sequence's shared part, its group
     int2* runs;               // per run slot: first piece, pieces
-    float2* piece_ml;         // [piece][2][128] (max, sum), log2 units
-    float* piece_o;           // [piece][2][head_dim / 4][128][4], normalised
+    float4* piece_lse;        // [piece][2][128]: log-sum-exp in log2 units (first of four), -inf: no key
+    float* piece_o;           // [piece][2][128][head_dim], normalised
     uint32_t* err;
     int batch, kv_heads, q_len, rows, max_blocks, num_blocks, n_groups;
     int pieces;               // pieces the workspace holds
@@ -84,7 +85,12 @@ cudaError_t launch_prefix(bool fp8, int head_dim, int block_size, int ctas, cons
 // Attention over a span of each sequence's keys (decode_span.cuh): the decode's parameters and
 // the rule of the rows.
 struct SpanParams {
+    // d.part_o [part][4 warps][head_tile * head_dim] in the accumulators' layout, d.part_ml
+    // [part][4 warps][head_tile][2]; d.tickets per (sequence, kv head, row tile); split_blocks,
+    // max_splits and merge_kernel are not used
     DecodeParams d;
+    int block_size;
+    int least;                // positions (16-token sub-blocks and SPAN_PAD per unit) of a range at least
     int window;               // keys a query sees back from its own position, itself included (0: all)
     float cap_log2, cap_in;   // score cap * log2(e) and 2 / cap; 0 without a cap
     const float* slopes;      // [q_heads] distance bias or null
@@ -92,6 +98,11 @@ struct SpanParams {
     const int32_t* prefix_lens;  // [batch] or null
     PrefixParams shared;      // the form behind a shared pass: its groups and partial results
 };
+// Positions that the span kernel's partition adds before each unit: what starting and finishing
+// a unit costs, in sub-blocks.
+constexpr int SPAN_PAD = 4;
+// Resident CTAs per SM of the span kernel.
+constexpr int SPAN_CTAS = 2;
 // The rule of the rows: a template argument of the span kernel.
 enum SpanRule { SPAN_MASK = 0, SPAN_CAP = 1, SPAN_BIAS = 2, SPAN_CAP_BIAS = 3, SPAN_SUFFIX = 4 };
 
@@ -212,14 +223,14 @@ cudaError_t launch_decode_bf16(int head_dim, int block_size, int head_tile, dim3
 cudaError_t launch_decode_fp8(int head_dim, int block_size, int head_tile, dim3 grid,
                               const CUtensorMap& tk, const CUtensorMap& tv,
                               const DecodeParams& p, cudaStream_t s);
-cudaError_t prepare_span_bf16(int head_dim, int block_size, int head_tile);
-cudaError_t prepare_span_fp8(int head_dim, int block_size, int head_tile);
-cudaError_t launch_span_bf16(SpanRule rule, int head_dim, int block_size, int head_tile, dim3 grid,
-                             const CUtensorMap& tk, const CUtensorMap& tv, const SpanParams& p,
-                             cudaStream_t s);
-cudaError_t launch_span_fp8(SpanRule rule, int head_dim, int block_size, int head_tile, dim3 grid,
-                            const CUtensorMap& tk, const CUtensorMap& tv, const SpanParams& p,
-                            cudaStream_t s);
+// The span kernel (decode_span.cuh), `heads` kv heads per CTA (1, 2 or 4); tk, tv: the pool's maps
+// with boxes of 16 slots.
+cudaError_t prepare_span_bf16(int head_dim, int head_tile, int heads);
+cudaError_t prepare_span_fp8(int head_dim, int head_tile, int heads);
+cudaError_t launch_span_bf16(SpanRule rule, int head_dim, int head_tile, int heads, int ctas, const CUtensorMap& tk,
+                             const CUtensorMap& tv, const SpanParams& p, cudaStream_t s);
+cudaError_t launch_span_fp8(SpanRule rule, int head_dim, int head_tile, int heads, int ctas, const CUtensorMap& tk,
+                            const CUtensorMap& tv, const SpanParams& p, cudaStream_t s);
 // The decode kernel with one CTA per group of `heads` kv heads (decode_heads.cuh), `ctas`
 // CTAs per SM; the variants built are listed in decode_heads.cu.
 bool decode_heads_supported(bool fp8, int head_dim, int block_size, int head_tile, int heads,

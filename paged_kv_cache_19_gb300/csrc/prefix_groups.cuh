@@ -53,8 +53,6 @@ __device__ __forceinline__ int prefix_run_base(const PrefixParams& p, int g, con
     return p.kv_heads * (gr.off * p.rows / PFX_PAIR + min(gr.off / 2, g));
 }
 
-// Numbers of a piece: [2 slots][D / 4][128 rows][4] fp32 outputs, [2 slots][128 rows] (max, sum).
-// A run of more than 128 rows has row tile s in slot s; one of fewer has the same rows in both
-// slots, each over every other token tile.
+// A piece has the rows of its run's pair in order (256 rows), whatever slots computed them.
 
 }  // namespace kvp

@@ -76,14 +76,15 @@ def test_matches_the_formula(shape, rule):
 
 
 def test_no_rule_is_the_plain_attention():
-    """Within rounding of paged_decode_attention and paged_attention_multi_query (bit for bit with
-    the same chunks: the arithmetic is the same)."""
+    """No mask at all and a mask that hides nothing: paged_attention_multi_query up to rounding."""
     for q_len in (1, 4):
         c = Cache(ctx=[50, 900, 4], hq=8, hk=2, d=128, bs=16, q_len=q_len)
-        out, lse = run(c, 128)
-        out2, lse2 = torch.empty_like(out), torch.empty_like(lse)
-        kp.paged_attention_multi_query(c.pool, c.q, c.tables, c.lens, c.scale, kv_split_tokens=128, out=out2, lse=lse2)
-        assert torch.equal(out, out2) and torch.equal(lse, lse2)
+        want = c.reference()
+        c.check(*run(c), want)
+        c.check(*run(c, window=10 ** 9, softcap=0.0, first_keys=i32([0, -3, 0]), prefix_lens=i32([0, 0, -1])), want)
+        out, lse = torch.empty_like(c.q), torch.empty(c.q.shape[:3], device="cuda")
+        kp.paged_attention_multi_query(c.pool, c.q, c.tables, c.lens, c.scale, out=out, lse=lse)
+        c.check(out, lse, want)
         c.pool.destroy()
 
 
@@ -192,6 +193,29 @@ def test_window_shrinks_the_workspace():
     c = Cache(ctx=[700], hq=8, hk=2, d=128, bs=16)
     size = lambda w: kp.paged_attention_masked_workspace_size(c.pool, 1, 8, 1, c.max_blocks, w, 16)  # noqa: E731
     assert size(17) < size(100) < size(0) == size(1 << 30) == size(44 * 16)
+    c.pool.destroy()
+
+
+def test_many_sequences():
+    """More sequences than a CTA has threads, most of them short or empty, and one long one."""
+    r = np.random.default_rng(2)
+    ctx = r.integers(0, 40, 700)
+    ctx[333] = 3000
+    c = Cache(ctx=ctx, hq=2, hk=1, d=64, bs=16)
+    c.check(*run(c, window=50), c.reference(hide(50)))
+    c.check(*run(c), c.reference())
+    assert c.pool.device_errors() == 0
+    c.pool.destroy()
+
+
+def test_repeated_calls_give_the_same_bits():
+    c = Cache(ctx=[3000, 17, 900], hq=8, hk=2, d=128, bs=16, q_len=3)
+    ws = torch.zeros(kp.paged_attention_masked_workspace_size(c.pool, 3, 8, 3, c.max_blocks, 0, 16), dtype=torch.uint8,
+                     device="cuda")
+    first = run(c, 16, workspace=ws)
+    for _ in range(20):
+        again = run(c, 16, workspace=ws)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
     c.pool.destroy()
 
 
