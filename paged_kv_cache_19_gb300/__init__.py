@@ -164,6 +164,28 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+# The handle of the current stream of a device without the Stream object around it, which costs
+# three microseconds of a call's ten.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+
+
+def _pool_stream(stream, pool) -> int | None:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(pool.device)
+    return _stream(stream)
+
+
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _at(t, dtype, n, name) -> int:
+    """Address of a contiguous CUDA tensor of n numbers."""
+    if t.dtype is not dtype or not t.is_contiguous() or not t.is_cuda or t.numel() != n:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} {dtype} numbers, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
+    return t.data_ptr()
+
+
 def _need(t, dtype, name):
     if t is None:
         return None
@@ -282,15 +304,15 @@ def paged_kv_append(pool: Pool, k_new, v_new, block_tables, context_lens=None, t
                                _ptr(context_lens), int(batch), _stream(stream)), "paged_kv_append")
 
 
-def _rows(t, heads, d, name):
-    """Token stride of a [tokens, heads, d] bf16 tensor whose token rows are contiguous."""
-    if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1:] != (heads, d):
-        raise ValueError(f"{name} must be a CUDA bf16 tensor [tokens, {heads}, {d}], got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    st = t.stride()
+def _rows(t, n, heads, d, name) -> int:
+    """Token stride of a [n, heads, d] bf16 tensor whose token rows are contiguous."""
+    shape, st = t.shape, t.stride()
+    if t.dtype is not _BF16 or not t.is_cuda or len(shape) != 3 or shape[0] != n or shape[1] != heads or shape[2] != d:
+        raise ValueError(f"{name} must be a CUDA bf16 tensor [{n}, {heads}, {d}], got "
+                         f"{t.dtype} {tuple(shape)} on {t.device}")
     if st[2] != 1 or (heads > 1 and st[1] != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {st}")
-    return st[0] if t.shape[0] > 1 else heads * d
+    return st[0] if n > 1 else heads * d
 
 
 def paged_norm_rope_append(pool: Pool, q, k, v, block_tables, context_lens=None, q_weight=None,
@@ -303,42 +325,29 @@ def paged_norm_rope_append(pool: Pool, q, k, v, block_tables, context_lens=None,
     q [T, Hq, d], k and v [T, Hkv, d]: bf16, rows of a token contiguous, any token stride (slices
     of one fused projection).  Tokens are addressed as in paged_kv_append, q_len per sequence.
     Returns the queries [T / q_len, Hq, q_len, d] ([T, Hq, d] for q_len 1 when out is not given)."""
-    lib = load_library()
-    n, heads = q.shape[0], q.shape[1]
-    d = pool.head_dim
-    qs, ks, vs = (_rows(q, heads, d, "q"), _rows(k, pool.kv_heads, d, "k"), _rows(v, pool.kv_heads, d, "v"))
-    if k.shape[0] != n or v.shape[0] != n:
-        raise ValueError("q, k and v must hold the same tokens")
-    _need(block_tables, torch.int32, "block_tables")
-    _need(context_lens, torch.int32, "context_lens")
-    _need(token_seq, torch.int32, "token_seq")
-    _need(token_pos, torch.int32, "token_pos")
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if _need(t, torch.float32, name) is not None and t.shape != (d,):
-            raise ValueError(f"{name} must have shape [{d}]")
-    _need(rope_table, torch.float32, "rope_table")
-    if rope_table is not None and rope_table.dim() != 2:
-        raise ValueError("rope_table must be [positions, rope_dim]")
+    lib = _lib or load_library()
+    n, heads, d = q.shape
+    kv = pool.kv_heads
+    qs, ks, vs = _rows(q, n, heads, pool.head_dim, "q"), _rows(k, n, kv, d, "k"), _rows(v, n, kv, d, "v")
     batch, max_blocks = block_tables.shape
-    for t, name in ((token_seq, "token_seq"), (token_pos, "token_pos")):
-        if t is not None and t.numel() != n:
-            raise ValueError(f"{name} must hold one entry per token")
-    if context_lens is not None and context_lens.numel() != batch:
-        raise ValueError("context_lens must hold one entry per sequence")
     if n % q_len:
         raise ValueError("the tokens must be q_len per sequence")
     if out is None:
-        shape = (n, heads, d) if q_len == 1 else (n // q_len, heads, q_len, d)
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
-    _need(out, torch.bfloat16, "out")
-    if out.numel() != n * heads * d:
-        raise ValueError("out does not hold the queries")
+        out = torch.empty((n, heads, d) if q_len == 1 else (n // q_len, heads, q_len, d), dtype=_BF16, device=q.device)
     positions, rope_dim = rope_table.shape if rope_table is not None else (0, 0)
-    _check(lib.paged_norm_rope_append(
-        pool.handle, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, heads, n, _ptr(q_weight),
-        _ptr(k_weight), float(eps), _ptr(rope_table), positions, rope_dim, int(interleaved),
-        _ptr(token_seq), _ptr(token_pos), block_tables.data_ptr(), max_blocks, _ptr(context_lens),
-        batch, int(q_len), out.data_ptr(), _stream(stream)), "paged_norm_rope_append")
+    status = lib.paged_norm_rope_append(
+        pool.handle, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, heads, n,
+        None if q_weight is None else _at(q_weight, _F32, d, "q_weight"),
+        None if k_weight is None else _at(k_weight, _F32, d, "k_weight"), eps,
+        None if rope_table is None else _at(rope_table, _F32, positions * rope_dim, "rope_table"),
+        positions, rope_dim, int(interleaved),
+        None if token_seq is None else _at(token_seq, _I32, n, "token_seq"),
+        None if token_pos is None else _at(token_pos, _I32, n, "token_pos"),
+        _at(block_tables, _I32, batch * max_blocks, "block_tables"), max_blocks,
+        None if context_lens is None else _at(context_lens, _I32, batch, "context_lens"), batch, q_len,
+        _at(out, _BF16, n * heads * d, "out"), _pool_stream(stream, pool))
+    if status:
+        raise KVError(status, "paged_norm_rope_append")
     return out
 
 
@@ -515,22 +524,26 @@ def paged_attention_masked_workspace_size(pool: Pool, batch: int, q_heads: int, 
     return n.value
 
 
-def _queries(pool, q, block_tables, context_lens, out, lse):
-    """Checks of an attention call over q [B, Hq, q_len, d] or [B, Hq, d]; (batch, heads, q_len)."""
-    _need(q, torch.bfloat16, "q")
-    _need(block_tables, torch.int32, "block_tables")
-    _need(context_lens, torch.int32, "context_lens")
-    _need(out, torch.bfloat16, "out")
-    _need(lse, torch.float32, "lse")
-    if q.dim() not in (3, 4) or q.shape[-1] != pool.head_dim:
-        raise ValueError(f"q must be [batch, q_heads, {pool.head_dim}] or [batch, q_heads, q_len, {pool.head_dim}]")
-    batch, heads = q.shape[0], q.shape[1]
-    q_len = q.shape[2] if q.dim() == 4 else 1
-    if block_tables.dim() != 2 or block_tables.shape[0] != batch or context_lens.numel() != batch:
-        raise ValueError("block_tables and context_lens must hold one row per sequence of q")
-    if out.numel() != q.numel() or (lse is not None and lse.numel() != batch * heads * q_len):
-        raise ValueError("out / lse sizes do not match q")
-    return batch, heads, q_len
+def _queries(pool, q, block_tables):
+    """Sizes of an attention call over q [B, Hq, q_len, d] or [B, Hq, d]: (batch, heads, q_len, blocks)."""
+    shape = q.shape
+    batch, max_blocks = block_tables.shape
+    if len(shape) not in (3, 4) or shape[-1] != pool.head_dim or shape[0] != batch:
+        raise ValueError(f"q must be [batch, q_heads, {pool.head_dim}] or [batch, q_heads, q_len, {pool.head_dim}] "
+                         f"and block_tables hold one row per sequence, got {tuple(shape)} and {tuple(block_tables.shape)}")
+    return batch, shape[1], shape[2] if len(shape) == 4 else 1, max_blocks
+
+
+def _workspace(workspace, need, q):
+    """Address and size of the caller's workspace, or of a zeroed one of need() bytes kept until
+    the call is enqueued (the caching allocator orders its reuse on the stream)."""
+    if workspace is None:
+        n = need()
+        workspace = torch.zeros(n, dtype=torch.uint8, device=q.device) if n else None
+        if workspace is None:
+            return None, 0, None
+    n = workspace.numel()
+    return _at(workspace, torch.uint8, n, "workspace"), n, workspace
 
 
 def paged_attention_masked(pool: Pool, q, block_tables, context_lens, scale: float,
@@ -541,27 +554,25 @@ def paged_attention_masked(pool: Pool, q, block_tables, context_lens, scale: flo
     softcap)), a sliding window, a bias by distance (alibi_slopes float32 [Hq]), a first visible
     key per sequence (first_keys int32 [B]) and a prefix every query sees (prefix_lens int32
     [B]); q bf16 [B, Hq, d] or [B, Hq, q_len, d].  Returns out (shaped like q)."""
-    lib = load_library()
+    lib = _lib or load_library()
+    batch, heads, q_len, max_blocks = _queries(pool, q, block_tables)
     if out is None:
         out = torch.empty_like(q)
-    batch, heads, q_len = _queries(pool, q, block_tables, context_lens, out, lse)
-    _need(alibi_slopes, torch.float32, "alibi_slopes")
-    if alibi_slopes is not None and alibi_slopes.numel() != heads:
-        raise ValueError("alibi_slopes must hold one slope per query head")
-    for t, name in ((first_keys, "first_keys"), (prefix_lens, "prefix_lens")):
-        if _need(t, torch.int32, name) is not None and t.numel() != batch:
-            raise ValueError(f"{name} must hold one position per sequence")
-    max_blocks = block_tables.shape[1]
-    if workspace is None:
-        need = paged_attention_masked_workspace_size(pool, batch, heads, q_len, max_blocks, window, kv_split_tokens)
-        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device) if need else None
-    _need(workspace, torch.uint8, "workspace")
-    mask = _AttentionMask(float(softcap), int(window), _ptr(alibi_slopes), _ptr(first_keys), _ptr(prefix_lens))
-    _check(lib.paged_attention_masked(
-        pool.handle, q.data_ptr(), heads, q_len, block_tables.data_ptr(), max_blocks,
-        context_lens.data_ptr(), batch, float(scale), ctypes.byref(mask), int(kv_split_tokens),
-        _ptr(workspace), 0 if workspace is None else workspace.numel(), out.data_ptr(), _ptr(lse),
-        _stream(stream)), "paged_attention_masked")
+    rows = batch * heads * q_len
+    ws, ws_bytes, keep = _workspace(workspace, lambda: paged_attention_masked_workspace_size(
+        pool, batch, heads, q_len, max_blocks, window, kv_split_tokens), q)
+    mask = _AttentionMask(softcap, window,
+                          None if alibi_slopes is None else _at(alibi_slopes, _F32, heads, "alibi_slopes"),
+                          None if first_keys is None else _at(first_keys, _I32, batch, "first_keys"),
+                          None if prefix_lens is None else _at(prefix_lens, _I32, batch, "prefix_lens"))
+    status = lib.paged_attention_masked(
+        pool.handle, _at(q, _BF16, rows * pool.head_dim, "q"), heads, q_len,
+        _at(block_tables, _I32, batch * max_blocks, "block_tables"), max_blocks,
+        _at(context_lens, _I32, batch, "context_lens"), batch, scale, mask, kv_split_tokens, ws, ws_bytes,
+        _at(out, _BF16, rows * pool.head_dim, "out"), None if lse is None else _at(lse, _F32, rows, "lse"),
+        _pool_stream(stream, pool))
+    if status:
+        raise KVError(status, "paged_attention_masked")
     return out
 
 
@@ -583,26 +594,23 @@ def paged_shared_prefix_attention(pool: Pool, q, block_tables, context_lens, gro
     is the sequences group_offsets[g] .. group_offsets[g + 1] - 1 (int32 [G + 1]) and shares the
     first group_blocks[g] entries of their tables (int32 [G]); BlockManager.prefix_groups makes
     both.  q bf16 [B, Hq, d] or [B, Hq, q_len, d].  Returns out (shaped like q)."""
-    lib = load_library()
+    lib = _lib or load_library()
+    batch, heads, q_len, max_blocks = _queries(pool, q, block_tables)
     if out is None:
         out = torch.empty_like(q)
-    batch, heads, q_len = _queries(pool, q, block_tables, context_lens, out, lse)
-    _need(group_offsets, torch.int32, "group_offsets")
-    _need(group_blocks, torch.int32, "group_blocks")
-    n_groups = group_blocks.numel()
-    if group_offsets.numel() != n_groups + 1:
-        raise ValueError("group_offsets must hold one entry more than group_blocks")
-    max_blocks = block_tables.shape[1]
-    if workspace is None:
-        need = paged_shared_prefix_workspace_size(pool, batch, heads, q_len, max_blocks, n_groups, kv_split_tokens)
-        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device) if need else None
-    _need(workspace, torch.uint8, "workspace")
-    _check(lib.paged_shared_prefix_attention(
-        pool.handle, q.data_ptr(), heads, q_len, block_tables.data_ptr(), max_blocks,
-        context_lens.data_ptr(), batch, group_offsets.data_ptr(), group_blocks.data_ptr(), n_groups,
-        float(scale), int(kv_split_tokens), _ptr(workspace),
-        0 if workspace is None else workspace.numel(), out.data_ptr(), _ptr(lse), _stream(stream)),
-        "paged_shared_prefix_attention")
+    rows = batch * heads * q_len
+    groups = group_blocks.numel()
+    ws, ws_bytes, keep = _workspace(workspace, lambda: paged_shared_prefix_workspace_size(
+        pool, batch, heads, q_len, max_blocks, groups, kv_split_tokens), q)
+    status = lib.paged_shared_prefix_attention(
+        pool.handle, _at(q, _BF16, rows * pool.head_dim, "q"), heads, q_len,
+        _at(block_tables, _I32, batch * max_blocks, "block_tables"), max_blocks,
+        _at(context_lens, _I32, batch, "context_lens"), batch,
+        _at(group_offsets, _I32, groups + 1, "group_offsets"), _at(group_blocks, _I32, groups, "group_blocks"), groups,
+        scale, kv_split_tokens, ws, ws_bytes, _at(out, _BF16, rows * pool.head_dim, "out"),
+        None if lse is None else _at(lse, _F32, rows, "lse"), _pool_stream(stream, pool))
+    if status:
+        raise KVError(status, "paged_shared_prefix_attention")
     return out
 
 

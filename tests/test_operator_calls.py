@@ -41,7 +41,9 @@ def test_a_null_pool_is_refused(lib):
 def test_host_tensors_are_refused():
     import torch
     with pytest.raises(ValueError):
-        kp._rows(torch.zeros(2, 4, 64, dtype=torch.bfloat16), 4, 64, "q")
+        kp._rows(torch.zeros(2, 4, 64, dtype=torch.bfloat16), 2, 4, 64, "q")
+    with pytest.raises(ValueError):
+        kp._at(torch.zeros(4, dtype=torch.int32), torch.int32, 4, "context_lens")
 
 
 def groups(bm, seqs, **kw):
