@@ -467,6 +467,7 @@ kv_status kv_pool_create(int num_blocks, int block_size, int kv_heads, int head_
             if (e != cudaSuccess) st = KV_ERR_CUDA;
         }
         if (kvp::prepare_decode_heads(fp8, head_dim, block_size) != cudaSuccess) st = KV_ERR_CUDA;
+        if (kvp::prepare_norm_rope_append(head_dim, fp8) != cudaSuccess) st = KV_ERR_CUDA;
         if (kvp::prepare_prefix(fp8, head_dim, block_size) != cudaSuccess) st = KV_ERR_CUDA;
     }
     if (st == KV_OK && cudaDeviceSynchronize() != cudaSuccess) st = KV_ERR_CUDA;
@@ -660,7 +661,7 @@ kv_status paged_norm_rope_append(kv_pool* pool, const void* q, int64_t q_stride,
     p.block_size = pool->block_size;
     p.q_len = q_len;
     p.chunks = 0;
-    return kvp::launch_norm_rope_append(p, pool->head_dim, pool->dtype == KV_DTYPE_FP8_E4M3,
+    return kvp::launch_norm_rope_append(p, pool->head_dim, pool->dtype == KV_DTYPE_FP8_E4M3, pool->num_sms,
                                         static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? KV_OK
                : KV_ERR_CUDA;

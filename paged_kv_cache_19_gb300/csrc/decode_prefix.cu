@@ -95,6 +95,13 @@ struct PfxItem {
     bool both;              // the slots take alternate tiles of the same rows
 };
 
+// a / b for non-negative values; in 32 bits where they fit.
+__device__ __forceinline__ long long pfx_div(long long a, long long b)
+{
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // The items of a CTA's range, walked by every role on its own (uniform in a warp).
 struct PfxWalk {
     long long u, hi, base, units;
@@ -125,7 +132,7 @@ struct PfxWalk {
             load(p, block_size);
         }
         const long long rel = u - base;
-        const int run = static_cast<int>(rel / tiles);
+        const int run = static_cast<int>(pfx_div(rel, tiles));
         it.tile0 = static_cast<int>(rel - static_cast<long long>(run) * tiles);
         const long long left = hi - u;
         it.n = left < tiles - it.tile0 ? static_cast<int>(left) : tiles - it.tile0;
@@ -145,7 +152,7 @@ struct PfxWalk {
 // The CTA that holds unit u of `units` cut into ranges for n CTAs.
 __device__ __forceinline__ int pfx_cta_of(long long u, long long units, int n)
 {
-    return static_cast<int>(((u + 1) * n - 1) / units);
+    return static_cast<int>(pfx_div((u + 1) * n - 1, units));
 }
 
 __device__ __forceinline__ bool pfx_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag)
@@ -157,6 +164,35 @@ __device__ __forceinline__ bool pfx_wait(uint32_t bar, uint32_t parity, volatile
         if ((i & 63u) == 0 && (*abort_flag || global_timer_ns() - t0 > WAIT_LIMIT_NS)) return false;
     }
 }
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+    return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return d;
+}
+
+__device__ __forceinline__ void tc_ld(uint32_t taddr, uint32_t (&r)[64]) { tc_ld64(taddr, r); }
+__device__ __forceinline__ void tc_ld(uint32_t taddr, uint32_t (&r)[128]) { tc_ld128(taddr, r); }
 
 // Eight floats, one 32-byte sector.
 __device__ __forceinline__ void store_sector(float* dst, const float* x)
@@ -255,8 +291,8 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             if (b < in0 || b >= in1) p.seqs[b] = make_int2(0, -1);
         const int ctas = units < gridDim.x ? static_cast<int>(units) : static_cast<int>(gridDim.x);
         const int c = blockIdx.x;
-        const long long lo = c < ctas ? units * c / ctas : 0;
-        const long long hi = c < ctas ? units * (c + 1) / ctas : 0;
+        const long long lo = c < ctas ? pfx_div(units * c, ctas) : 0;
+        const long long hi = c < ctas ? pfx_div(units * (c + 1), ctas) : 0;
         if (tid == 0) {
             ctl->units = units;
             ctl->ctas = ctas;
@@ -541,29 +577,44 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 tc_fence_after();
                 const uint32_t held = ctl->masks[(kt + i) % PFX_MASKS];
                 const int nvis = lim - (it.tile0 + i) * PFX_TILE;         // visible tokens of the tile
-                const bool whole = __all_sync(FULL_MASK, nvis >= PFX_TILE) && held == (1u << C::BLOCKS) - 1u;
-                const float mult = mult0;
-                // maximum of the scaled scores
-                float mx = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t a[32], b[32];
-                    tc_ld32(tm_s + c * 64, a);
-                    tc_ld32(tm_s + c * 64 + 32, b);
-                    tc_wait_ld();
-                    if (whole) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            mx = fmaxf(mx, fmaxf(__uint_as_float(a[j]) * mult, __uint_as_float(b[j]) * mult));
-                    } else {
+                float mult = mult0;
+                // A tile with hidden tokens (or a factor that turns the order round) is scaled and
+                // masked in place first, so that the loop below has one form.
+                if (!__all_sync(FULL_MASK, nvis >= PFX_TILE && mult0 >= 0.f) || held != (1u << C::BLOCKS) - 1u) {
+#pragma unroll 1
+                    for (int c = 0; c < PFX_TILE; c += 32) {
+                        uint32_t r[32];
+                        tc_ld32(tm_s + c, r);
+                        tc_wait_ld();
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
-                            const int ta = c * 64 + j, tb = ta + 32;
-                            if (ta < nvis && (held >> (ta / BS) & 1u)) mx = fmaxf(mx, __uint_as_float(a[j]) * mult);
-                            if (tb < nvis && (held >> (tb / BS) & 1u)) mx = fmaxf(mx, __uint_as_float(b[j]) * mult);
+                            const bool seen_by = c + j < nvis && (held >> ((c + j) / BS) & 1u);
+                            r[j] = __float_as_uint(seen_by ? __uint_as_float(r[j]) * mult0 : -INFINITY);
                         }
+                        tc_st32(tm_s + c, r);
                     }
+                    tc_wait_st();
+                    mult = 1.f;
                 }
+                // The row's scores: all in registers, or (8-bit cache: more threads per CTA) read twice.
+                constexpr int COLS = FP8 ? 64 : PFX_TILE;
+                uint32_t x[COLS];
+                float mx = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < PFX_TILE; c += COLS) {
+                    tc_ld(tm_s + c, x);
+                    tc_wait_ld();
+                    float m4[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) m4[j] = max3(__uint_as_float(x[j]), __uint_as_float(x[j + 4]), mx);
+#pragma unroll
+                    for (int j = 8; j < COLS; j += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            m4[e] = max3(m4[e], __uint_as_float(x[j + e]), __uint_as_float(x[j + 4 + e]));
+                    mx = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
+                }
+                mx *= mult;
                 float f = 1.f;
                 if (m_ref == -INFINITY) {
                     m_ref = mx;                     // nothing accumulated yet
@@ -587,37 +638,34 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     tc_wait_st();
                 }
                 const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-                float ls[4] = {0.f, 0.f, 0.f, 0.f};
+                const float2 mul2 = make_float2(mult, mult), sub2 = make_float2(-m_use, -m_use);
+                float2 ls[4];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    // probabilities over the scores they come from: 64 tokens become 32 columns,
-                    // all of which have been read by then
-                    uint32_t a[32], b[32], pk[32];
-                    tc_ld32(tm_s + c * 64, a);
-                    tc_ld32(tm_s + c * 64 + 32, b);
-                    tc_wait_ld();
-                    float x[64];
+                for (int j = 0; j < 4; ++j) ls[j] = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        x[j] = fmaf(__uint_as_float(a[j]), mult, -m_use);
-                        x[j + 32] = fmaf(__uint_as_float(b[j]), mult, -m_use);
+                for (int c = 0; c < PFX_TILE; c += COLS) {
+                    if (COLS < PFX_TILE) {
+                        tc_ld(tm_s + c, x);
+                        tc_wait_ld();
                     }
-                    if (!whole) {
+                    // probabilities over the scores they come from: 64 tokens become 32 columns, all
+                    // of which have been read by then
 #pragma unroll
-                        for (int j = 0; j < 64; ++j) {
-                            const int t = c * 64 + j;
-                            if (!(t < nvis && (held >> (t / BS) & 1u))) x[j] = -INFINITY;
+                    for (int h = 0; h < COLS; h += 64) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const float2 y = fma2(make_float2(__uint_as_float(x[h + 2 * j]), __uint_as_float(x[h + 2 * j + 1])),
+                                                  mul2, sub2);
+                            const float2 pr = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                            ls[j & 3] = add2(ls[j & 3], pr);
+                            pk[j] = FP8 ? pack_f16x2(pr.x, pr.y) : pack_bf16x2(pr.x, pr.y);
                         }
+                        tc_st32(tm_s + (c + h) / 2, pk);
                     }
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float p0 = fast_exp2(x[2 * j]), p1 = fast_exp2(x[2 * j + 1]);
-                        ls[j & 3] += p0 + p1;
-                        pk[j] = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-                    }
-                    tc_st32(tm_s + c * 32, pk);
                 }
-                l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                const float2 lt = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
+                l += lt.x + lt.y;
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();

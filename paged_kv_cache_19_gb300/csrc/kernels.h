@@ -250,7 +250,8 @@ cudaError_t launch_merge_attention_states(const uint16_t* outs, const float* lse
                                           long long rows, int head_dim, uint16_t* out,
                                           float* lse_out, cudaStream_t s);
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
-cudaError_t launch_norm_rope_append(const NormRopeParams& p, int head_dim, bool fp8, cudaStream_t s);
+cudaError_t prepare_norm_rope_append(int head_dim, bool fp8);
+cudaError_t launch_norm_rope_append(const NormRopeParams& p, int head_dim, bool fp8, int num_sms, cudaStream_t s);
 // Tokens per pipeline stage of the latent decode (0: block size not supported);
 // prod: the variant with a producer warp (small grids), else the three-CTA one.
 int mla_stage_tokens(int block_size, bool prod);

@@ -12,13 +12,17 @@
 // quotient rounded to binary32 first, as paged_kv_append does -- a key is rounded once here,
 // where norm, rotation and append as separate passes round it two or three times.
 //
-// What it must move is each row once in and once out; there is nothing else to do per byte, so
-// it is bound by memory for a prompt and by latency for a decode step.  A row of D numbers
-// belongs to D / 8 lanes (one 16-byte vector each): the sum of squares is a shuffle reduction
-// inside those lanes, and the partner of a rotated number sits in the same lane (interleaved
-// pairs) or a fixed number of lanes away (half-split pairs).  A lane group takes RPT rows of one
-// token: their loads are in flight together, and the token's position, table entry and
-// cos/sin row are fetched once for all of them.
+// What it must move is each row once in and once out; there is little to do per byte, so a prompt is
+// bound by memory as long as the instructions per row are few, and a decode step by latency.  A row
+// of D numbers belongs to D / 8 lanes, and a lane holds the two groups of four numbers that rotate
+// with each other (half-split pairs: groups rope_dim / 2 apart; interleaved pairs, and numbers that
+// do not rotate: neighbours): the rotation needs no exchange between lanes, the sum of squares one
+// shuffle reduction, and most arithmetic runs two numbers at a time.  Two forms, by the number of
+// tokens (launch_nra_form):
+//   * direct: a lane group takes RPT rows of one token, their loads in flight together, and looks
+//     the token's place up itself;
+//   * streaming (prompts): see paged_norm_rope_append_stream.
+// NRA_FIGURES
 #include "append_row.cuh"
 #include "device_common.cuh"
 #include "kernels.h"
@@ -28,18 +32,165 @@ namespace kvp {
 namespace {
 
 constexpr int NRA_THREADS = 256;
+constexpr int NRA_STREAM_TOKENS = 2;                // tokens per CTA from which the streaming form is taken
 
-// Four pairs of e4m3 codes of y / scale, low element first (the arithmetic of e4m3_codes8).
-__device__ __forceinline__ uint2 e4m3_codes8f(const float (&y)[8], float scale)
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
 {
-    uint32_t c[2] = {0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float2 v = make_float2(__fdiv_rn(y[2 * e], scale), __fdiv_rn(y[2 * e + 1], scale));
-        const uint32_t two = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
-        c[e >> 1] |= (two & 0xffffu) << (16 * (e & 1));
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return d;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+    return d;
+}
+
+// Four e4m3 codes of y / scale, low element first (the arithmetic of e4m3_codes8).
+__device__ __forceinline__ uint32_t e4m3_codes4(float2 lo, float2 hi, float scale)
+{
+    const float2 a = make_float2(__fdiv_rn(lo.x, scale), __fdiv_rn(lo.y, scale));
+    const float2 b = make_float2(__fdiv_rn(hi.x, scale), __fdiv_rn(hi.y, scale));
+    return (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3)) & 0xffffu) |
+           (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3)) << 16);
+}
+
+__device__ __forceinline__ float2 bf16x2_floats(uint32_t w)
+{
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// Where a token goes.
+struct NraToken {
+    int b, t;                                       // its row block of q_out: sequence or token, query token
+    bool cached;                                    // its block id is valid
+    size_t slot;                                    // first row of its slot in the pool
+};
+
+// A lane's numbers of a row -- at[0] .. at[0] + 3 and at[1] .. at[1] + 3 -- and how they rotate.
+struct NraLane {
+    int at[2];
+    int pair;                                       // first of its four pairs in the table's row
+    bool turn;
+
+    __device__ __forceinline__ void init(const NormRopeParams& p, int l)
+    {
+        turn = 8 * l < p.rope_dim;                  // rope_dim 0: no rotation
+        const bool split = turn && !p.interleaved;
+        at[0] = split ? 4 * l : 8 * l;
+        at[1] = split ? 4 * l + p.rope_dim / 2 : 8 * l + 4;
+        pair = 4 * l;
     }
-    return make_uint2(c[0], c[1]);
+};
+
+// cos and sin of a lane's four pairs.
+struct NraTurn {
+    float2 c[2], s[2];
+    __device__ __forceinline__ void load(const NormRopeParams& p, const float* row, const NraLane& ln)
+    {
+        const float4 a = *reinterpret_cast<const float4*>(row + ln.pair);
+        const float4 b = *reinterpret_cast<const float4*>(row + p.rope_dim / 2 + ln.pair);
+        c[0] = make_float2(a.x, a.y), c[1] = make_float2(a.z, a.w);
+        s[0] = make_float2(b.x, b.y), s[1] = make_float2(b.z, b.w);
+    }
+};
+
+// One lane's numbers (x0: at[0] .., x1: at[1] ..) of row r of a token: norm, rotation, store.
+// Uniform in the row's lanes.
+template <int D, bool FP8>
+__device__ __forceinline__ void nra_row(const NormRopeParams& p, const NraToken& tok, const NraLane& ln, const NraTurn& w,
+                                        uint2 x0, uint2 x1, int r, unsigned group_mask)
+{
+    constexpr int LPR = D / 8;
+    const bool is_q = r < p.q_heads;
+    const bool is_v = r >= p.q_heads + p.kv_heads;
+    const int h = is_q ? r : is_v ? r - p.q_heads - p.kv_heads : r - p.q_heads;
+    float2 y[4];                                    // y[0], y[1]: the first four numbers
+    if (!is_v || FP8) {
+        y[0] = bf16x2_floats(x0.x), y[1] = bf16x2_floats(x0.y);
+        y[2] = bf16x2_floats(x1.x), y[3] = bf16x2_floats(x1.y);
+    }
+    if (!is_v) {
+        const float* weight = is_q ? p.q_weight : p.k_weight;
+        if (weight != nullptr) {
+            const float2 sq = fma2(y[0], y[0], fma2(y[1], y[1], fma2(y[2], y[2], mul2(y[3], y[3]))));
+            float ss = sq.x + sq.y;
+#pragma unroll
+            for (int o = LPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(group_mask, ss, o);
+            const float inv = rsqrtf(ss * (1.f / D) + p.eps);
+            const float4 g0 = __ldg(reinterpret_cast<const float4*>(weight + ln.at[0]));
+            const float4 g1 = __ldg(reinterpret_cast<const float4*>(weight + ln.at[1]));
+            const float2 inv2 = make_float2(inv, inv);
+            y[0] = mul2(mul2(y[0], inv2), make_float2(g0.x, g0.y));
+            y[1] = mul2(mul2(y[1], inv2), make_float2(g0.z, g0.w));
+            y[2] = mul2(mul2(y[2], inv2), make_float2(g1.x, g1.y));
+            y[3] = mul2(mul2(y[3], inv2), make_float2(g1.z, g1.w));
+        }
+        if (ln.turn) {
+            if (p.interleaved) {
+                // pairs (y[0].x, y[0].y), ..: gathered into first and second numbers and back
+                const float2 a0 = make_float2(y[0].x, y[1].x), b0 = make_float2(y[0].y, y[1].y);
+                const float2 a1 = make_float2(y[2].x, y[3].x), b1 = make_float2(y[2].y, y[3].y);
+                const float2 n0 = make_float2(-b0.x, -b0.y), n1 = make_float2(-b1.x, -b1.y);
+                const float2 p0 = fma2(a0, w.c[0], mul2(n0, w.s[0])), q0 = fma2(b0, w.c[0], mul2(a0, w.s[0]));
+                const float2 p1 = fma2(a1, w.c[1], mul2(n1, w.s[1])), q1 = fma2(b1, w.c[1], mul2(a1, w.s[1]));
+                y[0] = make_float2(p0.x, q0.x), y[1] = make_float2(p0.y, q0.y);
+                y[2] = make_float2(p1.x, q1.x), y[3] = make_float2(p1.y, q1.y);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float2 a = y[e], b = y[2 + e], n = make_float2(-b.x, -b.y);
+                    y[e] = fma2(a, w.c[e], mul2(n, w.s[e]));
+                    y[2 + e] = fma2(b, w.c[e], mul2(a, w.s[e]));
+                }
+            }
+        }
+    }
+    if (is_q || !FP8) {
+        uint16_t* dst;
+        if (is_q) {
+            dst = p.q_out + ((static_cast<size_t>(tok.b) * p.q_heads + h) * p.q_len + tok.t) * D;
+        } else {
+            if (!tok.cached) return;
+            dst = reinterpret_cast<uint16_t*>(is_v ? p.v_pool : p.k_pool) + (tok.slot + h) * D;
+        }
+        if (!is_v) {
+            x0 = make_uint2(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y));
+            x1 = make_uint2(pack_bf16x2(y[2].x, y[2].y), pack_bf16x2(y[3].x, y[3].y));
+        }
+        *reinterpret_cast<uint2*>(dst + ln.at[0]) = x0;
+        *reinterpret_cast<uint2*>(dst + ln.at[1]) = x1;
+    } else if (tok.cached) {
+        const float scale = __ldg((is_v ? p.v_scale : p.k_scale) + h);
+        uint8_t* dst = (is_v ? p.v_pool : p.k_pool) + (tok.slot + h) * D;
+        *reinterpret_cast<uint32_t*>(dst + ln.at[0]) = e4m3_codes4(y[0], y[1], scale);
+        *reinterpret_cast<uint32_t*>(dst + ln.at[1]) = e4m3_codes4(y[2], y[3], scale);
+    }
+}
+
+// Sequence and position of token i, checked; flag: this thread reports what is wrong.  False: the
+// token writes nothing.
+__device__ __forceinline__ bool nra_place(const NormRopeParams& p, uint32_t i, bool flag, int& seq, int& pos)
+{
+    seq = p.token_seq != nullptr ? __ldg(p.token_seq + i) : static_cast<int>(i / static_cast<uint32_t>(p.q_len));
+    if (seq < 0 || seq >= p.batch) {
+        if (flag) atomicOr(p.err, KV_DEVERR_SEQ);
+        return false;
+    }
+    pos = p.token_pos != nullptr ? __ldg(p.token_pos + i)
+                                 : __ldg(p.ctx + seq) - p.q_len + static_cast<int>(i % static_cast<uint32_t>(p.q_len));
+    if (pos < 0 || pos / p.block_size >= p.max_blocks || (p.rope != nullptr && pos >= p.rope_positions)) {
+        if (flag) atomicOr(p.err, KV_DEVERR_POSITION);
+        return false;
+    }
+    return true;
 }
 
 template <int D, bool FP8, int RPT>
@@ -59,130 +210,170 @@ __global__ void __launch_bounds__(NRA_THREADS) paged_norm_rope_append_kernel(con
     const unsigned group_mask = ((1u << LPR) - 1u) << (threadIdx.x % 32 / LPR * LPR);
     const int rows = p.q_heads + 2 * p.kv_heads;
 
-    uint4 x[RPT];
+    NraLane ln;
+    ln.init(p, l);
+    uint2 x0[RPT], x1[RPT];
 #pragma unroll
     for (int j = 0; j < RPT; ++j) {
         const int r = r0 + j;
-        x[j] = make_uint4(0u, 0u, 0u, 0u);
+        x0[j] = x1[j] = make_uint2(0u, 0u);
         if (r < rows) {
             const uint16_t* src =
                 r < p.q_heads ? p.q + i * p.q_stride + r * D
                 : r < p.q_heads + p.kv_heads ? p.k + i * p.k_stride + (r - p.q_heads) * D
                                              : p.v + i * p.v_stride + (r - p.q_heads - p.kv_heads) * D;
-            x[j] = __ldg(reinterpret_cast<const uint4*>(src) + l);
+            x0[j] = __ldg(reinterpret_cast<const uint2*>(src + ln.at[0]));
+            x1[j] = __ldg(reinterpret_cast<const uint2*>(src + ln.at[1]));
         }
     }
-
-    const int t = static_cast<int>(i % static_cast<uint32_t>(p.q_len));
-    const int b = static_cast<int>(i / static_cast<uint32_t>(p.q_len));
-    const int seq = p.token_seq != nullptr ? __ldg(p.token_seq + i) : b;
     const bool flag = r0 == 0 && l == 0;            // one lane of the token reports
-    if (seq < 0 || seq >= p.batch) {
-        if (flag) atomicOr(p.err, KV_DEVERR_SEQ);
-        return;
-    }
-    const int pos = p.token_pos != nullptr ? __ldg(p.token_pos + i) : __ldg(p.ctx + seq) - p.q_len + t;
-    if (pos < 0 || pos / p.block_size >= p.max_blocks || (p.rope != nullptr && pos >= p.rope_positions)) {
-        if (flag) atomicOr(p.err, KV_DEVERR_POSITION);
-        return;
-    }
+    int seq, pos;
+    if (!nra_place(p, i, flag, seq, pos)) return;
     const int blk = __ldg(p.tables + static_cast<size_t>(seq) * p.max_blocks + pos / p.block_size);
-    const bool cached = blk >= 0 && blk < p.num_blocks;
-    if (!cached && flag) atomicOr(p.err, KV_DEVERR_BLOCK_ID);   // its query row is still computed
-    const size_t slot = (static_cast<size_t>(cached ? blk : 0) * p.block_size + pos % p.block_size) * p.kv_heads;
-
-    // cos / sin of this lane's numbers (half-split: number 8l + e pairs with the one rope_dim / 2
-    // away and uses entry (8l + e) mod rope_dim / 2; interleaved: pair 4l + e / 2)
-    const int half = p.rope_dim / 2;
-    const bool turn = p.rope != nullptr && 8 * l < p.rope_dim && r0 < p.q_heads + p.kv_heads;
-    const bool upper = 8 * l >= half;
-    float cs[8], sn[8];
-    if (turn) {
-        const float* row = p.rope + static_cast<size_t>(pos) * p.rope_dim;
-        if (p.interleaved) {
-            const float4 c = __ldg(reinterpret_cast<const float4*>(row) + l);
-            const float4 s = __ldg(reinterpret_cast<const float4*>(row + half) + l);
-            cs[0] = c.x, cs[1] = c.y, cs[2] = c.z, cs[3] = c.w;
-            sn[0] = s.x, sn[1] = s.y, sn[2] = s.z, sn[3] = s.w;
-        } else {
-            const float4* c = reinterpret_cast<const float4*>(row + (upper ? 8 * l - half : 8 * l));
-            const float4* s = reinterpret_cast<const float4*>(row + half + (upper ? 8 * l - half : 8 * l));
-            const float4 c0 = __ldg(c), c1 = __ldg(c + 1), s0 = __ldg(s), s1 = __ldg(s + 1);
-            cs[0] = c0.x, cs[1] = c0.y, cs[2] = c0.z, cs[3] = c0.w;
-            cs[4] = c1.x, cs[5] = c1.y, cs[6] = c1.z, cs[7] = c1.w;
-            sn[0] = s0.x, sn[1] = s0.y, sn[2] = s0.z, sn[3] = s0.w;
-            sn[4] = s1.x, sn[5] = s1.y, sn[6] = s1.z, sn[7] = s1.w;
-        }
-    }
-    const int partner = upper ? l - half / 8 : l + half / 8;
-    const int from = (threadIdx.x % 32 / LPR) * LPR + (turn && !p.interleaved ? partner : l);
-
+    NraToken tok;
+    tok.b = static_cast<int>(i / static_cast<uint32_t>(p.q_len));
+    tok.t = static_cast<int>(i % static_cast<uint32_t>(p.q_len));
+    tok.cached = blk >= 0 && blk < p.num_blocks;
+    if (!tok.cached && flag) atomicOr(p.err, KV_DEVERR_BLOCK_ID);       // its query row is still computed
+    tok.slot = (static_cast<size_t>(tok.cached ? blk : 0) * p.block_size + pos % p.block_size) * p.kv_heads;
+    NraTurn w;
+    if (ln.turn && r0 < p.q_heads + p.kv_heads) w.load(p, p.rope + static_cast<size_t>(pos) * p.rope_dim, ln);
 #pragma unroll
     for (int j = 0; j < RPT; ++j) {
-        const int r = r0 + j;
-        if (r >= rows) return;
-        const bool is_q = r < p.q_heads;
-        const bool is_v = r >= p.q_heads + p.kv_heads;
-        const int h = is_q ? r : is_v ? r - p.q_heads - p.kv_heads : r - p.q_heads;
-        if (is_v) {
-            if (!cached) return;
-            if constexpr (FP8)
-                reinterpret_cast<uint2*>(p.v_pool + (slot + h) * D)[l] = e4m3_codes8(x[j], __ldg(p.v_scale + h));
-            else
-                reinterpret_cast<uint4*>(p.v_pool + (slot + h) * D * 2)[l] = x[j];
-            continue;
+        if (r0 + j >= rows) return;
+        nra_row<D, FP8>(p, tok, ln, w, x0[j], x1[j], r0 + j, group_mask);
+    }
+}
+
+// The streaming form, for prompts: persistent CTAs take equal runs of tokens; a producer warp looks
+// up 32 tokens' places at a time and brings each token's rows and its cos/sin row into a ring of
+// stages with bulk copies, so that the loads run far ahead of the arithmetic and the chain
+// position -> table -> row is paid once per 32 tokens; eight warps take a token's rows from there.
+constexpr int NRS_CW = 8;
+constexpr int NRS_THREADS = (NRS_CW + 1) * 32;
+constexpr int NRS_CTAS = 3;                         // per SM
+constexpr int NRS_RING = 72 * 1024;
+constexpr int NRS_STAGES = 16;                      // at most
+
+struct NrsCtl {
+    uint64_t full[NRS_STAGES], empty[NRS_STAGES];
+    NraToken tok[NRS_STAGES];                       // b < 0: the token writes nothing
+};
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(NRS_THREADS, NRS_CTAS)
+paged_norm_rope_append_stream(const NormRopeParams p, int stage_bytes, int stages)
+{
+    constexpr int LPR = D / 8;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ NrsCtl ctl;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(smem_u32(&ctl.full[i]), 1);
+            mbar_init(smem_u32(&ctl.empty[i]), NRS_CW);
         }
-        float y[8];
-        const uint32_t w4[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            y[2 * e] = __uint_as_float(w4[e] << 16);
-            y[2 * e + 1] = __uint_as_float(w4[e] & 0xffff0000u);
-        }
-        const float* weight = is_q ? p.q_weight : p.k_weight;
-        if (weight != nullptr) {
-            float ss = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss += y[e] * y[e];
-#pragma unroll
-            for (int o = LPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(group_mask, ss, o);
-            const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-            const float4 g0 = __ldg(reinterpret_cast<const float4*>(weight) + 2 * l);
-            const float4 g1 = __ldg(reinterpret_cast<const float4*>(weight) + 2 * l + 1);
-            const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = y[e] * inv * g[e];
-        }
-        if (p.rope != nullptr) {
-            if (p.interleaved) {
-                if (turn) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float a = y[2 * e], c = y[2 * e + 1];
-                        y[2 * e] = a * cs[e] - c * sn[e];
-                        y[2 * e + 1] = c * cs[e] + a * sn[e];
-                    }
+        fence_mbar_init();
+    }
+    grid_dependency_wait();                         // inputs of the preceding kernel are ready
+    grid_dependents_launch();
+    __syncthreads();
+    const uint32_t lo = static_cast<uint32_t>(static_cast<unsigned long long>(p.num_tokens) * blockIdx.x / gridDim.x);
+    const uint32_t hi = static_cast<uint32_t>(static_cast<unsigned long long>(p.num_tokens) * (blockIdx.x + 1) / gridDim.x);
+    const uint32_t q_bytes = static_cast<uint32_t>(p.q_heads) * D * 2, kv_bytes = static_cast<uint32_t>(p.kv_heads) * D * 2;
+    const uint32_t rope_bytes = p.rope != nullptr ? static_cast<uint32_t>(p.rope_dim) * 4 : 0u;
+
+    if (warp == NRS_CW) {
+        bool ok = true;
+        int n = 0;                                  // tokens issued
+        const auto place = [&](uint32_t i, int& seq, int& pos, int& blk) {
+            seq = -1;
+            if (i >= hi) return;
+            if (nra_place(p, i, true, seq, pos)) {
+                blk = __ldg(p.tables + static_cast<size_t>(seq) * p.max_blocks + pos / p.block_size);
+                if (blk < 0 || blk >= p.num_blocks) {
+                    atomicOr(p.err, KV_DEVERR_BLOCK_ID);                // its query row is still computed
+                    blk = -1;
                 }
             } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float o = __shfl_sync(group_mask, y[e], from);
-                    if (turn) y[e] = upper ? y[e] * cs[e] + o * sn[e] : y[e] * cs[e] - o * sn[e];
+                seq = -1;
+            }
+        };
+        int seq, pos = 0, blk = -1;
+        place(lo + lane, seq, pos, blk);
+        for (uint32_t base = lo; base < hi && ok; base += 32) {
+            int seq2, pos2 = 0, blk2 = -1;          // the next 32 tokens
+            place(base + 32 + lane, seq2, pos2, blk2);
+            const int cnt = static_cast<int>(min(32u, hi - base));
+            for (int k = 0; k < cnt; ++k, ++n) {
+                const int s = n % stages;
+                const int tseq = __shfl_sync(FULL_MASK, seq, k);
+                const int tpos = __shfl_sync(FULL_MASK, pos, k);
+                const int tblk = __shfl_sync(FULL_MASK, blk, k);
+                ok = all_ok(mbar_wait_bounded(smem_u32(&ctl.empty[s]), (static_cast<uint32_t>(n / stages) & 1u) ^ 1u));
+                if (!ok) break;
+                const uint32_t i = base + k;
+                const uint32_t bar = smem_u32(&ctl.full[s]);
+                if (lane == 0) {
+                    NraToken tok;
+                    tok.b = tseq >= 0 ? static_cast<int>(i / static_cast<uint32_t>(p.q_len)) : -1;
+                    tok.t = static_cast<int>(i % static_cast<uint32_t>(p.q_len));
+                    tok.cached = tblk >= 0;
+                    tok.slot = (static_cast<size_t>(max(tblk, 0)) * p.block_size + tpos % p.block_size) * p.kv_heads;
+                    ctl.tok[s] = tok;
+                    if (tseq >= 0)
+                        mbar_arrive_expect_tx(bar, q_bytes + 2 * kv_bytes + rope_bytes);
+                    else
+                        mbar_arrive(bar);
+                }
+                __syncwarp();                       // armed before any byte can land
+                if (tseq >= 0 && lane < 4) {
+                    const uint32_t dst = smem_u32(ring + static_cast<size_t>(s) * stage_bytes);
+                    const void* src = lane == 0   ? static_cast<const void*>(p.q + i * p.q_stride)
+                                      : lane == 1 ? static_cast<const void*>(p.k + i * p.k_stride)
+                                      : lane == 2 ? static_cast<const void*>(p.v + i * p.v_stride)
+                                                  : static_cast<const void*>(p.rope + static_cast<size_t>(tpos) * p.rope_dim);
+                    const uint32_t off = lane == 0 ? 0u : lane == 1 ? q_bytes : lane == 2 ? q_bytes + kv_bytes : q_bytes + 2 * kv_bytes;
+                    const uint32_t bytes = lane == 0 ? q_bytes : lane < 3 ? kv_bytes : rope_bytes;
+                    if (bytes > 0) bulk_load(dst + off, src, bytes, bar);
                 }
             }
+            seq = seq2;
+            pos = pos2;
+            blk = blk2;
         }
-        if (is_q || !FP8) {
-            const uint4 o = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                                       pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-            if (is_q) {
-                const size_t row = (static_cast<size_t>(b) * p.q_heads + h) * p.q_len + t;
-                reinterpret_cast<uint4*>(p.q_out + row * D)[l] = o;
-            } else if (cached) {
-                reinterpret_cast<uint4*>(p.k_pool + (slot + h) * D * 2)[l] = o;
+        if (!ok && lane == 0) atomicOr(p.err, KV_DEVERR_TIMEOUT);
+        // copies still in flight must land before the CTA exits
+        for (int j = max(0, n - stages); j < n; ++j)
+            if (!mbar_wait_bounded(smem_u32(&ctl.full[j % stages]), static_cast<uint32_t>(j / stages) & 1u)) break;
+        return;
+    }
+
+    NraLane ln;
+    ln.init(p, lane % LPR);
+    const unsigned group_mask = ((1u << LPR) - 1u) << (lane / LPR * LPR);
+    const int rows = p.q_heads + 2 * p.kv_heads;
+    constexpr int GPC = NRS_CW * 32 / LPR;          // rows in hand at a time
+    const int count = static_cast<int>(hi - lo);
+    for (int n = 0; n < count; ++n) {
+        const int s = n % stages;
+        if (!all_ok(mbar_wait_bounded(smem_u32(&ctl.full[s]), static_cast<uint32_t>(n / stages) & 1u))) {
+            if (lane == 0) atomicOr(p.err, KV_DEVERR_TIMEOUT);
+            break;
+        }
+        const NraToken tok = ctl.tok[s];
+        if (tok.b >= 0) {
+            const uint8_t* st = ring + static_cast<size_t>(s) * stage_bytes;
+            NraTurn w;
+            if (ln.turn) w.load(p, reinterpret_cast<const float*>(st + q_bytes + 2 * kv_bytes), ln);
+            for (int r = threadIdx.x / LPR; r < rows; r += GPC) {
+                const uint16_t* x = reinterpret_cast<const uint16_t*>(st) + r * D;
+                nra_row<D, FP8>(p, tok, ln, w, *reinterpret_cast<const uint2*>(x + ln.at[0]),
+                                *reinterpret_cast<const uint2*>(x + ln.at[1]), r, group_mask);
             }
-        } else if (cached) {
-            reinterpret_cast<uint2*>(p.k_pool + (slot + h) * D)[l] = e4m3_codes8f(y, __ldg(p.k_scale + h));
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl.empty[s]));
     }
 }
 
@@ -199,17 +390,39 @@ cudaError_t launch_nra(NormRopeParams p, cudaStream_t s)
 }
 
 template <int D, bool FP8>
-cudaError_t launch_nra_rows(const NormRopeParams& p, cudaStream_t s)
+cudaError_t launch_nra_form(const NormRopeParams& p, int num_sms, cudaStream_t s)
 {
+    const long long bytes = (static_cast<long long>(p.q_heads) + 2 * p.kv_heads) * D * 2 + p.rope_dim * 4;
+    const long long stage = (bytes + 127) / 128 * 128;
+    const int ctas = num_sms * NRS_CTAS;
+    if (p.num_tokens >= NRA_STREAM_TOKENS * ctas && stage * 3 <= NRS_RING) {
+        const int stages = static_cast<int>(NRS_RING / stage < NRS_STAGES ? NRS_RING / stage : NRS_STAGES);
+        return launch_dependent(paged_norm_rope_append_stream<D, FP8>, dim3(static_cast<unsigned>(ctas)), dim3(NRS_THREADS),
+                                static_cast<size_t>(stages) * stage, s, p, static_cast<int>(stage), stages);
+    }
     return launch_nra<D, FP8, 4>(p, s);
+}
+
+template <int D, bool FP8>
+cudaError_t prepare_nra()
+{
+    return cudaFuncSetAttribute(paged_norm_rope_append_stream<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, NRS_RING);
 }
 
 }  // namespace
 
-cudaError_t launch_norm_rope_append(const NormRopeParams& p, int head_dim, bool fp8, cudaStream_t s)
+cudaError_t prepare_norm_rope_append(int head_dim, bool fp8)
 {
-    if (head_dim == 128) return fp8 ? launch_nra_rows<128, true>(p, s) : launch_nra_rows<128, false>(p, s);
-    if (head_dim == 64 && !fp8) return launch_nra_rows<64, false>(p, s);
+    if (head_dim == 128) return fp8 ? prepare_nra<128, true>() : prepare_nra<128, false>();
+    if (head_dim == 64 && !fp8) return prepare_nra<64, false>();
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_norm_rope_append(const NormRopeParams& p, int head_dim, bool fp8, int num_sms, cudaStream_t s)
+{
+    if (head_dim == 128)
+        return fp8 ? launch_nra_form<128, true>(p, num_sms, s) : launch_nra_form<128, false>(p, num_sms, s);
+    if (head_dim == 64 && !fp8) return launch_nra_form<64, false>(p, num_sms, s);
     return cudaErrorInvalidValue;
 }
 

@@ -172,6 +172,34 @@ def test_ragged_prompt_pieces():
     c.check(out)
 
 
+@pytest.mark.parametrize("kw", [dict(hq=4, hk=2, d=128, bs=16, rope_dim=128), dict(hq=5, hk=1, d=64, bs=32, rope_dim=32, norm=False),
+                                dict(hq=4, hk=4, d=128, bs=32, rope_dim=64, interleaved=True, fp8=True),
+                                dict(hq=64, hk=16, d=128, bs=16, rope_dim=0)],
+                         ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()))
+def test_long_prompts(kw):
+    """Enough tokens for every CTA's ring to go round; some of them bad, one batch of q_len tokens."""
+    r = np.random.default_rng(5)
+    n = 3001 if kw["hq"] < 64 else 1300
+    seq = np.sort(r.integers(0, 4, n))
+    pos = np.concatenate([np.arange((seq == b).sum()) + 7 * b for b in range(4)])
+    c = Call(batch=4, seq=seq, pos=pos, **kw)
+    bad = np.zeros(n, bool)
+    bad[[0, 31, 32, 700, n - 1]] = True
+    c.seq[bad] = [-1, 4, 10 ** 9, -5, 99]
+    out = torch.full((n, c.hq, c.d), 7.0, dtype=torch.bfloat16, device="cuda")
+    c.run(out=out)
+    assert c.pool.device_errors() == kp.DEVERR_SEQ
+    assert (out[torch.from_numpy(bad).cuda()] == 7.0).all()
+    c.seq[bad] = 0
+    c.check(out, written=~bad, q_written=~bad)
+    if kw["hq"] == 4 and not kw.get("fp8"):
+        c = Call(ctx=r.integers(5, 40, 301), q_len=5, **kw)
+        out = torch.empty((301, 4, 5, c.d), dtype=torch.bfloat16, device="cuda")
+        c.run(out=out)
+        assert c.pool.device_errors() == 0
+        c.check(out)
+
+
 def test_without_norm_and_rotation_it_is_the_append():
     """Same pool bytes as paged_kv_append, queries copied."""
     for fp8 in (False, True):
