@@ -68,17 +68,30 @@ struct PfxCfg {
     static_assert(!FP8 || D == 128, "fp8 path is laid out for head_dim 128");
 };
 
+constexpr int PFX_ITEMS = 4;                        // items handed on ahead
+
+// A run of one CTA: tiles tile0 .. tile0 + n - 1 of (group, kv head, pair).
+struct PfxItem {
+    int off, rows;          // first member; rows of the pair (1 .. 256)
+    int row0;               // group row of the pair's first row
+    int kvh, blocks, tile0, n, run;
+    int pieces;             // of the whole run (with tile 0)
+    int both;               // the slots take alternate tiles of the same rows
+};
+
 struct PfxCtl {
     uint64_t full[16], empty[16];                   // the ring the MMAs read
     uint64_t raw_full[4], raw_empty[4];             // fp8: landed codes
     uint64_t q_ready[2], s_full[2], p_full[2], o_full[2], mma_done;
+    uint64_t item_full[PFX_ITEMS], item_empty[PFX_ITEMS];
+    PfxItem items[PFX_ITEMS];                       // n 0: no more
     uint32_t tmem_base;
     int abort_flag;
     uint32_t masks[PFX_MASKS];                      // valid blocks of a token tile
     long long lo, hi, units;                        // this CTA's range, all units
     long long base;                                 // first unit of group0
     int group0, ctas;                               // group that holds lo; CTAs with units
-    long long scan[32];
+    long long scan[14];
     uint64_t x_full, x_free;                        // team 1's state handed over, read
     union {
         float q_up[2][PFX_TILE];                    // fp8: undoes a row's power-of-two scale (read at an
@@ -87,13 +100,6 @@ struct PfxCtl {
     };
 };
 
-// A run of one CTA: tiles tile0 .. tile0 + n - 1 of (group, kv head, pair).
-struct PfxItem {
-    int off, rows;          // first member; rows of the pair (1 .. 256)
-    int row0;               // group row of the pair's first row
-    int kvh, blocks, tile0, n, run;
-    bool both;              // the slots take alternate tiles of the same rows
-};
 
 // a / b for non-negative values; in 32 bits where they fit.
 __device__ __forceinline__ long long pfx_div(long long a, long long b)
@@ -102,7 +108,13 @@ __device__ __forceinline__ long long pfx_div(long long a, long long b)
     return a / b;
 }
 
-// The items of a CTA's range, walked by every role on its own (uniform in a warp).
+// The CTA that holds unit u of `units` cut into ranges for n CTAs.
+__device__ __forceinline__ int pfx_cta_of(long long u, long long units, int n)
+{
+    return static_cast<int>(pfx_div((u + 1) * n - 1, units));
+}
+
+// The items of a CTA's range.
 struct PfxWalk {
     long long u, hi, base, units;
     int g, pairs, tiles;
@@ -123,8 +135,9 @@ struct PfxWalk {
         g = ctl->group0;
         if (u < hi) load(p, block_size);
     }
-    __device__ __forceinline__ bool next(const PrefixParams& p, int block_size, PfxItem& it)
+    __device__ __forceinline__ bool next(const PrefixParams& p, const PfxCtl* ctl, int block_size, PfxItem& it)
     {
+        it.n = 0;
         if (u >= hi) return false;
         while (u >= base + units) {                 // hi is at most the last group's end
             base += units;
@@ -144,16 +157,12 @@ struct PfxWalk {
         it.both = it.rows <= PFX_TILE;
         it.blocks = gr.blocks;
         it.run = prefix_run_base(p, g, gr) + run;
+        // the run's pieces: one per CTA from the one of its first tile to the one of its last
+        it.pieces = it.tile0 == 0 ? pfx_cta_of(u + tiles - 1, ctl->units, ctl->ctas) - static_cast<int>(blockIdx.x) + 1 : 0;
         u += it.n;
         return true;
     }
 };
-
-// The CTA that holds unit u of `units` cut into ranges for n CTAs.
-__device__ __forceinline__ int pfx_cta_of(long long u, long long units, int n)
-{
-    return static_cast<int>(pfx_div((u + 1) * n - 1, units));
-}
 
 __device__ __forceinline__ bool pfx_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag)
 {
@@ -191,8 +200,31 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     return d;
 }
 
-__device__ __forceinline__ void tc_ld(uint32_t taddr, uint32_t (&r)[64]) { tc_ld64(taddr, r); }
-__device__ __forceinline__ void tc_ld(uint32_t taddr, uint32_t (&r)[128]) { tc_ld128(taddr, r); }
+// Maximum of 32 scores and mx.
+__device__ __forceinline__ float max_of(const uint32_t (&x)[32], float mx)
+{
+    float m[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 4]));
+#pragma unroll
+    for (int j = 8; j < 32; j += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m[e] = max3(m[e], __uint_as_float(x[j + e]), __uint_as_float(x[j + 4 + e]));
+    return max3(max3(m[0], m[1], mx), m[2], m[3]);
+}
+
+// 32 scores -> probabilities 2^(score * mul + sub), packed in pairs, and added to the sums.
+template <bool FP8>
+__device__ __forceinline__ void probs(const uint32_t (&x)[32], float2 mul, float2 sub, float2 (&sum)[2], uint32_t (&pk)[16])
+{
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const float2 y = fma2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), mul, sub);
+        const float2 pr = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+        sum[j & 1] = add2(sum[j & 1], pr);
+        pk[j] = FP8 ? pack_f16x2(pr.x, pr.y) : pack_bf16x2(pr.x, pr.y);
+    }
+}
 
 // Eight floats, one 32-byte sector.
 __device__ __forceinline__ void store_sector(float* dst, const float* x)
@@ -244,6 +276,10 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             mbar_init(smem_u32(&ctl->s_full[s]), 1);
             mbar_init(smem_u32(&ctl->p_full[s]), 4);
             mbar_init(smem_u32(&ctl->o_full[s]), 1);
+        }
+        for (int i = 0; i < PFX_ITEMS; ++i) {
+            mbar_init(smem_u32(&ctl->item_full[i]), 1);
+            mbar_init(smem_u32(&ctl->item_empty[i]), FP8 ? 13 : 9);     // MMA thread, softmax and converter warps
         }
         mbar_init(smem_u32(&ctl->mma_done), 1);
         mbar_init(smem_u32(&ctl->x_full), 4);
@@ -327,9 +363,18 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = ctl->tmem_base;
-    PfxWalk walk;
-    walk.init(p, ctl, BS);
     PfxItem it;
+    // item k as the producer handed it on; false: no more, or the wait gave up (then failed is set)
+    const auto take_item = [&](int k, bool leader, bool& failed) {
+        const int slot = k % PFX_ITEMS;
+        if (!pfx_wait(smem_u32(&ctl->item_full[slot]), static_cast<uint32_t>(k / PFX_ITEMS) & 1u, abort_flag)) {
+            failed = true;
+            return false;
+        }
+        it = ctl->items[slot];
+        if (leader) mbar_arrive(smem_u32(&ctl->item_empty[slot]));
+        return it.n > 0;
+    };
 
     if (warp == 8) {
         // ------------------------------------------------------------ loads
@@ -347,7 +392,19 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         int n = 0;                                  // tiles of K and V issued
         int kt = 0;                                 // K tiles issued
         bool ok = true;
-        while (ok && walk.next(p, BS, it)) {
+        PfxWalk walk;
+        walk.init(p, ctl, BS);
+        for (int k = 0; ok; ++k) {
+            const bool more = walk.next(p, ctl, BS, it);
+            const int slot = k % PFX_ITEMS;
+            ok = all_ok(pfx_wait(smem_u32(&ctl->item_empty[slot]), (static_cast<uint32_t>(k / PFX_ITEMS) & 1u) ^ 1u, abort_flag));
+            if (!ok) break;
+            if (lane == 0) {
+                ctl->items[slot] = it;
+                mbar_arrive(smem_u32(&ctl->item_full[slot]));
+            }
+            __syncwarp();
+            if (!more) break;
             const int32_t* trow = p.tables + static_cast<size_t>(it.off) * p.max_blocks;
             const int blk0 = it.tile0 * C::BLOCKS;
             const int nblk = min(it.n * C::BLOCKS, it.blocks - blk0);   // blocks of the prefix
@@ -439,7 +496,8 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 tc_fence_after();
                 return good;
             };
-            for (int k = 0; ok && walk.next(p, BS, it); ++k) {
+            bool failed = false;
+            for (int k = 0; ok && take_item(k, true, failed); ++k) {
                 for (int s = 0; ok && s < 2; ++s)
                     ok = pfx_wait(smem_u32(&ctl->q_ready[s]), static_cast<uint32_t>(k) & 1u, abort_flag);
                 tc_fence_after();
@@ -489,7 +547,7 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 tc_commit(smem_u32(&ctl->o_full[0]));
                 tc_commit(smem_u32(&ctl->o_full[1]));
             }
-            if (!ok) pfx_give_up(p, abort_flag);
+            if (!ok || failed) pfx_give_up(p, abort_flag);
             // every MMA issued must be complete before the tensor memory is freed
             tc_commit(smem_u32(&ctl->mma_done));
             mbar_wait_bounded(smem_u32(&ctl->mma_done), 0);
@@ -506,49 +564,61 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         int kt = 0;                                 // K tiles of the items before
         uint32_t seen = 0;                          // score tiles of this slot waited for
         int swaps = 0;                              // items whose slots were merged
-        for (int k = 0; walk.next(p, BS, it); ++k) {
+        for (int k = 0;; ++k) {
+            bool failed = false;
+            const bool more = take_item(k, false, failed);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->item_empty[k % PFX_ITEMS]));
+            ok = all_ok(!failed);
+            if (!ok || !more) break;
             // ---- this warp's 32 rows of q into shared memory (K-major, 128-byte swizzle);
             // the score MMAs of the item before are complete (o_full)
             const int first = it.row0 + (it.both ? 0 : s * PFX_TILE);   // group row of slot row 0
             const int rows = it.both ? it.rows : min(PFX_TILE, it.rows - s * PFX_TILE);
             constexpr int CH = D / 8;               // 16-byte chunks of a row
             constexpr int RPI = 32 / CH;            // rows of a warp-wide load
-            uint4 x[CH];
+            constexpr int INF = 4;                  // loads in flight
+            // (loops are kept rolled: the code of a launch is fetched once, and a tile or two per CTA
+            // is all that a short prefix has to hide that behind)
+#pragma unroll 1
+            for (int j0 = 0; j0 < CH; j0 += INF) {
+                uint4 x[INF];
 #pragma unroll
-            for (int j = 0; j < CH; ++j) {
-                const int r = w * 32 + j * RPI + lane / CH;
-                x[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (r < rows) {
-                    const int m = (first + r) / p.rows, rr = first + r - m * p.rows;
-                    const size_t at = (static_cast<size_t>(it.off + m) * p.kv_heads + it.kvh) * p.rows + rr;
-                    x[j] = __ldg(reinterpret_cast<const uint4*>(p.q + at * D) + lane % CH);
+                for (int j = 0; j < INF; ++j) {
+                    const int r = w * 32 + (j0 + j) * RPI + lane / CH;
+                    x[j] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < rows) {
+                        const int m = (first + r) / p.rows, rr = first + r - m * p.rows;
+                        const size_t at = (static_cast<size_t>(it.off + m) * p.kv_heads + it.kvh) * p.rows + rr;
+                        x[j] = __ldg(reinterpret_cast<const uint4*>(p.q + at * D) + lane % CH);
+                    }
                 }
-            }
 #pragma unroll
-            for (int j = 0; j < CH; ++j) {
-                const int r = w * 32 + j * RPI + lane / CH, ch = lane % CH;
-                if constexpr (FP8) {
-                    // the row's largest magnitude to [2^14, 2^15) by a power of two, then f16
-                    uint32_t v[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-                    uint32_t big = 0;
+                for (int j = 0; j < INF; ++j) {
+                    const int r = w * 32 + (j0 + j) * RPI + lane / CH, ch = lane % CH;
+                    if constexpr (FP8) {
+                        // the row's largest magnitude to [2^14, 2^15) by a power of two, then f16
+                        uint32_t v[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                        uint32_t big = 0;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        big = max(big, max((v[e] & 0x7fffu) << 16, v[e] & 0x7fff0000u));
+                        for (int e = 0; e < 4; ++e)
+                            big = max(big, max((v[e] & 0x7fffu) << 16, v[e] & 0x7fff0000u));
 #pragma unroll
-                    for (int o = CH / 2; o >= 1; o >>= 1) big = max(big, __shfl_xor_sync(FULL_MASK, big, o));
-                    const int ex = min(254, max(14, 268 - static_cast<int>(big >> 23)));  // of the factor
-                    const float up = __uint_as_float(static_cast<uint32_t>(min(254, 254 - ex)) << 23);
-                    const float down = __uint_as_float(static_cast<uint32_t>(ex) << 23);
+                        for (int o = CH / 2; o >= 1; o >>= 1) big = max(big, __shfl_xor_sync(FULL_MASK, big, o));
+                        const int ex = min(254, max(14, 268 - static_cast<int>(big >> 23)));  // of the factor
+                        const float up = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
+                        const float down = __uint_as_float(static_cast<uint32_t>(ex) << 23);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        v[e] = pack_f16x2(__uint_as_float(v[e] << 16) * down, __uint_as_float(v[e] & 0xffff0000u) * down);
-                    x[j] = make_uint4(v[0], v[1], v[2], v[3]);
-                    if (ch == 0) ctl->q_up[s][r] = up;
+                        for (int e = 0; e < 4; ++e)
+                            v[e] = pack_f16x2(__uint_as_float(v[e] << 16) * down, __uint_as_float(v[e] & 0xffff0000u) * down);
+                        x[j] = make_uint4(v[0], v[1], v[2], v[3]);
+                        if (ch == 0) ctl->q_up[s][r] = up;
+                    }
+                    const uint32_t dst = qs + (ch >> 3) * (PFX_TILE * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(x[j].x), "r"(x[j].y),
+                                 "r"(x[j].z), "r"(x[j].w)
+                                 : "memory");
                 }
-                const uint32_t dst = qs + (ch >> 3) * (PFX_TILE * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(x[j].x), "r"(x[j].y),
-                             "r"(x[j].z), "r"(x[j].w)
-                             : "memory");
             }
             fence_proxy_async_smem();
             tc_fence_before();
@@ -596,23 +666,18 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     tc_wait_st();
                     mult = 1.f;
                 }
-                // The row's scores: all in registers, or (8-bit cache: more threads per CTA) read twice.
-                constexpr int COLS = FP8 ? 64 : PFX_TILE;
-                uint32_t x[COLS];
+                // The maximum: 32 columns at a time, the next ones on their way meanwhile.
                 float mx = -INFINITY;
+                uint32_t a[32], b[32];
+                tc_ld32(tm_s, a);
 #pragma unroll
-                for (int c = 0; c < PFX_TILE; c += COLS) {
-                    tc_ld(tm_s + c, x);
-                    tc_wait_ld();
-                    float m4[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) m4[j] = max3(__uint_as_float(x[j]), __uint_as_float(x[j + 4]), mx);
-#pragma unroll
-                    for (int j = 8; j < COLS; j += 8)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            m4[e] = max3(m4[e], __uint_as_float(x[j + e]), __uint_as_float(x[j + 4 + e]));
-                    mx = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
+                for (int c = 0; c < PFX_TILE; c += 64) {
+                    tc_wait_ld(a);
+                    tc_ld32(tm_s + c + 32, b);
+                    mx = max_of(a, mx);
+                    tc_wait_ld(b);
+                    if (c + 64 < PFX_TILE) tc_ld32(tm_s + c + 64, a);
+                    mx = max_of(b, mx);
                 }
                 mx *= mult;
                 float f = 1.f;
@@ -639,32 +704,23 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 }
                 const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
                 const float2 mul2 = make_float2(mult, mult), sub2 = make_float2(-m_use, -m_use);
-                float2 ls[4];
+                float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                // Probabilities over the scores they come from: 32 tokens become 16 columns, all of
+                // which have been read by then.
+                tc_ld32(tm_s, a);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) ls[j] = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int c = 0; c < PFX_TILE; c += COLS) {
-                    if (COLS < PFX_TILE) {
-                        tc_ld(tm_s + c, x);
-                        tc_wait_ld();
-                    }
-                    // probabilities over the scores they come from: 64 tokens become 32 columns, all
-                    // of which have been read by then
-#pragma unroll
-                    for (int h = 0; h < COLS; h += 64) {
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float2 y = fma2(make_float2(__uint_as_float(x[h + 2 * j]), __uint_as_float(x[h + 2 * j + 1])),
-                                                  mul2, sub2);
-                            const float2 pr = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-                            ls[j & 3] = add2(ls[j & 3], pr);
-                            pk[j] = FP8 ? pack_f16x2(pr.x, pr.y) : pack_bf16x2(pr.x, pr.y);
-                        }
-                        tc_st32(tm_s + (c + h) / 2, pk);
-                    }
+                for (int c = 0; c < PFX_TILE; c += 64) {
+                    uint32_t pk[16];
+                    tc_wait_ld(a);
+                    tc_ld32(tm_s + c + 32, b);
+                    probs<FP8>(a, mul2, sub2, ls, pk);
+                    tc_wait_ld(b);
+                    tc_st16(tm_s + c / 2, pk);
+                    if (c + 64 < PFX_TILE) tc_ld32(tm_s + c + 64, a);
+                    probs<FP8>(b, mul2, sub2, ls, pk);
+                    tc_st16(tm_s + c / 2 + 16, pk);
                 }
-                const float2 lt = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
+                const float2 lt = add2(ls[0], ls[1]);
                 l += lt.x + lt.y;
                 tc_wait_st();
                 tc_fence_before();
@@ -740,12 +796,7 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 ok = all_ok(pfx_wait(smem_u32(&ctl->x_free), static_cast<uint32_t>(swaps - 1) & 1u, abort_flag));
                 if (!ok) break;
             }
-            if (it.tile0 == 0 && tid == 0) {
-                // the run's pieces: one per CTA from this one to the one of its last tile
-                const long long u0 = walk.u - it.n;
-                const int last = pfx_cta_of(u0 + walk.tiles - 1, ctl->units, ctl->ctas);
-                p.runs[it.run] = make_int2(static_cast<int>(blockIdx.x) + it.run, last - static_cast<int>(blockIdx.x) + 1);
-            }
+            if (it.tile0 == 0 && tid == 0) p.runs[it.run] = make_int2(static_cast<int>(blockIdx.x) + it.run, it.pieces);
             tc_fence_before();
             kt += it.n;
         }
@@ -756,7 +807,13 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             const int t = tid - 10 * 32;            // token of the tile
             bool ok = true;
             int n = 0;
-            while (ok && walk.next(p, BS, it)) {
+            bool failed = false;
+            for (int k = 0; ok; ++k) {
+                const bool more = take_item(k, false, failed);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl->item_empty[k % PFX_ITEMS]));
+                ok = all_ok(!failed);
+                if (!more) break;
                 for (int i = 0; ok && i < 2 * it.n; ++i, ++n) {
                     const int rs = n % C::NRAW, s = n % C::NRING;
                     ok = all_ok(pfx_wait(smem_u32(&ctl->raw_full[rs]), static_cast<uint32_t>(n / C::NRAW) & 1u, abort_flag) &&
@@ -764,7 +821,7 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     if (!ok) break;
                     const uint32_t src = smem_u32(raw) + rs * C::RAW + t * 128;
                     const uint32_t dst = smem_u32(ring) + s * C::TILE + (t >> 3) * C::OCTET + (t & 7) * 128;
-#pragma unroll
+#pragma unroll 2
                     for (int c = 0; c < 8; ++c) {   // 16 codes -> two 16-byte chunks
                         const uint4 v = lds128(src + ((c ^ (t & 7)) << 4));
                         const uint32_t q[4] = {v.x, v.y, v.z, v.w};
