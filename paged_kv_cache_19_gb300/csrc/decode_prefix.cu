@@ -92,7 +92,7 @@ struct PfxCtl {
     long long base;                                 // first unit of group0
     int group0, ctas;                               // group that holds lo; CTAs with units
     long long scan[14];
-    uint64_t x_full, x_free;                        // team 1's state handed over, read
+    uint64_t x_full, e_done[2];                     // team 1's state handed over; a team is done with an item
     union {
         float q_up[2][PFX_TILE];                    // fp8: undoes a row's power-of-two scale (read at an
                                                     // item's start)
@@ -226,14 +226,6 @@ __device__ __forceinline__ void probs(const uint32_t (&x)[32], float2 mul, float
     }
 }
 
-// Eight floats, one 32-byte sector.
-__device__ __forceinline__ void store_sector(float* dst, const float* x)
-{
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(x[0]), "f"(x[1]), "f"(x[2]),
-                 "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
-                 : "memory");
-}
-
 __device__ __forceinline__ void pfx_give_up(const PrefixParams& p, volatile int* abort_flag)
 {
     if (!*abort_flag) atomicOr(p.err, KV_DEVERR_TIMEOUT);
@@ -283,7 +275,7 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         }
         mbar_init(smem_u32(&ctl->mma_done), 1);
         mbar_init(smem_u32(&ctl->x_full), 4);
-        mbar_init(smem_u32(&ctl->x_free), 4);
+        for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&ctl->e_done[s]), 4);
         ctl->abort_flag = 0;
         fence_mbar_init();
     }
@@ -564,6 +556,7 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         int kt = 0;                                 // K tiles of the items before
         uint32_t seen = 0;                          // score tiles of this slot waited for
         int swaps = 0;                              // items whose slots were merged
+        bool last_handed = false;
         for (int k = 0;; ++k) {
             bool failed = false;
             const bool more = take_item(k, false, failed);
@@ -571,32 +564,56 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             if (lane == 0) mbar_arrive(smem_u32(&ctl->item_empty[k % PFX_ITEMS]));
             ok = all_ok(!failed);
             if (!ok || !more) break;
-            // ---- this warp's 32 rows of q into shared memory (K-major, 128-byte swizzle);
-            // the score MMAs of the item before are complete (o_full)
+            // ---- this warp's 32 rows of q into shared memory (K-major, 128-byte swizzle).  The score
+            // MMAs of the item before are complete (o_full); its epilogue, which goes through this
+            // memory, must be over in every warp of the team, and in team 0's if it merged.
+            if (k > 0) {
+                const uint32_t ph = static_cast<uint32_t>(k - 1) & 1u;
+                ok = pfx_wait(smem_u32(&ctl->e_done[s]), ph, abort_flag);
+                if (ok && s == 1 && last_handed) ok = pfx_wait(smem_u32(&ctl->e_done[0]), ph, abort_flag);
+                if (!all_ok(ok)) {
+                    ok = false;
+                    break;
+                }
+            }
             const int first = it.row0 + (it.both ? 0 : s * PFX_TILE);   // group row of slot row 0
             const int rows = it.both ? it.rows : min(PFX_TILE, it.rows - s * PFX_TILE);
             constexpr int CH = D / 8;               // 16-byte chunks of a row
             constexpr int RPI = 32 / CH;            // rows of a warp-wide load
-            constexpr int INF = 4;                  // loads in flight
-            // (loops are kept rolled: the code of a launch is fetched once, and a tile or two per CTA
-            // is all that a short prefix has to hide that behind)
-#pragma unroll 1
-            for (int j0 = 0; j0 < CH; j0 += INF) {
-                uint4 x[INF];
-#pragma unroll
-                for (int j = 0; j < INF; ++j) {
-                    const int r = w * 32 + (j0 + j) * RPI + lane / CH;
-                    x[j] = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < rows) {
-                        const int m = (first + r) / p.rows, rr = first + r - m * p.rows;
-                        const size_t at = (static_cast<size_t>(it.off + m) * p.kv_heads + it.kvh) * p.rows + rr;
-                        x[j] = __ldg(reinterpret_cast<const uint4*>(p.q + at * D) + lane % CH);
-                    }
+            constexpr int INF = 8;                  // loads in flight (8-bit cache; else all of them)
+            const int ch = lane % CH;
+            int r = w * 32 + lane / CH;             // the lane's row, its member and row of the member
+            int m = (first + r) / p.rows, rr = first + r - m * p.rows;
+            const auto source = [&]() {
+                return reinterpret_cast<const uint4*>(
+                           p.q + ((static_cast<size_t>(it.off + m) * p.kv_heads + it.kvh) * p.rows + rr) * D) + ch;
+            };
+            const auto target = [&]() { return qs + (ch >> 3) * (PFX_TILE * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4); };
+            const auto step = [&]() {
+                r += RPI;
+                for (rr += RPI; rr >= p.rows; rr -= p.rows) ++m;
+            };
+            // (loops are kept rolled: a launch fetches its code once, and a tile or two per CTA is all
+            // that a short prefix has to hide that behind)
+            if constexpr (!FP8) {
+#pragma unroll 2
+                for (int j = 0; j < CH; ++j, step()) {
+                    if (r < rows)
+                        cp_async16(target(), source());
+                    else
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(target()), "r"(0u) : "memory");
                 }
+                cp_async_wait_all();
+            } else {
+#pragma unroll 1
+                for (int j0 = 0; j0 < CH; j0 += INF) {
+                    uint4 x[INF];
+                    const int r0 = r;
 #pragma unroll
-                for (int j = 0; j < INF; ++j) {
-                    const int r = w * 32 + (j0 + j) * RPI + lane / CH, ch = lane % CH;
-                    if constexpr (FP8) {
+                    for (int j = 0; j < INF; ++j, step()) x[j] = r < rows ? __ldg(source()) : make_uint4(0u, 0u, 0u, 0u);
+                    r = r0;
+#pragma unroll
+                    for (int j = 0; j < INF; ++j, r += RPI) {
                         // the row's largest magnitude to [2^14, 2^15) by a power of two, then f16
                         uint32_t v[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
                         uint32_t big = 0;
@@ -611,13 +628,11 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             v[e] = pack_f16x2(__uint_as_float(v[e] << 16) * down, __uint_as_float(v[e] & 0xffff0000u) * down);
-                        x[j] = make_uint4(v[0], v[1], v[2], v[3]);
                         if (ch == 0) ctl->q_up[s][r] = up;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(target()), "r"(v[0]), "r"(v[1]),
+                                     "r"(v[2]), "r"(v[3])
+                                     : "memory");
                     }
-                    const uint32_t dst = qs + (ch >> 3) * (PFX_TILE * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(x[j].x), "r"(x[j].y),
-                                 "r"(x[j].z), "r"(x[j].w)
-                                 : "memory");
                 }
             }
             fence_proxy_async_smem();
@@ -771,31 +786,49 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 const size_t at = (static_cast<size_t>(blockIdx.x) + it.run) * PFX_PAIR + s * PFX_TILE + row;
                 if (row < rows)
                     p.piece_lse[at] = make_float4(l_out > 0.f ? m_out + __log2f(l_out) : -INFINITY, 0.f, 0.f, 0.f);
-                float* dst = p.piece_o + at * D;
+                // Through shared memory, half a row at a time, so that the warp's stores are whole
+                // rows: its own 128 bytes of every 512-byte line of the slot's query rows (idle by
+                // now; with a merge, the lines of the numbers it has just read), 16-byte chunk c of
+                // row i in line 32 (c / 8) + i at c % 8 ^ i % 8.
+                constexpr int HALF = D / 2;
+                const uint32_t stage = smem_u32(qsm) + s * C::QTILE + w * 128;
+                const auto chunk = [&](int i, int c) { return stage + ((c >> 3) * 32 + i) * 512 + (((c & 7) ^ (i & 7)) << 4); };
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t r[32];
-                    tc_ld32(tm_o + c * 32, r);
-                    tc_wait_ld();
-                    float x[32];
+                for (int d0 = 0; d0 < D; d0 += HALF) {
+#pragma unroll 1
+                    for (int c = 0; c < HALF; c += 32) {
+                        uint32_t x[32];
+                        tc_ld32(tm_o + d0 + c, x);
+                        tc_wait_ld(x);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        x[j] = __uint_as_float(r[j]) * keep;
-                        if (add != 0.f) x[j] += xo[(c * 32 + j) * PFX_TILE + row] * add;
-                    }
-                    if (row < rows) {
+                        for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * keep);
+                        if (add != 0.f) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8) store_sector(dst + c * 32 + j, x + j);
+                            for (int j = 0; j < 32; ++j)
+                                x[j] = __float_as_uint(__uint_as_float(x[j]) + xo[(d0 + c + j) * PFX_TILE + row] * add);
+                        }
+                        __syncwarp();               // (the lines of d0 + c .. are read by every lane)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(chunk(lane, c / 4 + j)), "r"(x[4 * j]),
+                                         "r"(x[4 * j + 1]), "r"(x[4 * j + 2]), "r"(x[4 * j + 3])
+                                         : "memory");
                     }
+                    __syncwarp();
+                    constexpr int CPR = HALF / 4;   // chunks of a row's half
+#pragma unroll 4
+                    for (int e = lane; e < 32 * CPR; e += 32) {
+                        const int i = e / CPR, c = e % CPR;
+                        const uint4 v = lds128(chunk(i, c));
+                        if (w * 32 + i < rows)
+                            *reinterpret_cast<uint4*>(p.piece_o + (at - lane + i) * D + d0 + c * 4) = v;
+                    }
+                    __syncwarp();
                 }
             }
-            if (handed) {
-                // the rows' memory is free for the next item's once team 0 has read it
-                __syncwarp();
-                if (s == 0 && lane == 0) mbar_arrive(smem_u32(&ctl->x_free));
-                ok = all_ok(pfx_wait(smem_u32(&ctl->x_free), static_cast<uint32_t>(swaps - 1) & 1u, abort_flag));
-                if (!ok) break;
-            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->e_done[s]));
+            last_handed = handed;
             if (it.tile0 == 0 && tid == 0) p.runs[it.run] = make_int2(static_cast<int>(blockIdx.x) + it.run, it.pieces);
             tc_fence_before();
             kt += it.n;
