@@ -88,13 +88,17 @@ def test_no_rule_is_the_plain_attention():
         c.pool.destroy()
 
 
-def test_freed_blocks_before_a_window_are_not_looked_at():
-    c = Cache(ctx=[500, 90, 4], hq=8, hk=2, d=128, bs=16, q_len=2)
+@pytest.mark.parametrize("kw", [dict(hk=2, d=128, bs=16), dict(hk=4, d=64, bs=16), dict(hk=8, d=128, bs=16, fp8=True),
+                                dict(hk=1, d=128, bs=32, fp8=True), dict(hk=2, d=64, bs=32)], ids=str)
+@pytest.mark.parametrize("ctx", [[500, 90, 4], [505, 88, 61], [511, 57, 73]])
+def test_freed_blocks_before_a_window_are_not_looked_at(kw, ctx):
+    c = Cache(ctx=ctx, hq=8, q_len=2, **kw)
+    bs = kw["bs"]
     want = c.reference(hide(40))
     tab = c.tab.copy()
     raw = c.pool.raw_bytes()
     for b in range(3):
-        lo = max(0, c.ctx[b] - 2 - 40 + 1) // 16
+        lo = max(0, c.ctx[b] - 2 - 40 + 1) // bs
         for j in range(lo):
             for t in raw:
                 t[tab[b, j]] = 0xFF
@@ -152,11 +156,27 @@ def test_padded_batch_bad_lengths_and_bad_blocks():
     assert c.pool.device_errors() & kp.DEVERR_CONTEXT
     c.lens = i32([40, 0, 33])
     tab = c.tab.copy()
-    tab[0, 1] = -7
+    tab[0, 1] = -7            # the second half of a 32-token piece of work
     c.tables = i32(tab)
     got = run(c)
     assert c.pool.device_errors() == kp.DEVERR_BLOCK_ID
     c.check(*got, c.reference(lambda b, pos, t: (t > pos) | ((b == 0) & (t // 16 == 1))))
+    c.pool.destroy()
+
+
+@pytest.mark.parametrize("kw", [dict(hk=2, d=64, bs=16), dict(hk=4, d=128, bs=16, fp8=True), dict(hk=4, d=128, bs=32, fp8=True),
+                                dict(hk=1, d=128, bs=16)], ids=str)
+def test_bad_blocks_anywhere_are_skipped(kw):
+    c = Cache(ctx=[200, 77], hq=8, q_len=3, **kw)
+    bs = kw["bs"]
+    bad = {(0, 0), (0, 3), (0, 5), (1, 1), (1, 2)}
+    tab = c.tab.copy()
+    for i, (b, j) in enumerate(bad):
+        tab[b, j] = [-1, 10 ** 6, c.nb][i % 3]
+    c.tables = i32(tab)
+    out = run(c, prefix_lens=i32([0, 0]))
+    assert c.pool.device_errors() == kp.DEVERR_BLOCK_ID
+    c.check(*out, c.reference(lambda b, pos, t: (t > pos) | np.isin(t // bs, [j for bb, j in bad if bb == b])))
     c.pool.destroy()
 
 
