@@ -242,6 +242,55 @@ struct SpanWalk {
     }
 };
 
+__device__ __forceinline__ int ticket_add(int* ticket)
+{
+    int old;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(ticket) : "memory");
+    return old;
+}
+
+// The queries' MMA operand (load_q_frags) from rows in shared memory.  An 8-bit cache takes 32
+// consecutive numbers of a row per thread: four vector loads instead of load_q_frags' 32 scalars.
+template <bool FP8, int D, int TOK, int NT>
+__device__ __forceinline__ float load_q_staged(uint32_t (&qf)[D / 16][NT / 8][2], const uint8_t* rows, int nh, int lane,
+                                               float scale_log2, const float* k_scale, int kvh)
+{
+    if constexpr (!FP8) {
+        return load_q_frags<FP8, D, TOK, NT>(qf, reinterpret_cast<const uint16_t*>(rows), nh, lane, scale_log2, k_scale, kvh);
+    } else {
+        // as in load_q_frags: a power-of-two scale keeps max|q| below 2^15, undone in the factor
+        uint32_t x[NT / 8][16];
+        uint32_t big = 0;
+#pragma unroll
+        for (int nt = 0; nt < NT / 8; ++nt) {
+            const int hl = nt * 8 + (lane >> 2);
+            const uint32_t at = smem_u32(rows) + hl * (D * 2) + (lane & 3) * 64;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 v = hl < nh ? lds128(at + i * 16) : make_uint4(0u, 0u, 0u, 0u);
+                x[nt][4 * i] = v.x, x[nt][4 * i + 1] = v.y, x[nt][4 * i + 2] = v.z, x[nt][4 * i + 3] = v.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) big = max(big, max((x[nt][i] & 0x7fffu) << 16, x[nt][i] & 0x7fff0000u));
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) big = max(big, __shfl_xor_sync(FULL_MASK, big, o));
+        const int shift = max(0, static_cast<int>(big >> 23) - 126 - 15);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+#pragma unroll
+        for (int nt = 0; nt < NT / 8; ++nt)
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t v = x[nt][2 * ks + e];
+                    qf[ks][nt][e] = pack_f16x2(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xffff0000u) * down);
+                }
+        return scale_log2 * up * __ldg(k_scale + kvh);
+    }
+}
+
 // Kinds of a stage, in the low bits of its tag.
 constexpr int TAG_KV = 1;             // a sub-block; the boxes that landed in bits 24 ..
 constexpr int TAG_Q = 2;              // the unit's query rows
@@ -620,8 +669,7 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             const uint8_t* st_sm = smem + s * S::HSTAGE;
             last = tag & TAG_LAST;
             if ((tag & 3) == TAG_Q) {
-                rows.sl2 = load_q_frags<FP8, D, TOK, NT>(
-                    qf, reinterpret_cast<const uint16_t*>(st_sm + h * (NT * D * 2)), nh, lane, p.scale_log2, p.k_scale, kvh);
+                rows.sl2 = load_q_staged<FP8, D, TOK, NT>(qf, st_sm + h * (NT * D * 2), nh, lane, p.scale_log2, p.k_scale, kvh);
             } else {
                 const bool mine = WPH == 1 || turn % WPH == warp % WPH;
                 ++turn;
@@ -668,24 +716,22 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     for (int j = 0; j < 2; ++j)
                         ml[own * NT + nt * 8 + 2 * c + j] = make_float2(st.m[nt][j], st.l[nt][j]);
             }
-            __threadfence();                         // partial visible before the ticket
+            // One acquire-release add by lane 0: the other lanes' stores come before it (__syncwarp),
+            // the loads of the last warp after it.
             __syncwarp();
             int last = 0;
             if (lane == 0) {
                 int* ticket = p.tickets + static_cast<size_t>(it.unit) * HC + h;
-                last = atomicAdd(ticket, 1) == parts - 1;
-                if (last) {
-                    *ticket = 0;                     // ready for the next call
-                    __threadfence();
-                }
+                last = ticket_add(ticket) == parts - 1;
+                if (last) *ticket = 0;               // ready for the next call
             }
             last = __shfl_sync(FULL_MASK, last, 0);
             if (!last) continue;
-            __threadfence();
+            __syncwarp();
             // all partials in order (this warp's own among them), so the bits do not depend on
             // which warp is last
             reset_state(st);
-#pragma unroll 1
+#pragma unroll 2
             for (int e = 0; e < parts; ++e) {
                 const size_t at = part(e);
                 float f[C::NTT][2], g[C::NTT][2];
