@@ -265,10 +265,8 @@ kv_status make_span_plan(const kv_pool* pl, int batch, int q_heads, int q_len, i
     p.heads = pl->kv_heads % 4 == 0 ? 4 : pl->kv_heads % 2 == 0 ? 2 : 1;
     p.units = static_cast<long long>(batch) * (pl->kv_heads / p.heads) * p.head_groups;
     if (p.units > (1 << 28)) return KV_ERR_UNSUPPORTED;
-    const int tokens = kvp::span_tokens(pl->dtype == KV_DTYPE_FP8_E4M3, pl->head_dim);
-    p.least = split_tokens > 0 ? (split_tokens + tokens - 1) / tokens : kSpanLeast;
-    // (a span of whole blocks may begin and end inside a sub-block)
-    const long long subs = static_cast<long long>(span_blocks) * pl->block_size / tokens + 2 + kvp::SPAN_PAD;
+    p.least = split_tokens > 0 ? split_tokens / 16 : kSpanLeast;
+    const long long subs = static_cast<long long>(span_blocks) * (pl->block_size / 16) + kvp::SPAN_PAD;
     const long long most = (p.units * subs + p.least - 1) / p.least;
     const long long resident = static_cast<long long>(pl->num_sms) * kvp::SPAN_CTAS;
     p.ctas = static_cast<int>(most < resident ? most : resident);

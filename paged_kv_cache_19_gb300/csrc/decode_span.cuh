@@ -11,8 +11,8 @@
 // sequence's keys behind the blocks that its group shares and takes the pieces that the shared
 // pass left for its rows (prefix_groups.cuh) into the merge.
 //
-// A unit is (sequence, group of HC kv heads, tile of query rows) with the sub-blocks (16 or 32
-// tokens) its rows see.  Windows, document starts and shared parts make the units of a batch short and unequal,
+// A unit is (sequence, group of HC kv heads, tile of query rows) with the 16-token sub-blocks its
+// rows see.  Windows, document starts and shared parts make the units of a batch short and unequal,
 // so the grid is persistent -- the CTAs that are resident together -- and the units' sub-blocks,
 // each unit preceded by SPAN_PAD positions for what starting and finishing it costs, are cut into
 // equal contiguous ranges, one per CTA.
@@ -53,7 +53,7 @@ __device__ __forceinline__ float capped_tanh(float y)
 }
 
 // The rule of the rows of a thread's accumulator columns, positions absolute.
-template <int NTT, int RULE, bool BOXED>
+template <int NTT, int RULE>
 struct SpanRows {
     static constexpr bool CAP = RULE == SPAN_CAP || RULE == SPAN_CAP_BIAS;
     static constexpr bool BIAS = RULE == SPAN_BIAS || RULE == SPAN_CAP_BIAS;
@@ -62,31 +62,23 @@ struct SpanRows {
     int pos[NTT][2];
     float sl2, cap_in, cap_log2;      // tanh argument: score * sl2 * cap_in = 2 log2(e) x / cap
     int tile_lo, tile_hi;             // keys that some row of the tile sees
-    int base;                         // position of the sub-block's first token
-    int box_lo, box_hi;               // its tokens that have landed (BOXED: it has two boxes)
+    int base;                         // position of the block's first token
     __device__ __forceinline__ float logit(float s, int tok, int nt, int j) const
     {
         const int t = base + tok;
         float x = s * sl2;
         if constexpr (CAP) x = cap_log2 * capped_tanh(x * cap_in);
         if constexpr (BIAS) x -= slope[nt][j] * static_cast<float>(abs(pos[nt][j] - t));
-        const bool landed = !BOXED || (t >= box_lo && t < box_hi);
-        return t >= lo[nt][j] && t < hi[nt][j] && landed ? x : -INFINITY;
+        return t >= lo[nt][j] && t < hi[nt][j] ? x : -INFINITY;
     }
-    __device__ __forceinline__ int value_lo() const { return (BOXED ? max(tile_lo, box_lo) : tile_lo) - base; }
-    __device__ __forceinline__ int value_hi() const { return (BOXED ? min(tile_hi, box_hi) : tile_hi) - base; }
+    __device__ __forceinline__ int value_lo() const { return tile_lo - base; }
+    __device__ __forceinline__ int value_hi() const { return tile_hi - base; }
 };
 
-constexpr int SPAN_BOX = 16;          // tokens of a TMA box
-
-// Tokens of a sub-block: 32 where 16 tokens of a kv head are only 2 KB (an 8-bit cache, or head_dim
-// 64): the two 16-token tiles are independent work for a warp whose time is latency, and the cost of
-// a stage is paid half as often.
-template <bool FP8, int D>
-constexpr int span_tok() { return FP8 || D == 64 ? 32 : 16; }
+constexpr int SPAN_TOK = 16;          // tokens of a sub-block
 
 // The keys of one sequence.
-template <int RULE, int TOK>
+template <int RULE>
 struct SpanSeq {
     int ctx, first, visible, group;   // group: whose shared pass holds the keys before first, or -1
     __device__ __forceinline__ void load(const SpanParams& sp, int b, bool flag)
@@ -138,8 +130,8 @@ struct SpanSeq {
     {
         int lo, hi;
         tile_keys(sp, hg, nt, lo, hi);
-        sub = lo / TOK;
-        return hi > lo ? (hi + TOK - 1) / TOK - sub : 0;
+        sub = lo / SPAN_TOK;
+        return hi > lo ? (hi + SPAN_TOK - 1) / SPAN_TOK - sub : 0;
     }
 };
 
@@ -151,20 +143,19 @@ struct SpanRange {
 };
 
 // A run of sub-blocks of one unit.
-template <int RULE, int TOK>
+template <int RULE>
 struct SpanItem {
-    SpanSeq<RULE, TOK> seq;
+    SpanSeq<RULE> seq;
     int b, kg, hg, unit;              // sequence, group of kv heads, row tile; -1: no more items
-    int lo, hi;                       // keys that some row of the tile sees
     int sub0, n;                      // sub-blocks [sub0, sub0 + n) of the sequence
     int split, nsplit;                // which of the unit's pieces this is
     int range0;                       // range of its first piece
 };
 
 // Walks the units of a CTA's range.
-template <int RULE, int TOK, int NT, int HC>
+template <int RULE, int NT, int HC>
 struct SpanWalk {
-    SpanSeq<RULE, TOK> seq;
+    SpanSeq<RULE> seq;
     long long lo, hi, total, at;      // at: position of the current unit
     int b, kg, hg, ranges;
     bool pending;                     // the sequence of the next unit is not loaded yet
@@ -193,16 +184,15 @@ struct SpanWalk {
     {
         return static_cast<int>(((pos + 1) * ranges - 1) / total);
     }
-    __device__ __forceinline__ bool next(const SpanParams& sp, SpanItem<RULE, TOK>& it)
+    __device__ __forceinline__ bool next(const SpanParams& sp, SpanItem<RULE>& it)
     {
         while (at < hi) {
             if (pending) {
                 seq.load(sp, b, false);
                 pending = false;
             }
-            int sub, key_lo, key_hi;
+            int sub;
             const int n = seq.tile_subs(sp, hg, NT, sub);
-            seq.tile_keys(sp, hg, NT, key_lo, key_hi);
             const long long first = at + SPAN_PAD, end = first + n;
             const long long a = max(lo, first), z = min(hi, end);
             const bool mine = n > 0 ? a < z : at >= lo;
@@ -211,8 +201,6 @@ struct SpanWalk {
                 it.b = b;
                 it.kg = kg;
                 it.hg = hg;
-                it.lo = key_lo;
-                it.hi = key_hi;
                 it.unit = (b * (sp.d.kv_heads / HC) + kg) * sp.d.head_groups + hg;
                 it.split = 0;
                 it.nsplit = 1;
@@ -251,12 +239,12 @@ __device__ __forceinline__ int ticket_add(int* ticket)
 
 // The queries' MMA operand (load_q_frags) from rows in shared memory.  An 8-bit cache takes 32
 // consecutive numbers of a row per thread: four vector loads instead of load_q_frags' 32 scalars.
-template <bool FP8, int D, int TOK, int NT>
+template <bool FP8, int D, int NT>
 __device__ __forceinline__ float load_q_staged(uint32_t (&qf)[D / 16][NT / 8][2], const uint8_t* rows, int nh, int lane,
                                                float scale_log2, const float* k_scale, int kvh)
 {
     if constexpr (!FP8) {
-        return load_q_frags<FP8, D, TOK, NT>(qf, reinterpret_cast<const uint16_t*>(rows), nh, lane, scale_log2, k_scale, kvh);
+        return load_q_frags<FP8, D, SPAN_TOK, NT>(qf, reinterpret_cast<const uint16_t*>(rows), nh, lane, scale_log2, k_scale, kvh);
     } else {
         // as in load_q_frags: a power-of-two scale keeps max|q| below 2^15, undone in the factor
         uint32_t x[NT / 8][16];
@@ -292,7 +280,8 @@ __device__ __forceinline__ float load_q_staged(uint32_t (&qf)[D / 16][NT / 8][2]
 }
 
 // Kinds of a stage, in the low bits of its tag.
-constexpr int TAG_KV = 1;             // a sub-block; the boxes that landed in bits 24 ..
+constexpr int TAG_SKIP = 0;           // a sub-block of an invalid block: nothing landed
+constexpr int TAG_KV = 1;             // a sub-block
 constexpr int TAG_Q = 2;              // the unit's query rows
 constexpr int TAG_PIECE = 3;          // rows [a, b) of a piece: a, b in bits 8 .., 16 ..; the heads that
 constexpr int TAG_LAST = 4;           // have it in bits 24 ..
@@ -314,9 +303,9 @@ struct PieceRows {
 // out_scale: the factor that takes its outputs to the state's units.
 template <bool FP8, int D, int NT>
 __device__ __forceinline__ void fold_piece(const float* o, const float* lse, int a, int b, float out_scale,
-                                           WarpState<DecodeCfg<FP8, D, span_tok<FP8, D>(), NT>>& st, int lane)
+                                           WarpState<DecodeCfg<FP8, D, SPAN_TOK, NT>>& st, int lane)
 {
-    using C = DecodeCfg<FP8, D, span_tok<FP8, D>(), NT>;
+    using C = DecodeCfg<FP8, D, SPAN_TOK, NT>;
     const int r = lane >> 2;
 #pragma unroll
     for (int nt = 0; nt < C::NTT; ++nt)
@@ -343,9 +332,8 @@ __device__ __forceinline__ void fold_piece(const float* o, const float* lse, int
 }
 
 template <bool FP8, int D, int NT, int HC>
-struct SpanCfg : DecodeCfg<FP8, D, span_tok<FP8, D>(), NT> {
-    static constexpr int TOK = span_tok<FP8, D>();
-    using C = DecodeCfg<FP8, D, TOK, NT>;
+struct SpanCfg : DecodeCfg<FP8, D, SPAN_TOK, NT> {
+    using C = DecodeCfg<FP8, D, SPAN_TOK, NT>;
     static constexpr int NCW = 4;                   // consumer warps
     static constexpr int WPH = NCW / HC;            // of one kv head
     static constexpr int THREADS = (NCW + 1) * 32;
@@ -368,9 +356,8 @@ __global__ void __launch_bounds__(SpanCfg<FP8, D, NT, HC>::THREADS, SpanCfg<FP8,
 paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                   const SpanParams sp)
 {
+    using C = DecodeCfg<FP8, D, SPAN_TOK, NT>;
     using S = SpanCfg<FP8, D, NT, HC>;
-    using C = typename S::C;
-    constexpr int TOK = S::TOK;
     constexpr int NST = S::NST, THREADS = S::THREADS, NCW = S::NCW, WPH = S::WPH, QUEUE = S::QUEUE;
     constexpr bool SUFFIX = RULE == SPAN_SUFFIX;
     const DecodeParams& p = sp.d;
@@ -380,7 +367,7 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         SpanRange range;
         long long scan[THREADS / 32];
         int tag[NST];                                // what the stage holds
-        SpanItem<RULE, TOK> queue[QUEUE];
+        SpanItem<RULE> queue[QUEUE];
     };
     static_assert(sizeof(Ctl) <= S::CTL, "control block");
     extern __shared__ uint8_t smem_raw[];
@@ -418,7 +405,7 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         const auto positions = [&](int b) {
             long long w = 0;
             if (b < p.batch) {
-                SpanSeq<RULE, TOK> s;
+                SpanSeq<RULE> s;
                 s.load(sp, b, blockIdx.x == 0);
                 int sub;
                 for (int t = 0; t < p.head_groups; ++t) w += s.tile_subs(sp, t, NT, sub) + SPAN_PAD;
@@ -471,22 +458,18 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
 
     // ------------------------------------------------------------ producer warp
     if (warp == NCW) {
-        SpanWalk<RULE, TOK, NT, HC> walk;
+        SpanWalk<RULE, NT, HC> walk;
         walk.init(sp, ctl->range, total, ranges);
-        constexpr int BOXES = TOK / SPAN_BOX;        // of a sub-block and head
-        const int per_block = sp.block_size / SPAN_BOX;                 // boxes of a block: 1 or 2
-        // lane i < 2 HC BOXES loads box i % BOXES of the K (first HC BOXES lanes) or V tile of kv head
-        // kg * HC + i / BOXES % HC
-        constexpr int LOADS = 2 * HC * BOXES;
-        const int my_h = lane / BOXES % HC, my_box = lane % BOXES;
-        const CUtensorMap* my_map = lane < HC * BOXES ? &tmk : &tmv;
-        const uint32_t my_off = static_cast<uint32_t>((lane < HC * BOXES ? 0 : HC * C::TILE) + my_h * C::TILE +
-                                                      my_box * (C::TILE / BOXES));
+        const int per_block = sp.block_size / SPAN_TOK;                 // 1 or 2
+        // lane i < 2 HC loads the K (i < HC) or V tile of kv head kg * HC + i % HC
+        const int my_h = lane % HC;
+        const CUtensorMap* my_map = lane < HC ? &tmk : &tmv;
+        const uint32_t my_off = static_cast<uint32_t>((lane < HC ? 0 : HC * C::TILE) + my_h * C::TILE);
         int ids = -1, ids_b = -1, ids_at = 0;        // table entries ids_at .. ids_at + 31 of sequence ids_b
         int n = 0;                                   // stages issued
         bool ok = true;
         for (int k = 0; ok; ++k) {
-            SpanItem<RULE, TOK> it;
+            SpanItem<RULE> it;
             const bool more = walk.next(sp, it);
             if (!more) it.b = -1;
             const int slot = k % QUEUE;
@@ -565,29 +548,24 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             ++n;
             // ---- the sub-blocks
             for (int i = 0; i < it.n; ++i) {
-                // the boxes of this sub-block: the first may lie before the keys, the last behind
-                const int box0 = (it.sub0 + i) * BOXES;
-                const int entry0 = per_block == 2 ? box0 >> 1 : box0;
-                const int entry1 = per_block == 2 ? (box0 + BOXES - 1) >> 1 : box0 + BOXES - 1;
-                if (ids_b != it.b || entry0 < ids_at || entry1 >= ids_at + 32) {
+                const int sub = it.sub0 + i;
+                const int entry = per_block == 2 ? sub >> 1 : sub;
+                if (ids_b != it.b || entry < ids_at || entry >= ids_at + 32) {
                     ids_b = it.b;
-                    ids_at = entry0;
-                    const int j = entry0 + lane;
+                    ids_at = entry;
+                    const int j = entry + lane;
                     ids = j < p.max_blocks ? __ldg(p.tables + static_cast<size_t>(it.b) * p.max_blocks + j) : -1;
                 }
-                const int box = box0 + my_box;
-                const int blk = __shfl_sync(FULL_MASK, ids, (per_block == 2 ? box >> 1 : box) - ids_at);
-                const bool wanted = box * SPAN_BOX < it.hi && (box + 1) * SPAN_BOX > it.lo;
-                const bool good = wanted && blk >= 0 && blk < p.num_blocks;
-                if (wanted && !good && lane < BOXES) atomicOr(p.err, KV_DEVERR_BLOCK_ID);     // skipped: never addressed
-                const uint32_t have = __ballot_sync(FULL_MASK, good) & ((1u << BOXES) - 1u);
+                const int blk = __shfl_sync(FULL_MASK, ids, entry - ids_at);
+                const bool good = blk >= 0 && blk < p.num_blocks;
+                if (!good && lane == 0) atomicOr(p.err, KV_DEVERR_BLOCK_ID);    // skipped: never addressed
                 if (i + 1 == it.n) count_pieces();
-                ok = arm(TAG_KV | (i + 1 == it.n && pieces == 0 ? TAG_LAST : 0) | static_cast<int>(have << 24),
-                         static_cast<uint32_t>(__popc(have)) * (S::HSTAGE / BOXES));
+                ok = arm((good ? TAG_KV : TAG_SKIP) | (i + 1 == it.n && pieces == 0 ? TAG_LAST : 0),
+                         good ? static_cast<uint32_t>(S::HSTAGE) : 0u);
                 if (!ok) break;
-                if (good && lane < LOADS)
+                if (good && lane < 2 * HC)
                     tma_load_5d(stage() + my_off, my_map, 0, 0, it.kg * HC + my_h,
-                                per_block == 2 ? (box & 1) * SPAN_BOX : 0, blk, bar());
+                                per_block == 2 ? (sub & 1) * SPAN_TOK : 0, blk, bar());
                 ++n;
             }
             if (!ok || pieces == 0) continue;
@@ -630,7 +608,7 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     for (int k = 0;; ++k) {
         ok = all_ok(mbar_wait_bounded(smem_u32(&ctl->item_full[k % QUEUE]), static_cast<uint32_t>(k / QUEUE) & 1u));
         if (!ok) break;
-        const SpanItem<RULE, TOK> it = ctl->queue[k % QUEUE];
+        const SpanItem<RULE> it = ctl->queue[k % QUEUE];
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl->item_empty[k % QUEUE]));
         if (it.b < 0) break;
@@ -638,7 +616,7 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         const int nh = min(NT, p.rows - it.hg * NT);                    // real rows in this tile
         const size_t row0 = (static_cast<size_t>(b) * p.kv_heads + kvh) * p.rows + it.hg * NT;
         uint32_t qf[C::KS][C::NTT][2];
-        SpanRows<C::NTT, RULE, (TOK > SPAN_BOX)> rows;
+        SpanRows<C::NTT, RULE> rows;
         rows.cap_in = sp.cap_in;
         rows.cap_log2 = sp.cap_log2;
         it.seq.tile_keys(sp, it.hg, NT, rows.tile_lo, rows.tile_hi);
@@ -669,17 +647,14 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             const uint8_t* st_sm = smem + s * S::HSTAGE;
             last = tag & TAG_LAST;
             if ((tag & 3) == TAG_Q) {
-                rows.sl2 = load_q_staged<FP8, D, TOK, NT>(qf, st_sm + h * (NT * D * 2), nh, lane, p.scale_log2, p.k_scale, kvh);
+                rows.sl2 = load_q_staged<FP8, D, NT>(qf, st_sm + h * (NT * D * 2), nh, lane, p.scale_log2, p.k_scale, kvh);
             } else {
                 const bool mine = WPH == 1 || turn % WPH == warp % WPH;
                 ++turn;
-                if ((tag & 3) == TAG_KV && mine && (tag >> 24 & 0xff) != 0) {
-                    // a box that is missing: the keys of the others (its memory holds something else)
+                if ((tag & 3) == TAG_KV && mine) {
                     const uint32_t tk = smem_u32(st_sm) + h * C::TILE;
-                    rows.base = sub * TOK;
-                    rows.box_lo = tag >> 24 & 1 ? rows.base : rows.base + SPAN_BOX;
-                    rows.box_hi = tag >> 25 & 1 ? rows.base + TOK : rows.base + SPAN_BOX;
-                    process_block_rows<FP8, D, TOK, NT>(tk, tk + HC * C::TILE, rows, qf, st, lane);
+                    rows.base = sub * SPAN_TOK;
+                    process_block_rows<FP8, D, SPAN_TOK, NT>(tk, tk + HC * C::TILE, rows, qf, st, lane);
                 }
                 if (SUFFIX && (tag & 3) == TAG_PIECE && mine && (tag >> (24 + h) & 1))
                     fold_piece<FP8, D, NT>(reinterpret_cast<const float*>(st_sm + h * C::STAGE),

@@ -90,7 +90,7 @@ struct SpanParams {
     // max_splits and merge_kernel are not used
     DecodeParams d;
     int block_size;
-    int least;                // positions (sub-blocks and SPAN_PAD per unit) of a range at least
+    int least;                // positions (16-token sub-blocks and SPAN_PAD per unit) of a range at least
     int window;               // keys a query sees back from its own position, itself included (0: all)
     float cap_log2, cap_in;   // score cap * log2(e) and 2 / cap; 0 without a cap
     const float* slopes;      // [q_heads] distance bias or null
@@ -101,8 +101,6 @@ struct SpanParams {
 // Positions that the span kernel's partition adds before each unit: what starting and finishing
 // a unit costs, in sub-blocks.
 constexpr int SPAN_PAD = 4;
-// Tokens of its sub-blocks (span_tok in decode_span.cuh).
-inline int span_tokens(bool fp8, int head_dim) { return fp8 || head_dim == 64 ? 32 : 16; }
 // Resident CTAs per SM of the span kernel.
 constexpr int SPAN_CTAS = 2;
 // The rule of the rows: a template argument of the span kernel.
