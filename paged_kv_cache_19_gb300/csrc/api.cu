@@ -247,7 +247,7 @@ struct SpanPlan {
 };
 
 // Least positions of a CTA's range with the automatic choice.
-constexpr int kSpanLeast = 4 + kvp::SPAN_PAD;
+constexpr int kSpanLeast = 2 + kvp::SPAN_PAD;
 
 kv_status make_span_plan(const kv_pool* pl, int batch, int q_heads, int q_len, int max_blocks,
                          int span_blocks, int split_tokens, SpanPlan* out)
@@ -338,9 +338,8 @@ SpanLayout span_layout(const kv_pool* pl, const SpanPlan& p)
     return w;
 }
 
-// The shared prefix pass's part of a workspace (behind the span kernel's): the sequences' shared
-// parts, run entries, log-sum-exps, partial outputs.  Pieces: one per run and one per range
-// border of the grid (one CTA per SM).
+// The shared prefix pass's part of a workspace (behind the span kernel's): run entries, log-sum-exps,
+// partial outputs.  Pieces: one per run and one per range border of the grid (one CTA per SM).
 struct PrefixLayout {
     size_t runs, piece_lse, piece_o, total;
     long long pieces;
@@ -352,8 +351,7 @@ PrefixLayout prefix_layout(const kv_pool* pl, int batch, const SpanPlan& p, int 
     if (n_groups == 0 || batch < 2) return w;
     const long long runs = kvp::prefix_run_slots(batch, pl->kv_heads, p.rows, n_groups);
     w.pieces = runs + pl->num_sms;
-    w.runs = round_up(static_cast<size_t>(batch) * sizeof(int2), kAlign);
-    w.piece_lse = w.runs + round_up(static_cast<size_t>(runs) * sizeof(int2), kAlign);
+    w.piece_lse = round_up(static_cast<size_t>(runs) * sizeof(int2), kAlign);
     w.piece_o = w.piece_lse + static_cast<size_t>(w.pieces) * 256 * sizeof(float4);
     w.total = w.piece_o + static_cast<size_t>(w.pieces) * 256 * pl->head_dim * sizeof(float);
     return w;
@@ -986,7 +984,6 @@ kv_status paged_shared_prefix_attention(const kv_pool* pool, const void* q, int 
     s.group_blocks = group_blocks;
     s.k_scale = pool->k_scale;
     s.v_scale = pool->v_scale;
-    s.seqs = reinterpret_cast<int2*>(ws);
     s.runs = reinterpret_cast<int2*>(ws + l.runs);
     s.piece_lse = reinterpret_cast<float4*>(ws + l.piece_lse);
     s.piece_o = reinterpret_cast<float*>(ws + l.piece_o);

@@ -309,14 +309,6 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         long long units = 0;
         for (int w = 0; w < C::THREADS / 32; ++w) units += ctl->scan[w];
         if (!all) units = 0;
-        // the sequences' shared parts, for the suffix kernel
-        for (int g = all ? blockIdx.x : p.n_groups; g < p.n_groups; g += gridDim.x) {
-            const PrefixGroup gr = load_prefix_group(p, g);
-            for (int m = tid; m < gr.n; m += C::THREADS) p.seqs[gr.off + m] = make_int2(gr.blocks * BS, g);
-        }
-        const int in0 = all ? __ldg(p.group_offsets) : p.batch, in1 = all ? __ldg(p.group_offsets + p.n_groups) : p.batch;
-        for (int b = blockIdx.x * C::THREADS + tid; b < p.batch; b += gridDim.x * C::THREADS)
-            if (b < in0 || b >= in1) p.seqs[b] = make_int2(0, -1);
         const int ctas = units < gridDim.x ? static_cast<int>(units) : static_cast<int>(gridDim.x);
         const int c = blockIdx.x;
         const long long lo = c < ctas ? pfx_div(units * c, ctas) : 0;

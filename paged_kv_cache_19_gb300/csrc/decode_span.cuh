@@ -37,6 +37,7 @@
 
 #include "decode_common.cuh"
 #include "prefix_groups.cuh"
+#include "tcgen05.cuh"
 
 namespace kvp {
 
@@ -81,16 +82,19 @@ constexpr int SPAN_TOK = 16;          // tokens of a sub-block
 template <int RULE>
 struct SpanSeq {
     int ctx, first, visible, group;   // group: whose shared pass holds the keys before first, or -1
-    __device__ __forceinline__ void load(const SpanParams& sp, int b, bool flag)
+    // g: the group that holds the sequence (-1: none), its members and shared blocks (SPAN_SUFFIX)
+    __device__ __forceinline__ void load(const SpanParams& sp, int b, bool flag, int g = -1, int members = 0, int blocks = 0)
     {
         const DecodeParams& p = sp.d;
-        ctx = __ldg(p.ctx + b);
+        // (not through L1: the suffix kernel may start before the shared pass has completed)
+        ctx = __ldcg(p.ctx + b);
         first = visible = 0;
         group = -1;
         if constexpr (RULE == SPAN_SUFFIX) {
-            const int2 s = __ldcg(sp.shared.seqs + b);
-            first = max(0, s.x);
-            group = s.x > 0 ? s.y : -1;
+            if (g >= 0 && prefix_shares(sp.shared, members, blocks)) {
+                first = blocks * sp.block_size;
+                group = g;
+            }
         } else {
             if (sp.first_keys != nullptr) first = max(0, __ldg(sp.first_keys + b));
             if (sp.prefix_lens != nullptr) visible = __ldg(sp.prefix_lens + b);
@@ -140,7 +144,21 @@ struct SpanRange {
     long long lo, hi;
     long long base;                   // position of sequence b0's first unit
     int b0;
+    int g;                            // SPAN_SUFFIX: the group that holds b0, or the next one (the
+                                      // number of groups: none); -1: nothing is shared
 };
+
+// Group of sequence b among n groups whose offsets are in order: -1 outside all of them.
+__device__ __forceinline__ int find_group(const int* off, int n, int b)
+{
+    if (n == 0 || b < off[0] || b >= off[n]) return -1;
+    int lo = 0, hi = n;                                 // off[lo] <= b < off[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        (off[mid] <= b ? lo : hi) = mid;
+    }
+    return lo;
+}
 
 // A run of sub-blocks of one unit.
 template <int RULE>
@@ -158,7 +176,29 @@ struct SpanWalk {
     SpanSeq<RULE> seq;
     long long lo, hi, total, at;      // at: position of the current unit
     int b, kg, hg, ranges;
+    int g, g_end;                     // SPAN_SUFFIX: group of b, or the next one; first sequence behind it
     bool pending;                     // the sequence of the next unit is not loaded yet
+
+    __device__ __forceinline__ void load_seq(const SpanParams& sp)
+    {
+        if constexpr (RULE == SPAN_SUFFIX) {
+            const PrefixParams& s = sp.shared;
+            if (g >= 0) {
+                while (g < s.n_groups && g_end <= b) {
+                    ++g;
+                    if (g < s.n_groups) g_end = __ldcg(s.group_offsets + g + 1);
+                }
+                if (g < s.n_groups) {
+                    const int start = __ldcg(s.group_offsets + g), blocks = __ldcg(s.group_blocks + g);
+                    if (start <= b) {
+                        seq.load(sp, b, false, g, g_end - start, blocks);
+                        return;
+                    }
+                }
+            }
+        }
+        seq.load(sp, b, false);
+    }
 
     __device__ __forceinline__ void init(const SpanParams& sp, const SpanRange& r, long long all, int n_ranges)
     {
@@ -172,7 +212,9 @@ struct SpanWalk {
         if (lo >= hi) return;
         at = r.base;
         b = r.b0;
-        seq.load(sp, b, false);
+        g = r.g;
+        g_end = RULE == SPAN_SUFFIX && g >= 0 && g < sp.shared.n_groups ? __ldcg(sp.shared.group_offsets + g + 1) : 0;
+        load_seq(sp);
         // whole groups of kv heads before the range
         long long per = 0;
         int sub;
@@ -188,7 +230,7 @@ struct SpanWalk {
     {
         while (at < hi) {
             if (pending) {
-                seq.load(sp, b, false);
+                load_seq(sp);
                 pending = false;
             }
             int sub;
@@ -394,8 +436,36 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         prefetch_tensormap(&tmk);
         prefetch_tensormap(&tmv);
     }
-    grid_dependency_wait();                          // inputs of the preceding kernel are ready
+    // Inputs of the preceding kernel are ready.  The suffix form's preceding kernel is the shared
+    // pass, which has waited for the kernels before it when it lets this one launch: only the pieces
+    // it leaves are waited for, before the first is read (and before this CTA ends).
+    if (!SUFFIX) grid_dependency_wait();
     grid_dependents_launch();                        // this grid is resident: the next may launch
+
+    // ---- the groups (suffix form), in the ring's memory until the loads begin
+    const int* off = sp.shared.group_offsets;
+    const int* blocks = sp.shared.group_blocks;
+    bool grouped = false;                            // the offsets are in order
+    if constexpr (SUFFIX) {
+        const int n = sp.shared.n_groups;
+        int* mine = reinterpret_cast<int*>(smem);
+        const bool fits = (2 * static_cast<size_t>(n) + 1) * 4 <= static_cast<size_t>(NST) * S::HSTAGE;
+        bool ok = true;
+        for (int g = tid; g <= n; g += THREADS) {
+            const int a = __ldcg(off + g);
+            if (fits) mine[g] = a;
+            if (g < n) {
+                const int e = __ldcg(off + g + 1);
+                ok = ok && 0 <= a && a <= e && e <= p.batch;
+                if (fits) mine[n + 1 + g] = __ldcg(blocks + g);
+            }
+        }
+        grouped = __syncthreads_and(ok);             // bad offsets: nothing is shared
+        if (fits) {
+            off = mine;
+            blocks = mine + n + 1;
+        }
+    }
 
     // ---- this CTA's range: the positions of all sequences, then the one it begins in.  A round
     // takes one sequence per thread; more than THREADS of them are gone through twice.
@@ -406,7 +476,11 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             long long w = 0;
             if (b < p.batch) {
                 SpanSeq<RULE> s;
-                s.load(sp, b, blockIdx.x == 0);
+                const int g = SUFFIX && grouped ? find_group(off, sp.shared.n_groups, b) : -1;
+                if (SUFFIX && g >= 0)
+                    s.load(sp, b, blockIdx.x == 0, g, off[g + 1] - off[g], blocks[g]);
+                else
+                    s.load(sp, b, blockIdx.x == 0);
                 int sub;
                 for (int t = 0; t < p.head_groups; ++t) w += s.tile_subs(sp, t, NT, sub) + SPAN_PAD;
                 w *= p.kv_heads / HC;
@@ -447,12 +521,17 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             if (base <= lo && lo < base + w) {
                 ctl->range.base = base;
                 ctl->range.b0 = b0 + tid;
+                if (SUFFIX) {
+                    const int g = find_group(off, grouped ? sp.shared.n_groups : 0, b0 + tid);
+                    ctl->range.g = !grouped ? -1 : g >= 0 ? g : b0 + tid < off[0] ? 0 : sp.shared.n_groups;
+                }
             }
         }
         if (tid == 0) {
             ctl->range.lo = lo;
             ctl->range.hi = hi;
         }
+        if (SUFFIX) fence_proxy_async_smem();        // the ring's memory goes to the copies
         __syncthreads();
     }
 
@@ -508,6 +587,7 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             int2 run[SEGS];
             int pieces = 0;                          // stages of pieces
             if (SUFFIX && it.seq.group >= 0 && it.split == 0) {
+                grid_dependency_wait();              // the pieces of the shared pass are there
                 const PrefixGroup gr = load_prefix_group(sp.shared, it.seq.group);
                 const int pairs = prefix_pairs(sp.shared, gr);
                 const int base = prefix_run_base(sp.shared, it.seq.group, gr);
@@ -554,7 +634,7 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     ids_b = it.b;
                     ids_at = entry;
                     const int j = entry + lane;
-                    ids = j < p.max_blocks ? __ldg(p.tables + static_cast<size_t>(it.b) * p.max_blocks + j) : -1;
+                    ids = j < p.max_blocks ? __ldcg(p.tables + static_cast<size_t>(it.b) * p.max_blocks + j) : -1;
                 }
                 const int blk = __shfl_sync(FULL_MASK, ids, entry - ids_at);
                 const bool good = blk >= 0 && blk < p.num_blocks;
@@ -594,6 +674,7 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             }
         }
         if (!ok && lane == 0 && n != p.stop_stage) atomicOr(p.err, KV_DEVERR_TIMEOUT);
+        if (SUFFIX) grid_dependency_wait();          // the grid ends behind the shared pass
         // Drain: the CTA must not exit while a copy into its shared memory is in flight.
         for (int i = max(0, n - NST); i < n; ++i)
             if (!mbar_wait_bounded(smem_u32(&ctl->full[i % NST]), static_cast<uint32_t>(i / NST) & 1u)) break;

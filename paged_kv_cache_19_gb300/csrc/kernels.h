@@ -62,7 +62,6 @@ struct PrefixParams {
     const int32_t* group_blocks;    // [n_groups]
     const float* k_scale;     // [kv_heads] (fp8 cache)
     const float* v_scale;
-    int2* seqs;               // [batch]: tokens of the sequence's shared part, its group
     int2* runs;               // per run slot: first piece, pieces
     float4* piece_lse;        // [piece][2][128]: log-sum-exp in log2 units (first of four), -inf: no key
     float* piece_o;           // [piece][2][128][head_dim], normalised

@@ -22,14 +22,20 @@ struct PrefixGroup {
     int blocks;                            // shared blocks; 0: computed without sharing
 };
 
-// Group g, its block count checked; a single sequence has nobody to share with.
+// Whether a group shares anything: its block count is in range, and a single sequence has nobody to
+// share with.
+__device__ __forceinline__ bool prefix_shares(const PrefixParams& p, int members, int blocks)
+{
+    return members >= 2 && blocks > 0 && blocks <= p.max_blocks;
+}
+
 __device__ __forceinline__ PrefixGroup load_prefix_group(const PrefixParams& p, int g)
 {
     PrefixGroup gr;
     gr.off = __ldg(p.group_offsets + g);
     gr.n = __ldg(p.group_offsets + g + 1) - gr.off;
     const int blocks = __ldg(p.group_blocks + g);
-    gr.blocks = gr.n >= 2 && blocks > 0 && blocks <= p.max_blocks ? blocks : 0;
+    gr.blocks = prefix_shares(p, gr.n, blocks) ? blocks : 0;
     return gr;
 }
 

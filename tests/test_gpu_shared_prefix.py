@@ -145,7 +145,8 @@ def test_bad_groups_share_nothing_and_are_right():
         c.check(*run(c, offsets=off, blocks=blk), want)
         assert c.pool.device_errors() == kp.DEVERR_GROUP
     # groups that cover part of the batch, empty ones among them, or none
-    for off, blk in (([2, 2, 6, 6], [10, 9, 10]), ([7, 10], [6]), ([0], [])):
+    for off, blk in (([2, 2, 6, 6], [10, 9, 10]), ([7, 10], [6]), ([0], []), ([1, 4, 4, 7, 9], [9, 3, 10, 6]),
+                     ([3, 3], [2]), ([10, 10], [1])):
         c.check(*run(c, offsets=off, blocks=np.array(blk, int)), want)
         assert c.pool.device_errors() == 0
     c.pool.destroy()
@@ -155,6 +156,19 @@ def test_more_groups_than_threads():
     groups = [(1 + (i % 3), i % 4) for i in range(700)]
     c = Cache(ctx=batch(groups, 16, 20), hq=2, hk=1, d=64, bs=16, shared=groups)
     c.check(*run(c), c.reference())
+    assert c.pool.device_errors() == 0
+    c.pool.destroy()
+
+
+def test_more_sequences_than_threads_around_the_groups():
+    """Sequences before, between and behind groups, over several rounds of the partition."""
+    groups = [(1, 0)] * 200 + [(3, 5), (1, 2), (170, 2), (2, 9)] + [(1, 1)] * 150
+    c = Cache(ctx=batch(groups, 16, 30), hq=4, hk=4, d=64, bs=16, shared=groups)
+    want = c.reference()
+    c.check(*run(c), want)
+    o = np.array(c.offsets)
+    # only the groups in the middle are named
+    c.check(*run(c, offsets=o[200:205], blocks=c.blocks[200:204]), want)
     assert c.pool.device_errors() == 0
     c.pool.destroy()
 
