@@ -69,10 +69,20 @@ __device__ __forceinline__ float2 bf16x2_floats(uint32_t w)
 
 // Where a token goes.
 struct NraToken {
-    int b, t;                                       // its row block of q_out: sequence or token, query token
-    bool cached;                                    // its block id is valid
-    size_t slot;                                    // first row of its slot in the pool
+    long long q_row;                                // row of q_out of its head 0; < 0: the token writes nothing
+    long long slot;                                 // first row of its slot in the pool; < 0: not cached
 };
+
+__device__ __forceinline__ NraToken nra_token(const NormRopeParams& p, uint32_t i, int pos, int blk)
+{
+    const uint32_t b = i / static_cast<uint32_t>(p.q_len), t = i - b * static_cast<uint32_t>(p.q_len);
+    NraToken tok;
+    tok.q_row = static_cast<long long>(b) * p.q_heads * p.q_len + t;
+    tok.slot = blk >= 0 && blk < p.num_blocks
+                   ? (static_cast<long long>(blk) * p.block_size + pos % p.block_size) * p.kv_heads
+                   : -1;
+    return tok;
+}
 
 // A lane's numbers of a row -- at[0] .. at[0] + 3 and at[1] .. at[1] + 3 -- and how they rotate.
 struct NraLane {
@@ -90,89 +100,105 @@ struct NraLane {
     }
 };
 
-// cos and sin of a lane's four pairs.
+// cos, sin and -sin of a lane's four pairs.
 struct NraTurn {
-    float2 c[2], s[2];
+    float2 c[2], s[2], n[2];
     __device__ __forceinline__ void load(const NormRopeParams& p, const float* row, const NraLane& ln)
     {
         const float4 a = *reinterpret_cast<const float4*>(row + ln.pair);
         const float4 b = *reinterpret_cast<const float4*>(row + p.rope_dim / 2 + ln.pair);
         c[0] = make_float2(a.x, a.y), c[1] = make_float2(a.z, a.w);
         s[0] = make_float2(b.x, b.y), s[1] = make_float2(b.z, b.w);
+        n[0] = make_float2(-b.x, -b.y), n[1] = make_float2(-b.z, -b.w);
     }
 };
 
-// One lane's numbers (x0: at[0] .., x1: at[1] ..) of row r of a token: norm, rotation, store.
-// Uniform in the row's lanes.
-template <int D, bool FP8>
-__device__ __forceinline__ void nra_row(const NormRopeParams& p, const NraToken& tok, const NraLane& ln, const NraTurn& w,
-                                        uint2 x0, uint2 x1, int r, unsigned group_mask)
+// A lane's numbers: y[0], y[1] the first four, y[2], y[3] the others.
+__device__ __forceinline__ void nra_unpack(uint2 x0, uint2 x1, float2 (&y)[4])
 {
-    constexpr int LPR = D / 8;
-    const bool is_q = r < p.q_heads;
-    const bool is_v = r >= p.q_heads + p.kv_heads;
-    const int h = is_q ? r : is_v ? r - p.q_heads - p.kv_heads : r - p.q_heads;
-    float2 y[4];                                    // y[0], y[1]: the first four numbers
-    if (!is_v || FP8) {
-        y[0] = bf16x2_floats(x0.x), y[1] = bf16x2_floats(x0.y);
-        y[2] = bf16x2_floats(x1.x), y[3] = bf16x2_floats(x1.y);
-    }
-    if (!is_v) {
-        const float* weight = is_q ? p.q_weight : p.k_weight;
-        if (weight != nullptr) {
-            const float2 sq = fma2(y[0], y[0], fma2(y[1], y[1], fma2(y[2], y[2], mul2(y[3], y[3]))));
-            float ss = sq.x + sq.y;
+    y[0] = bf16x2_floats(x0.x), y[1] = bf16x2_floats(x0.y);
+    y[2] = bf16x2_floats(x1.x), y[3] = bf16x2_floats(x1.y);
+}
+
+__device__ __forceinline__ void nra_weights(const float* weight, const NraLane& ln, float2 (&g)[4])
+{
+    const float4 g0 = __ldg(reinterpret_cast<const float4*>(weight + ln.at[0]));
+    const float4 g1 = __ldg(reinterpret_cast<const float4*>(weight + ln.at[1]));
+    g[0] = make_float2(g0.x, g0.y), g[1] = make_float2(g0.z, g0.w);
+    g[2] = make_float2(g1.x, g1.y), g[3] = make_float2(g1.z, g1.w);
+}
+
+template <int D>
+__device__ __forceinline__ void nra_norm(float2 (&y)[4], const float2 (&g)[4], float eps, unsigned group_mask)
+{
+    const float2 sq = fma2(y[0], y[0], fma2(y[1], y[1], fma2(y[2], y[2], mul2(y[3], y[3]))));
+    float ss = sq.x + sq.y;
 #pragma unroll
-            for (int o = LPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(group_mask, ss, o);
-            const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-            const float4 g0 = __ldg(reinterpret_cast<const float4*>(weight + ln.at[0]));
-            const float4 g1 = __ldg(reinterpret_cast<const float4*>(weight + ln.at[1]));
-            const float2 inv2 = make_float2(inv, inv);
-            y[0] = mul2(mul2(y[0], inv2), make_float2(g0.x, g0.y));
-            y[1] = mul2(mul2(y[1], inv2), make_float2(g0.z, g0.w));
-            y[2] = mul2(mul2(y[2], inv2), make_float2(g1.x, g1.y));
-            y[3] = mul2(mul2(y[3], inv2), make_float2(g1.z, g1.w));
-        }
-        if (ln.turn) {
-            if (p.interleaved) {
-                // pairs (y[0].x, y[0].y), ..: gathered into first and second numbers and back
-                const float2 a0 = make_float2(y[0].x, y[1].x), b0 = make_float2(y[0].y, y[1].y);
-                const float2 a1 = make_float2(y[2].x, y[3].x), b1 = make_float2(y[2].y, y[3].y);
-                const float2 n0 = make_float2(-b0.x, -b0.y), n1 = make_float2(-b1.x, -b1.y);
-                const float2 p0 = fma2(a0, w.c[0], mul2(n0, w.s[0])), q0 = fma2(b0, w.c[0], mul2(a0, w.s[0]));
-                const float2 p1 = fma2(a1, w.c[1], mul2(n1, w.s[1])), q1 = fma2(b1, w.c[1], mul2(a1, w.s[1]));
-                y[0] = make_float2(p0.x, q0.x), y[1] = make_float2(p0.y, q0.y);
-                y[2] = make_float2(p1.x, q1.x), y[3] = make_float2(p1.y, q1.y);
-            } else {
+    for (int o = D / 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(group_mask, ss, o);
+    float inv;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(ss, 1.f / D, eps)));
+    const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float2 a = y[e], b = y[2 + e], n = make_float2(-b.x, -b.y);
-                    y[e] = fma2(a, w.c[e], mul2(n, w.s[e]));
-                    y[2 + e] = fma2(b, w.c[e], mul2(a, w.s[e]));
-                }
-            }
+    for (int e = 0; e < 4; ++e) y[e] = mul2(mul2(y[e], inv2), g[e]);
+}
+
+__device__ __forceinline__ void nra_rotate(float2 (&y)[4], const NraTurn& w, bool interleaved)
+{
+    if (interleaved) {
+        // pairs (y[0].x, y[0].y), ..: gathered into first and second numbers and back
+        const float2 a0 = make_float2(y[0].x, y[1].x), b0 = make_float2(y[0].y, y[1].y);
+        const float2 a1 = make_float2(y[2].x, y[3].x), b1 = make_float2(y[2].y, y[3].y);
+        const float2 p0 = fma2(b0, w.n[0], mul2(a0, w.c[0])), q0 = fma2(a0, w.s[0], mul2(b0, w.c[0]));
+        const float2 p1 = fma2(b1, w.n[1], mul2(a1, w.c[1])), q1 = fma2(a1, w.s[1], mul2(b1, w.c[1]));
+        y[0] = make_float2(p0.x, q0.x), y[1] = make_float2(p0.y, q0.y);
+        y[2] = make_float2(p1.x, q1.x), y[3] = make_float2(p1.y, q1.y);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float2 a = y[e], b = y[2 + e];
+            y[e] = fma2(b, w.n[e], mul2(a, w.c[e]));
+            y[2 + e] = fma2(a, w.s[e], mul2(b, w.c[e]));
         }
     }
-    if (is_q || !FP8) {
-        uint16_t* dst;
-        if (is_q) {
-            dst = p.q_out + ((static_cast<size_t>(tok.b) * p.q_heads + h) * p.q_len + tok.t) * D;
-        } else {
-            if (!tok.cached) return;
-            dst = reinterpret_cast<uint16_t*>(is_v ? p.v_pool : p.k_pool) + (tok.slot + h) * D;
-        }
-        if (!is_v) {
-            x0 = make_uint2(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y));
-            x1 = make_uint2(pack_bf16x2(y[2].x, y[2].y), pack_bf16x2(y[3].x, y[3].y));
-        }
+}
+
+__device__ __forceinline__ void nra_store(uint16_t* dst, const NraLane& ln, const float2 (&y)[4])
+{
+    *reinterpret_cast<uint2*>(dst + ln.at[0]) = make_uint2(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y));
+    *reinterpret_cast<uint2*>(dst + ln.at[1]) = make_uint2(pack_bf16x2(y[2].x, y[2].y), pack_bf16x2(y[3].x, y[3].y));
+}
+
+__device__ __forceinline__ void nra_store_codes(uint8_t* dst, const NraLane& ln, const float2 (&y)[4], float scale)
+{
+    *reinterpret_cast<uint32_t*>(dst + ln.at[0]) = e4m3_codes4(y[0], y[1], scale);
+    *reinterpret_cast<uint32_t*>(dst + ln.at[1]) = e4m3_codes4(y[2], y[3], scale);
+}
+
+// Key (r < kv_heads) or value row of a cached token whose slot's rows begin at row `slot` of the
+// pool; g: the keys' weights (norm).  Uniform in the row's lanes.
+template <int D, bool FP8>
+__device__ __forceinline__ void nra_kv_row(const NormRopeParams& p, size_t slot, const NraLane& ln, const NraTurn& w, bool norm,
+                                           const float2 (&g)[4], uint2 x0, uint2 x1, int r, unsigned group_mask)
+{
+    const bool is_v = r >= p.kv_heads;
+    const int h = is_v ? r - p.kv_heads : r;
+    uint8_t* pool = is_v ? p.v_pool : p.k_pool;
+    if (is_v && !FP8) {
+        uint16_t* dst = reinterpret_cast<uint16_t*>(pool) + (slot + h) * D;
         *reinterpret_cast<uint2*>(dst + ln.at[0]) = x0;
         *reinterpret_cast<uint2*>(dst + ln.at[1]) = x1;
-    } else if (tok.cached) {
-        const float scale = __ldg((is_v ? p.v_scale : p.k_scale) + h);
-        uint8_t* dst = (is_v ? p.v_pool : p.k_pool) + (tok.slot + h) * D;
-        *reinterpret_cast<uint32_t*>(dst + ln.at[0]) = e4m3_codes4(y[0], y[1], scale);
-        *reinterpret_cast<uint32_t*>(dst + ln.at[1]) = e4m3_codes4(y[2], y[3], scale);
+        return;
     }
+    float2 y[4];
+    nra_unpack(x0, x1, y);
+    if (!is_v) {
+        if (norm) nra_norm<D>(y, g, p.eps, group_mask);
+        if (ln.turn) nra_rotate(y, w, p.interleaved);
+    }
+    if constexpr (FP8)
+        nra_store_codes(pool + (slot + h) * D, ln, y, __ldg((is_v ? p.v_scale : p.k_scale) + h));
+    else
+        nra_store(reinterpret_cast<uint16_t*>(pool) + (slot + h) * D, ln, y);
 }
 
 // Sequence and position of token i, checked; flag: this thread reports what is wrong.  False: the
@@ -230,18 +256,29 @@ __global__ void __launch_bounds__(NRA_THREADS) paged_norm_rope_append_kernel(con
     int seq, pos;
     if (!nra_place(p, i, flag, seq, pos)) return;
     const int blk = __ldg(p.tables + static_cast<size_t>(seq) * p.max_blocks + pos / p.block_size);
-    NraToken tok;
-    tok.b = static_cast<int>(i / static_cast<uint32_t>(p.q_len));
-    tok.t = static_cast<int>(i % static_cast<uint32_t>(p.q_len));
-    tok.cached = blk >= 0 && blk < p.num_blocks;
-    if (!tok.cached && flag) atomicOr(p.err, KV_DEVERR_BLOCK_ID);       // its query row is still computed
-    tok.slot = (static_cast<size_t>(tok.cached ? blk : 0) * p.block_size + pos % p.block_size) * p.kv_heads;
+    const NraToken tok = nra_token(p, i, pos, blk);
+    if (tok.slot < 0 && flag) atomicOr(p.err, KV_DEVERR_BLOCK_ID);      // its query row is still computed
     NraTurn w;
     if (ln.turn && r0 < p.q_heads + p.kv_heads) w.load(p, p.rope + static_cast<size_t>(pos) * p.rope_dim, ln);
+    const bool norm = p.q_weight != nullptr;
 #pragma unroll
     for (int j = 0; j < RPT; ++j) {
-        if (r0 + j >= rows) return;
-        nra_row<D, FP8>(p, tok, ln, w, x0[j], x1[j], r0 + j, group_mask);
+        const int r = r0 + j;
+        if (r >= rows) return;
+        float2 g[4];
+        if (r < p.q_heads) {
+            float2 y[4];
+            nra_unpack(x0[j], x1[j], y);
+            if (norm) {
+                nra_weights(p.q_weight, ln, g);
+                nra_norm<D>(y, g, p.eps, group_mask);
+            }
+            if (ln.turn) nra_rotate(y, w, p.interleaved);
+            nra_store(p.q_out + (tok.q_row + static_cast<long long>(r) * p.q_len) * D, ln, y);
+        } else if (tok.slot >= 0) {
+            if (norm && r < p.q_heads + p.kv_heads) nra_weights(p.k_weight, ln, g);
+            nra_kv_row<D, FP8>(p, tok.slot, ln, w, norm, g, x0[j], x1[j], r - p.q_heads, group_mask);
+        }
     }
 }
 
@@ -257,7 +294,7 @@ constexpr int NRS_STAGES = 16;                      // at most
 
 struct NrsCtl {
     uint64_t full[NRS_STAGES], empty[NRS_STAGES];
-    NraToken tok[NRS_STAGES];                       // b < 0: the token writes nothing
+    NraToken tok[NRS_STAGES];
 };
 
 template <int D, bool FP8>
@@ -315,11 +352,8 @@ paged_norm_rope_append_stream(const NormRopeParams p, int stage_bytes, int stage
                 const uint32_t i = base + k;
                 const uint32_t bar = smem_u32(&ctl.full[s]);
                 if (lane == 0) {
-                    NraToken tok;
-                    tok.b = tseq >= 0 ? static_cast<int>(i / static_cast<uint32_t>(p.q_len)) : -1;
-                    tok.t = static_cast<int>(i % static_cast<uint32_t>(p.q_len));
-                    tok.cached = tblk >= 0;
-                    tok.slot = (static_cast<size_t>(max(tblk, 0)) * p.block_size + tpos % p.block_size) * p.kv_heads;
+                    NraToken tok = nra_token(p, i, tpos, tblk);
+                    if (tseq < 0) tok.q_row = -1;
                     ctl.tok[s] = tok;
                     if (tseq >= 0)
                         mbar_arrive_expect_tx(bar, q_bytes + 2 * kv_bytes + rope_bytes);
@@ -352,9 +386,16 @@ paged_norm_rope_append_stream(const NormRopeParams p, int stage_bytes, int stage
     NraLane ln;
     ln.init(p, lane % LPR);
     const unsigned group_mask = ((1u << LPR) - 1u) << (lane / LPR * LPR);
-    const int rows = p.q_heads + 2 * p.kv_heads;
     constexpr int GPC = NRS_CW * 32 / LPR;          // rows in hand at a time
     const int count = static_cast<int>(hi - lo);
+    const int group = threadIdx.x / LPR;
+    const bool norm = p.q_weight != nullptr;
+    float2 gq[4], gk[4];
+    if (norm) {
+        nra_weights(p.q_weight, ln, gq);
+        nra_weights(p.k_weight, ln, gk);
+    }
+    const long long q_step = static_cast<long long>(p.q_len) * D;
     for (int n = 0; n < count; ++n) {
         const int s = n % stages;
         if (!all_ok(mbar_wait_bounded(smem_u32(&ctl.full[s]), static_cast<uint32_t>(n / stages) & 1u))) {
@@ -362,14 +403,24 @@ paged_norm_rope_append_stream(const NormRopeParams p, int stage_bytes, int stage
             break;
         }
         const NraToken tok = ctl.tok[s];
-        if (tok.b >= 0) {
+        if (tok.q_row >= 0) {
             const uint8_t* st = ring + static_cast<size_t>(s) * stage_bytes;
             NraTurn w;
             if (ln.turn) w.load(p, reinterpret_cast<const float*>(st + q_bytes + 2 * kv_bytes), ln);
-            for (int r = threadIdx.x / LPR; r < rows; r += GPC) {
-                const uint16_t* x = reinterpret_cast<const uint16_t*>(st) + r * D;
-                nra_row<D, FP8>(p, tok, ln, w, *reinterpret_cast<const uint2*>(x + ln.at[0]),
-                                *reinterpret_cast<const uint2*>(x + ln.at[1]), r, group_mask);
+            const uint16_t* x = reinterpret_cast<const uint16_t*>(st) + group * D;
+            uint16_t* dst = p.q_out + tok.q_row * D + group * q_step;
+            for (int r = group; r < p.q_heads; r += GPC, x += GPC * D, dst += GPC * q_step) {
+                float2 y[4];
+                nra_unpack(*reinterpret_cast<const uint2*>(x + ln.at[0]), *reinterpret_cast<const uint2*>(x + ln.at[1]), y);
+                if (norm) nra_norm<D>(y, gq, p.eps, group_mask);
+                if (ln.turn) nra_rotate(y, w, p.interleaved);
+                nra_store(dst, ln, y);
+            }
+            if (tok.slot >= 0) {
+                x = reinterpret_cast<const uint16_t*>(st + q_bytes) + group * D;
+                for (int r = group; r < 2 * p.kv_heads; r += GPC, x += GPC * D)
+                    nra_kv_row<D, FP8>(p, tok.slot, ln, w, norm, gk, *reinterpret_cast<const uint2*>(x + ln.at[0]),
+                                       *reinterpret_cast<const uint2*>(x + ln.at[1]), r, group_mask);
             }
         }
         __syncwarp();
