@@ -2,13 +2,15 @@
 
 The functions mirror the C ABI in include/kv_paged.h, include/kv_mla.h and
 include/kv_block_manager.h one to one and only
-marshal arguments (torch tensors -> device pointers, the current stream).
+marshal arguments (torch tensors -> device pointers, the current stream); those of the calls
+that a step makes once per layer do it natively (binding/calls.cpp).
 Every step of the computation runs in the library's CUDA kernels; there is no
 CPU path, and importing a function without the built library raises.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import threading
 
@@ -61,12 +63,6 @@ class _BlockCopy(ctypes.Structure):
     _fields_ = [("src", ctypes.c_int32), ("dst", ctypes.c_int32)]
 
 
-class _AttentionMask(ctypes.Structure):
-    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32),
-                ("alibi_slopes", ctypes.c_void_p), ("first_keys", ctypes.c_void_p),
-                ("prefix_lens", ctypes.c_void_p)]
-
-
 class KVError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -114,7 +110,7 @@ def load_library():
                                              P], I),
             "paged_multi_query_workspace_size": ([P, I, I, I, I, I, ctypes.POINTER(S)], I),
             "paged_attention_masked": ([P, P, I, I, P, I, P, I, ctypes.c_float,
-                                        ctypes.POINTER(_AttentionMask), I, P, S, P, P, P], I),
+                                        P, I, P, S, P, P, P], I),
             "paged_attention_masked_workspace_size": ([P, I, I, I, I, I, I, ctypes.POINTER(S)], I),
             "paged_shared_prefix_attention": ([P, P, I, I, P, I, P, I, P, P, I, ctypes.c_float, I, P, S,
                                                P, P, P], I),
@@ -175,15 +171,16 @@ def _pool_stream(stream, pool) -> int | None:
     return _stream(stream)
 
 
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_binding = None
 
 
-def _at(t, dtype, n, name) -> int:
-    """Address of a contiguous CUDA tensor of n numbers."""
-    if t.dtype is not dtype or not t.is_contiguous() or not t.is_cuda or t.numel() != n:
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} {dtype} numbers, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
-    return t.data_ptr()
+def _native():
+    """The native binding of the per-layer calls (built beside the library)."""
+    global _binding
+    if _binding is None:
+        load_library()
+        _binding = importlib.import_module(__name__ + "._calls")
+    return _binding
 
 
 def _need(t, dtype, name):
@@ -304,17 +301,6 @@ def paged_kv_append(pool: Pool, k_new, v_new, block_tables, context_lens=None, t
                                _ptr(context_lens), int(batch), _stream(stream)), "paged_kv_append")
 
 
-def _rows(t, n, heads, d, name) -> int:
-    """Token stride of a [n, heads, d] bf16 tensor whose token rows are contiguous."""
-    shape, st = t.shape, t.stride()
-    if t.dtype is not _BF16 or not t.is_cuda or len(shape) != 3 or shape[0] != n or shape[1] != heads or shape[2] != d:
-        raise ValueError(f"{name} must be a CUDA bf16 tensor [{n}, {heads}, {d}], got "
-                         f"{t.dtype} {tuple(shape)} on {t.device}")
-    if st[2] != 1 or (heads > 1 and st[1] != d):
-        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {st}")
-    return st[0] if n > 1 else heads * d
-
-
 def paged_norm_rope_append(pool: Pool, q, k, v, block_tables, context_lens=None, q_weight=None,
                            k_weight=None, eps: float = 1e-6, rope_table=None,
                            interleaved: bool = False, q_len: int = 1, token_seq=None,
@@ -325,27 +311,13 @@ def paged_norm_rope_append(pool: Pool, q, k, v, block_tables, context_lens=None,
     q [T, Hq, d], k and v [T, Hkv, d]: bf16, rows of a token contiguous, any token stride (slices
     of one fused projection).  Tokens are addressed as in paged_kv_append, q_len per sequence.
     Returns the queries [T / q_len, Hq, q_len, d] ([T, Hq, d] for q_len 1 when out is not given)."""
-    lib = _lib or load_library()
-    n, heads, d = q.shape
-    kv = pool.kv_heads
-    qs, ks, vs = _rows(q, n, heads, pool.head_dim, "q"), _rows(k, n, kv, d, "k"), _rows(v, n, kv, d, "v")
-    batch, max_blocks = block_tables.shape
-    if n % q_len:
-        raise ValueError("the tokens must be q_len per sequence")
     if out is None:
-        out = torch.empty((n, heads, d) if q_len == 1 else (n // q_len, heads, q_len, d), dtype=_BF16, device=q.device)
-    positions, rope_dim = rope_table.shape if rope_table is not None else (0, 0)
-    status = lib.paged_norm_rope_append(
-        pool.handle, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, heads, n,
-        None if q_weight is None else _at(q_weight, _F32, d, "q_weight"),
-        None if k_weight is None else _at(k_weight, _F32, d, "k_weight"), eps,
-        None if rope_table is None else _at(rope_table, _F32, positions * rope_dim, "rope_table"),
-        positions, rope_dim, int(interleaved),
-        None if token_seq is None else _at(token_seq, _I32, n, "token_seq"),
-        None if token_pos is None else _at(token_pos, _I32, n, "token_pos"),
-        _at(block_tables, _I32, batch * max_blocks, "block_tables"), max_blocks,
-        None if context_lens is None else _at(context_lens, _I32, batch, "context_lens"), batch, q_len,
-        _at(out, _BF16, n * heads * d, "out"), _pool_stream(stream, pool))
+        n, heads, d = q.shape
+        out = torch.empty((n, heads, d) if q_len == 1 else (n // q_len, heads, q_len, d), dtype=torch.bfloat16,
+                          device=q.device)
+    status = (_binding or _native()).norm_rope_append(
+        pool._h.value, pool.head_dim, pool.kv_heads, q, k, v, block_tables, context_lens, q_weight, k_weight, eps,
+        rope_table, interleaved, q_len, token_seq, token_pos, out, _pool_stream(stream, pool))
     if status:
         raise KVError(status, "paged_norm_rope_append")
     return out
@@ -524,26 +496,9 @@ def paged_attention_masked_workspace_size(pool: Pool, batch: int, q_heads: int, 
     return n.value
 
 
-def _queries(pool, q, block_tables):
-    """Sizes of an attention call over q [B, Hq, q_len, d] or [B, Hq, d]: (batch, heads, q_len, blocks)."""
-    shape = q.shape
-    batch, max_blocks = block_tables.shape
-    if len(shape) not in (3, 4) or shape[-1] != pool.head_dim or shape[0] != batch:
-        raise ValueError(f"q must be [batch, q_heads, {pool.head_dim}] or [batch, q_heads, q_len, {pool.head_dim}] "
-                         f"and block_tables hold one row per sequence, got {tuple(shape)} and {tuple(block_tables.shape)}")
-    return batch, shape[1], shape[2] if len(shape) == 4 else 1, max_blocks
-
-
-def _workspace(workspace, need, q):
-    """Address and size of the caller's workspace, or of a zeroed one of need() bytes kept until
-    the call is enqueued (the caching allocator orders its reuse on the stream)."""
-    if workspace is None:
-        n = need()
-        workspace = torch.zeros(n, dtype=torch.uint8, device=q.device) if n else None
-        if workspace is None:
-            return None, 0, None
-    n = workspace.numel()
-    return _at(workspace, torch.uint8, n, "workspace"), n, workspace
+def _zeroed(need: int, q):
+    """A workspace for one call (the caching allocator orders its reuse on the stream)."""
+    return torch.zeros(need, dtype=torch.uint8, device=q.device) if need else None
 
 
 def paged_attention_masked(pool: Pool, q, block_tables, context_lens, scale: float,
@@ -554,23 +509,15 @@ def paged_attention_masked(pool: Pool, q, block_tables, context_lens, scale: flo
     softcap)), a sliding window, a bias by distance (alibi_slopes float32 [Hq]), a first visible
     key per sequence (first_keys int32 [B]) and a prefix every query sees (prefix_lens int32
     [B]); q bf16 [B, Hq, d] or [B, Hq, q_len, d].  Returns out (shaped like q)."""
-    lib = _lib or load_library()
-    batch, heads, q_len, max_blocks = _queries(pool, q, block_tables)
     if out is None:
         out = torch.empty_like(q)
-    rows = batch * heads * q_len
-    ws, ws_bytes, keep = _workspace(workspace, lambda: paged_attention_masked_workspace_size(
-        pool, batch, heads, q_len, max_blocks, window, kv_split_tokens), q)
-    mask = _AttentionMask(softcap, window,
-                          None if alibi_slopes is None else _at(alibi_slopes, _F32, heads, "alibi_slopes"),
-                          None if first_keys is None else _at(first_keys, _I32, batch, "first_keys"),
-                          None if prefix_lens is None else _at(prefix_lens, _I32, batch, "prefix_lens"))
-    status = lib.paged_attention_masked(
-        pool.handle, _at(q, _BF16, rows * pool.head_dim, "q"), heads, q_len,
-        _at(block_tables, _I32, batch * max_blocks, "block_tables"), max_blocks,
-        _at(context_lens, _I32, batch, "context_lens"), batch, scale, mask, kv_split_tokens, ws, ws_bytes,
-        _at(out, _BF16, rows * pool.head_dim, "out"), None if lse is None else _at(lse, _F32, rows, "lse"),
-        _pool_stream(stream, pool))
+    if workspace is None:
+        workspace = _zeroed(paged_attention_masked_workspace_size(
+            pool, q.shape[0], q.shape[1], q.shape[2] if q.dim() == 4 else 1, block_tables.shape[1], window,
+            kv_split_tokens), q)
+    status = (_binding or _native()).attention_masked(
+        pool._h.value, pool.head_dim, q, block_tables, context_lens, scale, softcap, window, alibi_slopes, first_keys,
+        prefix_lens, kv_split_tokens, workspace, out, lse, _pool_stream(stream, pool))
     if status:
         raise KVError(status, "paged_attention_masked")
     return out
@@ -594,21 +541,15 @@ def paged_shared_prefix_attention(pool: Pool, q, block_tables, context_lens, gro
     is the sequences group_offsets[g] .. group_offsets[g + 1] - 1 (int32 [G + 1]) and shares the
     first group_blocks[g] entries of their tables (int32 [G]); BlockManager.prefix_groups makes
     both.  q bf16 [B, Hq, d] or [B, Hq, q_len, d].  Returns out (shaped like q)."""
-    lib = _lib or load_library()
-    batch, heads, q_len, max_blocks = _queries(pool, q, block_tables)
     if out is None:
         out = torch.empty_like(q)
-    rows = batch * heads * q_len
-    groups = group_blocks.numel()
-    ws, ws_bytes, keep = _workspace(workspace, lambda: paged_shared_prefix_workspace_size(
-        pool, batch, heads, q_len, max_blocks, groups, kv_split_tokens), q)
-    status = lib.paged_shared_prefix_attention(
-        pool.handle, _at(q, _BF16, rows * pool.head_dim, "q"), heads, q_len,
-        _at(block_tables, _I32, batch * max_blocks, "block_tables"), max_blocks,
-        _at(context_lens, _I32, batch, "context_lens"), batch,
-        _at(group_offsets, _I32, groups + 1, "group_offsets"), _at(group_blocks, _I32, groups, "group_blocks"), groups,
-        scale, kv_split_tokens, ws, ws_bytes, _at(out, _BF16, rows * pool.head_dim, "out"),
-        None if lse is None else _at(lse, _F32, rows, "lse"), _pool_stream(stream, pool))
+    if workspace is None:
+        workspace = _zeroed(paged_shared_prefix_workspace_size(
+            pool, q.shape[0], q.shape[1], q.shape[2] if q.dim() == 4 else 1, block_tables.shape[1],
+            group_blocks.numel(), kv_split_tokens), q)
+    status = (_binding or _native()).shared_prefix_attention(
+        pool._h.value, pool.head_dim, q, block_tables, context_lens, group_offsets, group_blocks, scale,
+        kv_split_tokens, workspace, out, lse, _pool_stream(stream, pool))
     if status:
         raise KVError(status, "paged_shared_prefix_attention")
     return out

@@ -1,4 +1,4 @@
-"""Build of the CUDA library libkvpaged.so (sm_103a only).
+"""Build of the CUDA library libkvpaged.so (sm_103a only) and of its native binding _calls.so.
 
 Each translation unit is compiled by nvcc in parallel into _build/, then the
 objects are linked into a shared library next to this file.  The CUDA runtime
@@ -12,6 +12,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkvpaged.so")
+BINDING_SRC = os.path.join(PKG, "binding", "calls.cpp")
+BINDING = os.path.join(PKG, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE,
@@ -38,13 +41,13 @@ def sources() -> list[str]:
 
 def _deps() -> list[str]:
     return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
+            + glob.glob(os.path.join(INCLUDE, "*.h")) + [BINDING_SRC, os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -67,14 +70,38 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
-        objs = list(ex.map(compile_one, sources()))
+    def compile_binding():
+        import torch
+        root = os.path.dirname(torch.__file__)
+        obj = os.path.join(BUILD, "binding.o")
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               "-I" + INCLUDE, "-I" + os.path.join(root, "include"),
+               "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               "-I" + sysconfig.get_paths()["include"], "-c", BINDING_SRC, "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on calls.cpp:\n{r.stdout}\n{r.stderr}")
+        return obj, os.path.join(root, "lib")
+
+    # the longest translation units first
+    srcs = sorted(sources(), key=lambda f: ("span" not in f, f))
+    with ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 1)) as ex:
+        binding = ex.submit(compile_binding)
+        objs = list(ex.map(compile_one, srcs))
+        binding_obj, torch_lib = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
+    cmd = [nvcc, *ARCH, "-shared", "-Xlinker", "-soname=libkvpaged.so", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, binding_obj, LIB, "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
     return LIB
 
 

@@ -225,9 +225,12 @@ cudaError_t launch_decode_fp8(int head_dim, int block_size, int head_tile, dim3 
 // The span kernel (decode_span.cuh), `heads` kv heads per CTA (1, 2 or 4); tk, tv: the pool's maps
 // with boxes of 16 slots.
 cudaError_t prepare_span_bf16(int head_dim, int head_tile, int heads);
+cudaError_t prepare_span_bf16_64(int head_dim, int head_tile, int heads);
 cudaError_t prepare_span_fp8(int head_dim, int head_tile, int heads);
 cudaError_t launch_span_bf16(SpanRule rule, int head_dim, int head_tile, int heads, int ctas, const CUtensorMap& tk,
                              const CUtensorMap& tv, const SpanParams& p, cudaStream_t s);
+cudaError_t launch_span_bf16_64(SpanRule rule, int head_dim, int head_tile, int heads, int ctas, const CUtensorMap& tk,
+                                const CUtensorMap& tv, const SpanParams& p, cudaStream_t s);
 cudaError_t launch_span_fp8(SpanRule rule, int head_dim, int head_tile, int heads, int ctas, const CUtensorMap& tk,
                             const CUtensorMap& tv, const SpanParams& p, cudaStream_t s);
 // The decode kernel with one CTA per group of `heads` kv heads (decode_heads.cuh), `ctas`

@@ -32,7 +32,10 @@ namespace kvp {
 namespace {
 
 constexpr int NRA_THREADS = 256;
-constexpr int NRA_STREAM_TOKENS = 2;                // tokens per CTA from which the streaming form is taken
+// Rows per SM up to which a lane group of the direct form takes one row, or two (else four): fewer
+// rows per lane group start sooner, more of them pay a token's lookups once.
+constexpr int NRA_ROWS_1 = 54, NRA_ROWS_2 = 160;
+constexpr int NRA_STREAM_TOKENS = 3;                // tokens per CTA from which the streaming form is taken
 
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b)
@@ -451,6 +454,9 @@ cudaError_t launch_nra_form(const NormRopeParams& p, int num_sms, cudaStream_t s
         return launch_dependent(paged_norm_rope_append_stream<D, FP8>, dim3(static_cast<unsigned>(ctas)), dim3(NRS_THREADS),
                                 static_cast<size_t>(stages) * stage, s, p, static_cast<int>(stage), stages);
     }
+    const long long rows = static_cast<long long>(p.num_tokens) * (p.q_heads + 2 * p.kv_heads);
+    if (rows <= static_cast<long long>(NRA_ROWS_1) * num_sms) return launch_nra<D, FP8, 1>(p, s);
+    if (rows <= static_cast<long long>(NRA_ROWS_2) * num_sms) return launch_nra<D, FP8, 2>(p, s);
     return launch_nra<D, FP8, 4>(p, s);
 }
 

@@ -38,12 +38,26 @@ def test_a_null_pool_is_refused(lib):
     assert lib.paged_shared_prefix_workspace_size(None, 1, 1, 1, 1, 0, 0, None) == bad
 
 
-def test_host_tensors_are_refused():
+def test_host_tensors_are_refused(lib):
+    """The native binding looks at every tensor before it calls the library."""
     import torch
-    with pytest.raises(ValueError):
-        kp._rows(torch.zeros(2, 4, 64, dtype=torch.bfloat16), 2, 4, 64, "q")
-    with pytest.raises(ValueError):
-        kp._at(torch.zeros(4, dtype=torch.int32), torch.int32, 4, "context_lens")
+    c = kp._native()
+    q, kv = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    t, l = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)  # noqa: E741
+    out = torch.empty_like(q)
+    for call, args in ((c.norm_rope_append, (1, 64, 2, q, kv, kv, t, l, None, None, 1e-6, None, False, 1, None, None, out, 0)),
+                       (c.attention_masked, (1, 64, q, t, l, 1.0, 0.0, 0, None, None, None, 0, None, out, None, 0)),
+                       (c.shared_prefix_attention, (1, 64, q, t, l, l, l[:1], 1.0, 0, None, out, None, 0))):
+        with pytest.raises(ValueError, match="CUDA"):
+            call(*args)
+        with pytest.raises(RuntimeError, match="destroyed"):
+            call(None, *args[1:])
+        with pytest.raises(TypeError):
+            call(*args[:-1])
+        with pytest.raises(ValueError, match="tensor"):
+            call(*args[:2], *[None if isinstance(x, torch.Tensor) else x for x in args[2:]])
+        with pytest.raises(ValueError):
+            call(*args[:1], 128, *args[2:])
 
 
 def groups(bm, seqs, **kw):
