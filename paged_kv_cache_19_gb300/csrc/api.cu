@@ -267,6 +267,7 @@ kv_status make_span_plan(const kv_pool* pl, int batch, int q_heads, int q_len, i
     if (p.units > (1 << 28)) return KV_ERR_UNSUPPORTED;
     p.least = split_tokens > 0 ? split_tokens / 16 : kSpanLeast;
     const long long subs = static_cast<long long>(span_blocks) * (pl->block_size / 16) + kvp::SPAN_PAD;
+    if (p.head_groups * subs > (1 << 30)) return KV_ERR_UNSUPPORTED;        // positions of a kv head group
     const long long most = (p.units * subs + p.least - 1) / p.least;
     const long long resident = static_cast<long long>(pl->num_sms) * kvp::SPAN_CTAS;
     p.ctas = static_cast<int>(most < resident ? most : resident);

@@ -10,7 +10,8 @@
 // about a hundred rows on it is bound by the tensor cores and the exponentials instead of memory.
 //
 // Persistent, one CTA per SM; the units are (group, kv head, pair of 128-row tiles, 128-token
-// tile) in that order and every CTA takes an equal contiguous range (prefix_groups.cuh), so a
+// tile) in that order, with PFX_PAD positions before each run for what starting one costs, and every
+// CTA takes an equal contiguous range (prefix_groups.cuh), so a
 // run -- one (group, kv head, pair) -- is cut at range borders and each cut leaves a normalised
 // fp32 partial (a piece) that the suffix kernel merges by log-sum-exp.  Warps:
 //   * 0-3 and 4-7: two softmax teams, one per slot (128 rows: thread = row = tensor-memory lane).
@@ -101,17 +102,10 @@ struct PfxCtl {
 };
 
 
-// a / b for non-negative values; in 32 bits where they fit.
-__device__ __forceinline__ long long pfx_div(long long a, long long b)
-{
-    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
-}
-
 // The CTA that holds unit u of `units` cut into ranges for n CTAs.
 __device__ __forceinline__ int pfx_cta_of(long long u, long long units, int n)
 {
-    return static_cast<int>(pfx_div((u + 1) * n - 1, units));
+    return static_cast<int>(div_small((u + 1) * n - 1, units));
 }
 
 // The items of a CTA's range.
@@ -125,7 +119,7 @@ struct PfxWalk {
         gr = load_prefix_group(p, g);
         pairs = prefix_pairs(p, gr);
         tiles = (gr.blocks * block_size + PFX_TILE - 1) / PFX_TILE;
-        units = static_cast<long long>(p.kv_heads) * pairs * tiles;
+        units = tiles > 0 ? static_cast<long long>(p.kv_heads) * pairs * (tiles + PFX_PAD) : 0;
     }
     __device__ __forceinline__ void init(const PrefixParams& p, const PfxCtl* ctl, int block_size)
     {
@@ -138,16 +132,26 @@ struct PfxWalk {
     __device__ __forceinline__ bool next(const PrefixParams& p, const PfxCtl* ctl, int block_size, PfxItem& it)
     {
         it.n = 0;
-        if (u >= hi) return false;
-        while (u >= base + units) {                 // hi is at most the last group's end
-            base += units;
-            ++g;
-            load(p, block_size);
+        int run, first;                             // the run at u; its tile there (< 0: padding)
+        long long left;
+        for (;;) {
+            if (u >= hi) return false;
+            while (u >= base + units) {             // hi is at most the last group's end
+                base += units;
+                ++g;
+                load(p, block_size);
+            }
+            const long long rel = u - base;
+            run = static_cast<int>(div_small(rel, tiles + PFX_PAD));
+            first = static_cast<int>(rel - static_cast<long long>(run) * (tiles + PFX_PAD)) - PFX_PAD;
+            if (first < 0) {
+                u -= first;                         // over the padding
+                first = 0;
+            }
+            left = hi - u;
+            if (left > 0) break;
         }
-        const long long rel = u - base;
-        const int run = static_cast<int>(pfx_div(rel, tiles));
-        it.tile0 = static_cast<int>(rel - static_cast<long long>(run) * tiles);
-        const long long left = hi - u;
+        it.tile0 = first;
         it.n = left < tiles - it.tile0 ? static_cast<int>(left) : tiles - it.tile0;
         it.kvh = run / pairs;
         const int pair = run - it.kvh * pairs;
@@ -311,8 +315,8 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         if (!all) units = 0;
         const int ctas = units < gridDim.x ? static_cast<int>(units) : static_cast<int>(gridDim.x);
         const int c = blockIdx.x;
-        const long long lo = c < ctas ? pfx_div(units * c, ctas) : 0;
-        const long long hi = c < ctas ? pfx_div(units * (c + 1), ctas) : 0;
+        const long long lo = c < ctas ? div_small(units * c, ctas) : 0;
+        const long long hi = c < ctas ? div_small(units * (c + 1), ctas) : 0;
         if (tid == 0) {
             ctl->units = units;
             ctl->ctas = ctas;

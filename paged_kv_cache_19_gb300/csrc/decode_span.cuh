@@ -140,10 +140,13 @@ struct SpanSeq {
 };
 
 // A CTA's range of positions [lo, hi), and where it begins.
+template <int RULE>
 struct SpanRange {
     long long lo, hi;
     long long base;                   // position of sequence b0's first unit
     int b0;
+    int per;                          // positions of one of its groups of kv heads
+    SpanSeq<RULE> seq;
     int g;                            // SPAN_SUFFIX: the group that holds b0, or the next one (the
                                       // number of groups: none); -1: nothing is shared
 };
@@ -200,7 +203,7 @@ struct SpanWalk {
         seq.load(sp, b, false);
     }
 
-    __device__ __forceinline__ void init(const SpanParams& sp, const SpanRange& r, long long all, int n_ranges)
+    __device__ __forceinline__ void init(const SpanParams& sp, const SpanRange<RULE>& r, long long all, int n_ranges)
     {
         lo = r.lo;
         hi = r.hi;
@@ -214,17 +217,14 @@ struct SpanWalk {
         b = r.b0;
         g = r.g;
         g_end = RULE == SPAN_SUFFIX && g >= 0 && g < sp.shared.n_groups ? __ldcg(sp.shared.group_offsets + g + 1) : 0;
-        load_seq(sp);
+        seq = r.seq;
         // whole groups of kv heads before the range
-        long long per = 0;
-        int sub;
-        for (int t = 0; t < sp.d.head_groups; ++t) per += seq.tile_subs(sp, t, NT, sub) + SPAN_PAD;
-        kg = static_cast<int>((lo - at) / per);
-        at += kg * per;
+        kg = static_cast<int>(div_small(lo - at, r.per));
+        at += static_cast<long long>(kg) * r.per;
     }
     __device__ __forceinline__ int range_of(long long pos) const
     {
-        return static_cast<int>(((pos + 1) * ranges - 1) / total);
+        return static_cast<int>(div_small((pos + 1) * ranges - 1, total));
     }
     __device__ __forceinline__ bool next(const SpanParams& sp, SpanItem<RULE>& it)
     {
@@ -406,7 +406,7 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     struct Ctl {
         uint64_t full[NST], empty[NST];
         uint64_t item_full[QUEUE], item_empty[QUEUE];
-        SpanRange range;
+        SpanRange<RULE> range;
         long long scan[THREADS / 32];
         int tag[NST];                                // what the stage holds
         SpanItem<RULE> queue[QUEUE];
@@ -472,46 +472,54 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     long long total = 0;
     int ranges;
     {
-        const auto positions = [&](int b) {
-            long long w = 0;
+        SpanSeq<RULE> mine;                          // the thread's sequence of the round
+        const auto positions = [&](int b) {          // of one of its groups of kv heads
+            int w = 0;
             if (b < p.batch) {
-                SpanSeq<RULE> s;
                 const int g = SUFFIX && grouped ? find_group(off, sp.shared.n_groups, b) : -1;
                 if (SUFFIX && g >= 0)
-                    s.load(sp, b, blockIdx.x == 0, g, off[g + 1] - off[g], blocks[g]);
+                    mine.load(sp, b, blockIdx.x == 0, g, off[g + 1] - off[g], blocks[g]);
                 else
-                    s.load(sp, b, blockIdx.x == 0);
+                    mine.load(sp, b, blockIdx.x == 0);
                 int sub;
-                for (int t = 0; t < p.head_groups; ++t) w += s.tile_subs(sp, t, NT, sub) + SPAN_PAD;
-                w *= p.kv_heads / HC;
+                for (int t = 0; t < p.head_groups; ++t) w += mine.tile_subs(sp, t, NT, sub) + SPAN_PAD;
             }
             return w;
         };
-        long long w = 0, sum = 0;
-        for (int b = tid; b < p.batch; b += THREADS) sum += w = positions(b);
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
-        if (lane == 0) ctl->scan[warp] = sum;
-        __syncthreads();
-#pragma unroll
-        for (int v = 0; v < THREADS / 32; ++v) total += ctl->scan[v];
-        const long long most = (total + sp.least - 1) / sp.least;       // ranges of `least` positions or more
-        ranges = most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
-        const int k = blockIdx.x;
-        const long long lo = k < ranges ? total * k / ranges : total;
-        const long long hi = k < ranges ? total * (k + 1) / ranges : total;
-        long long before = 0;
-        for (int b0 = 0; lo < hi && b0 < p.batch && before <= lo; b0 += THREADS) {
-            if (p.batch > THREADS) w = positions(b0 + tid);
-            long long x = w;
+        const int kgs = p.kv_heads / HC;
+        int per = positions(tid);
+        const auto scan = [&](long long x) {         // inclusive, in the warp; the warps' sums in ctl
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long y = __shfl_up_sync(FULL_MASK, x, o);
                 if (lane >= o) x += y;
             }
-            __syncthreads();                         // the sums before this round are read
             if (lane == 31) ctl->scan[warp] = x;
-            __syncthreads();
+            return x;
+        };
+        // the whole batch's positions; where it is more than one round, the rounds are summed first
+        const bool one = p.batch <= THREADS;
+        long long x = static_cast<long long>(per) * kgs;
+        if (!one)
+            for (int b = tid + THREADS; b < p.batch; b += THREADS) x += static_cast<long long>(positions(b)) * kgs;
+        x = scan(x);
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < THREADS / 32; ++v) total += ctl->scan[v];
+        const long long most = div_small(total + sp.least - 1, sp.least);       // ranges of `least` positions or more
+        ranges = most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
+        const int k = blockIdx.x;
+        const long long lo = k < ranges ? div_small(total * k, ranges) : total;
+        const long long hi = k < ranges ? div_small(total * (k + 1), ranges) : total;
+        long long before = 0;
+        for (int b0 = 0; lo < hi && b0 < p.batch && before <= lo; b0 += THREADS) {
+            if (!one) {
+                per = positions(b0 + tid);
+                __syncthreads();                     // the sums before this round are read
+                x = scan(static_cast<long long>(per) * kgs);
+                __syncthreads();
+            }
+            const long long w = static_cast<long long>(per) * kgs;
             long long base = before + x - w;
 #pragma unroll
             for (int v = 0; v < THREADS / 32; ++v) {
@@ -521,6 +529,8 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             if (base <= lo && lo < base + w) {
                 ctl->range.base = base;
                 ctl->range.b0 = b0 + tid;
+                ctl->range.per = per;
+                ctl->range.seq = mine;
                 if (SUFFIX) {
                     const int g = find_group(off, grouped ? sp.shared.n_groups : 0, b0 + tid);
                     ctl->range.g = !grouped ? -1 : g >= 0 ? g : b0 + tid < off[0] ? 0 : sp.shared.n_groups;
@@ -787,32 +797,48 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             // all partials in order (this warp's own among them), so the bits do not depend on
             // which warp is last
             reset_state(st);
-#pragma unroll 2
-            for (int e = 0; e < parts; ++e) {
-                const size_t at = part(e);
-                float f[C::NTT][2], g[C::NTT][2];
+            constexpr int UN = C::NTT == 1 ? 3 : 1;  // parts in flight
+#pragma unroll 1
+            for (int e0 = 0; e0 < parts; e0 += UN) {
+                float2 v[UN][C::NTT][2];
+                float4 x[UN][C::KS][C::NTT];
 #pragma unroll
-                for (int nt = 0; nt < C::NTT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float2 v = __ldcg(ml + at * NT + nt * 8 + 2 * c + j);
-                        const float m = v.y > 0.f ? fmaxf(st.m[nt][j], v.x) : st.m[nt][j];
-                        f[nt][j] = m > -INFINITY ? fast_exp2(st.m[nt][j] - m) : 1.f;
-                        g[nt][j] = v.y > 0.f ? fast_exp2(v.x - m) : 0.f;
-                        st.m[nt][j] = m;
-                        st.l[nt][j] = st.l[nt][j] * f[nt][j] + g[nt][j] * v.y;
-                    }
-                const float4* other = reinterpret_cast<const float4*>(p.part_o) + at * (S::REGS4 * 32) + lane;
-#pragma unroll
-                for (int ms = 0; ms < C::KS; ++ms)
+                for (int u = 0; u < UN; ++u) {
+                    const size_t at = part(min(e0 + u, parts - 1));
+                    const float4* other = reinterpret_cast<const float4*>(p.part_o) + at * (S::REGS4 * 32) + lane;
 #pragma unroll
                     for (int nt = 0; nt < C::NTT; ++nt) {
-                        const float4 x = __ldcg(other + (ms * C::NTT + nt) * 32);
-                        st.o[ms][nt][0] = st.o[ms][nt][0] * f[nt][0] + x.x * g[nt][0];
-                        st.o[ms][nt][1] = st.o[ms][nt][1] * f[nt][1] + x.y * g[nt][1];
-                        st.o[ms][nt][2] = st.o[ms][nt][2] * f[nt][0] + x.z * g[nt][0];
-                        st.o[ms][nt][3] = st.o[ms][nt][3] * f[nt][1] + x.w * g[nt][1];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) v[u][nt][j] = __ldcg(ml + at * NT + nt * 8 + 2 * c + j);
+#pragma unroll
+                        for (int ms = 0; ms < C::KS; ++ms) x[u][ms][nt] = __ldcg(other + (ms * C::NTT + nt) * 32);
                     }
+                }
+#pragma unroll
+                for (int u = 0; u < UN; ++u) {
+                    if (e0 + u >= parts) break;
+#pragma unroll
+                    for (int nt = 0; nt < C::NTT; ++nt) {
+                        float f[2], g[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float2 w = v[u][nt][j];
+                            const float m = w.y > 0.f ? fmaxf(st.m[nt][j], w.x) : st.m[nt][j];
+                            f[j] = m > -INFINITY ? fast_exp2(st.m[nt][j] - m) : 1.f;
+                            g[j] = w.y > 0.f ? fast_exp2(w.x - m) : 0.f;
+                            st.m[nt][j] = m;
+                            st.l[nt][j] = st.l[nt][j] * f[j] + g[j] * w.y;
+                        }
+#pragma unroll
+                        for (int ms = 0; ms < C::KS; ++ms) {
+                            const float4 y = x[u][ms][nt];
+                            st.o[ms][nt][0] = st.o[ms][nt][0] * f[0] + y.x * g[0];
+                            st.o[ms][nt][1] = st.o[ms][nt][1] * f[1] + y.y * g[1];
+                            st.o[ms][nt][2] = st.o[ms][nt][2] * f[0] + y.z * g[0];
+                            st.o[ms][nt][3] = st.o[ms][nt][3] * f[1] + y.w * g[1];
+                        }
+                    }
+                }
             }
         }
         if constexpr (FP8) {

@@ -17,6 +17,15 @@ namespace kvp {
 constexpr int PFX_TILE = 128;              // tokens of a unit, rows of a row tile
 constexpr int PFX_PAIR = 2 * PFX_TILE;     // rows of a run
 
+constexpr int PFX_PAD = 8;                 // what starting a run costs, in units
+
+// a / b for non-negative values; in 32 bits where they fit.
+__device__ __forceinline__ long long div_small(long long a, long long b)
+{
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 struct PrefixGroup {
     int off, n;                            // members
     int blocks;                            // shared blocks; 0: computed without sharing
