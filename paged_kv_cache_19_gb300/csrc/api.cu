@@ -243,7 +243,7 @@ kv_status make_plan(const kv_pool* pl, int batch, int q_heads, int q_len, int ma
 // fewer where ranges of the least length cover everything.
 struct SpanPlan {
     int rows, head_tile, head_groups, heads, least, ctas;
-    long long units, parts;         // parts: states of four warps, per unit and per range border
+    long long units;
 };
 
 // Least positions of a CTA's range with the automatic choice.
@@ -262,16 +262,14 @@ kv_status make_span_plan(const kv_pool* pl, int batch, int q_heads, int q_len, i
     p.rows = q_heads / pl->kv_heads * q_len;
     p.head_tile = kvp::head_tile_for_group(p.rows);
     p.head_groups = (p.rows + p.head_tile - 1) / p.head_tile;
-    p.heads = pl->kv_heads % 4 == 0 ? 4 : pl->kv_heads % 2 == 0 ? 2 : 1;
-    p.units = static_cast<long long>(batch) * (pl->kv_heads / p.heads) * p.head_groups;
-    if (p.units > (1 << 28)) return KV_ERR_UNSUPPORTED;
-    p.least = split_tokens > 0 ? split_tokens / 16 : kSpanLeast;
     const long long subs = static_cast<long long>(span_blocks) * (pl->block_size / 16) + kvp::SPAN_PAD;
     if (p.head_groups * subs > (1 << 30)) return KV_ERR_UNSUPPORTED;        // positions of a kv head group
-    const long long most = (p.units * subs + p.least - 1) / p.least;
     const long long resident = static_cast<long long>(pl->num_sms) * kvp::SPAN_CTAS;
+    p.heads = pl->kv_heads % 4 == 0 ? 4 : pl->kv_heads % 2 == 0 ? 2 : 1;
+    p.units = static_cast<long long>(batch) * (pl->kv_heads / p.heads) * p.head_groups;
+    p.least = split_tokens > 0 ? split_tokens / 16 : kSpanLeast;
+    const long long most = (p.units * subs + p.least - 1) / p.least;
     p.ctas = static_cast<int>(most < resident ? most : resident);
-    p.parts = 4 * (p.units + p.ctas);
     *out = p;
     return KV_OK;
 }
@@ -324,7 +322,9 @@ size_t workspace_bytes_for(const kv_pool* pl, int batch, const Plan& p)
     return workspace_layout(pl, batch, p).total;
 }
 
-// Workspace of the span kernel: tickets, (max, sum) pairs, partial outputs.
+// Workspace of the span kernel: tickets, then the pieces of cut units, two per CTA and head: (max, sum)
+// pairs, partial outputs.  The tickets' place does not depend on the call's sizes: whatever call
+// used the workspace before, they are zero.
 struct SpanLayout {
     size_t part_ml, part_o, total;
 };
@@ -332,8 +332,8 @@ struct SpanLayout {
 SpanLayout span_layout(const kv_pool* pl, const SpanPlan& p)
 {
     SpanLayout w;
-    const size_t rows = static_cast<size_t>(p.parts) * p.head_tile;
-    w.part_ml = round_up(static_cast<size_t>(p.units) * p.heads * sizeof(int), kAlign);
+    const size_t rows = static_cast<size_t>(p.ctas) * 2 * p.heads * p.head_tile;
+    w.part_ml = round_up(static_cast<size_t>(pl->num_sms) * kvp::SPAN_CTAS * 2 * 4 * sizeof(int), kAlign);
     w.part_o = w.part_ml + round_up(rows * 2 * sizeof(float), kAlign);
     w.total = w.part_o + round_up(rows * pl->head_dim * sizeof(float), kAlign);
     return w;

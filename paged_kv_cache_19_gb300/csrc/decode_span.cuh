@@ -25,9 +25,10 @@
 //     (4 / HC)-th one) into an online-softmax state in registers (decode_common.cuh,
 //     process_block_rows under the rule of SpanRows).  With four heads a warp owns its rows and
 //     finishes a unit by itself.
-// Where several warps hold parts of the same rows -- a unit cut by a range border, or several warps
-// per head -- each leaves its fp32 state in the accumulators' layout, and the warp that finishes
-// last merges them in order (a ticket per unit and head, zero between calls).
+// Several warps of one head hand their states to the first of them through shared memory.  The
+// pieces of a unit cut by a range border go through global memory: each leaves its fp32 state in the
+// accumulators' layout, and the warp that finishes last merges them in order (tickets by range and
+// head, zero between calls); many pieces in two levels.
 // SPAN_FIGURES
 // Bound by the K/V bytes of the visible blocks.  The cap costs one ex2 and one reciprocal per
 // score (capped_tanh), the bias one add and one multiply; both are template flags, so a plain
@@ -167,7 +168,7 @@ __device__ __forceinline__ int find_group(const int* off, int n, int b)
 template <int RULE>
 struct SpanItem {
     SpanSeq<RULE> seq;
-    int b, kg, hg, unit;              // sequence, group of kv heads, row tile; -1: no more items
+    int b, kg, hg;                    // sequence, group of kv heads, row tile; b -1: no more items
     int sub0, n;                      // sub-blocks [sub0, sub0 + n) of the sequence
     int split, nsplit;                // which of the unit's pieces this is
     int range0;                       // range of its first piece
@@ -243,10 +244,9 @@ struct SpanWalk {
                 it.b = b;
                 it.kg = kg;
                 it.hg = hg;
-                it.unit = (b * (sp.d.kv_heads / HC) + kg) * sp.d.head_groups + hg;
                 it.split = 0;
                 it.nsplit = 1;
-                it.range0 = static_cast<int>(blockIdx.x);      // with unit: an index of its own
+                it.range0 = static_cast<int>(blockIdx.x);
                 it.sub0 = sub;
                 it.n = n;
                 if (n > 0 && (first < lo || end > hi)) {
@@ -340,6 +340,31 @@ struct PieceRows {
     }
 };
 
+// Another state's 8-row tile nt -- its rows' (max, sum) pairs a, b and its accumulators x(ms) --
+// folded into st.
+template <class C, class X>
+__device__ __forceinline__ void fold_state(WarpState<C>& st, int nt, float2 a, float2 b, const X& x)
+{
+    float f[2], g[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const float2 w = j == 0 ? a : b;
+        const float m = w.y > 0.f ? fmaxf(st.m[nt][j], w.x) : st.m[nt][j];
+        f[j] = m > -INFINITY ? fast_exp2(st.m[nt][j] - m) : 1.f;
+        g[j] = w.y > 0.f ? fast_exp2(w.x - m) : 0.f;
+        st.m[nt][j] = m;
+        st.l[nt][j] = st.l[nt][j] * f[j] + g[j] * w.y;
+    }
+#pragma unroll
+    for (int ms = 0; ms < C::KS; ++ms) {
+        const float4 y = x(ms);
+        st.o[ms][nt][0] = st.o[ms][nt][0] * f[0] + y.x * g[0];
+        st.o[ms][nt][1] = st.o[ms][nt][1] * f[1] + y.y * g[1];
+        st.o[ms][nt][2] = st.o[ms][nt][2] * f[0] + y.z * g[0];
+        st.o[ms][nt][3] = st.o[ms][nt][3] * f[1] + y.w * g[1];
+    }
+}
+
 // Rows [a, b) of a piece -- normalised outputs o [row][D] and log-sum-exps (log2 units, 4 floats
 // apart; -inf: the row saw nothing) in shared memory -- folded into the state as one more block;
 // out_scale: the factor that takes its outputs to the state's units.
@@ -385,11 +410,14 @@ struct SpanCfg : DecodeCfg<FP8, D, SPAN_TOK, NT> {
     static constexpr int RPS = C::STAGE / (D * 4) < NT ? C::STAGE / (D * 4) : NT;   // rows of a piece stage
     static constexpr int LSE = HC * RPS * 16;       // and their log-sum-exps, 16 bytes a row
     static constexpr int CTL = 2048;                // barriers, items
-    static constexpr int BUDGET = 228 * 1024 / MINB - 1024 /* reserved */ - 1024 /* alignment */ - CTL;
-    static constexpr int NST = BUDGET / (HSTAGE + LSE) < 16 ? BUDGET / (HSTAGE + LSE) : 16;
-    static constexpr int SMEM = 1024 + NST * (HSTAGE + LSE) + CTL;
-    static constexpr int QUEUE = 8;                 // items handed on ahead
     static constexpr int REGS4 = C::KS * C::NTT;    // groups of four accumulators of a thread
+    static constexpr int HAND = WPH > 1 ? (NCW - HC) * (REGS4 * 16 + C::NTT * 16) * 32 : 0;   // states handed over
+    static constexpr int BUDGET = 228 * 1024 / MINB - 1024 /* reserved */ - 1024 /* alignment */ - CTL - HAND;
+    static constexpr int NST = BUDGET / (HSTAGE + LSE) < 16 ? BUDGET / (HSTAGE + LSE) : 16;
+    static constexpr int SMEM = 1024 + NST * (HSTAGE + LSE) + HAND + CTL;
+    static constexpr int QUEUE = 8;                 // items handed on ahead
+    // Pieces of a unit from which the merge takes two levels, and the least group.
+    static constexpr int MERGE_ONE = 12, MERGE_LEAST = 3;
     static_assert(NST >= 3 && SMEM <= 227 * 1024, "a ring of three stages at least");
 };
 
@@ -406,6 +434,7 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     struct Ctl {
         uint64_t full[NST], empty[NST];
         uint64_t item_full[QUEUE], item_empty[QUEUE];
+        uint64_t hand_full[HC], hand_free[HC];       // a head's states handed over, read
         SpanRange<RULE> range;
         long long scan[THREADS / 32];
         int tag[NST];                                // what the stage holds
@@ -416,7 +445,8 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* lse_sm = smem + NST * S::HSTAGE;
-    Ctl* ctl = reinterpret_cast<Ctl*>(lse_sm + NST * S::LSE);
+    uint8_t* hand_sm = lse_sm + NST * S::LSE;
+    Ctl* ctl = reinterpret_cast<Ctl*>(hand_sm + S::HAND);
 
     const int tid = threadIdx.x;
     const int warp = tid >> 5;
@@ -431,6 +461,10 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         for (int i = 0; i < QUEUE; ++i) {
             mbar_init(smem_u32(&ctl->item_full[i]), 1);
             mbar_init(smem_u32(&ctl->item_empty[i]), NCW);
+        }
+        for (int i = 0; i < HC; ++i) {
+            mbar_init(smem_u32(&ctl->hand_full[i]), WPH > 1 ? WPH - 1 : 1);
+            mbar_init(smem_u32(&ctl->hand_free[i]), 1);
         }
         fence_mbar_init();
         prefetch_tensormap(&tmk);
@@ -761,85 +795,123 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
 
         // -------------------------------------------------------- the unit's end
         reduce_row_sums(st);
-        const int parts = it.nsplit * WPH;           // warps that hold parts of these rows
-        if (parts > 1) {
-            // part e of the head: warp e % WPH of the unit's piece e / WPH
-            const size_t part0 = (static_cast<size_t>(it.range0) + it.unit) * NCW + h * WPH;
-            const auto part = [&](int e) { return part0 + e / WPH * NCW + e % WPH; };
-            const size_t own = part(it.split * WPH + warp % WPH);
-            float4* mine = reinterpret_cast<float4*>(p.part_o) + own * (S::REGS4 * 32) + lane;
+        if constexpr (WPH > 1) {
+            // The head's other warps hand their states to the first, in the accumulators' layout.
+            constexpr int STATE = (S::REGS4 + C::NTT) * 32;             // 16-byte vectors of a state
+            const int w = warp % WPH;
+            float4* state = reinterpret_cast<float4*>(hand_sm) + (h * (WPH - 1) + (w > 0 ? w - 1 : 0)) * STATE + lane;
+            if (w > 0) {
+                // (the states before have been read: hand_free has completed once per unit)
+                ok = k == 0 || all_ok(mbar_wait_bounded(smem_u32(&ctl->hand_free[h]), static_cast<uint32_t>(k - 1) & 1u));
+                if (!ok) break;
 #pragma unroll
-            for (int ms = 0; ms < C::KS; ++ms)
+                for (int ms = 0; ms < C::KS; ++ms)
+#pragma unroll
+                    for (int nt = 0; nt < C::NTT; ++nt)
+                        state[(ms * C::NTT + nt) * 32] =
+                            make_float4(st.o[ms][nt][0], st.o[ms][nt][1], st.o[ms][nt][2], st.o[ms][nt][3]);
 #pragma unroll
                 for (int nt = 0; nt < C::NTT; ++nt)
-                    mine[(ms * C::NTT + nt) * 32] =
-                        make_float4(st.o[ms][nt][0], st.o[ms][nt][1], st.o[ms][nt][2], st.o[ms][nt][3]);
-            float2* ml = reinterpret_cast<float2*>(p.part_ml);
-            if (r == 0) {
-#pragma unroll
-                for (int nt = 0; nt < C::NTT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        ml[own * NT + nt * 8 + 2 * c + j] = make_float2(st.m[nt][j], st.l[nt][j]);
+                    state[(S::REGS4 + nt) * 32] = make_float4(st.m[nt][0], st.l[nt][0], st.m[nt][1], st.l[nt][1]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl->hand_full[h]));
+                continue;
             }
-            // One acquire-release add by lane 0: the other lanes' stores come before it (__syncwarp),
-            // the loads of the last warp after it.
-            __syncwarp();
-            int last = 0;
-            if (lane == 0) {
-                int* ticket = p.tickets + static_cast<size_t>(it.unit) * HC + h;
-                last = ticket_add(ticket) == parts - 1;
-                if (last) *ticket = 0;               // ready for the next call
-            }
-            last = __shfl_sync(FULL_MASK, last, 0);
-            if (!last) continue;
-            __syncwarp();
-            // all partials in order (this warp's own among them), so the bits do not depend on
-            // which warp is last
-            reset_state(st);
-            constexpr int UN = C::NTT == 1 ? 3 : 1;  // parts in flight
+            ok = all_ok(mbar_wait_bounded(smem_u32(&ctl->hand_full[h]), static_cast<uint32_t>(k) & 1u));
+            if (!ok) break;
 #pragma unroll 1
-            for (int e0 = 0; e0 < parts; e0 += UN) {
-                float2 v[UN][C::NTT][2];
-                float4 x[UN][C::KS][C::NTT];
+            for (int e = 0; e < WPH - 1; ++e, state += STATE)
 #pragma unroll
-                for (int u = 0; u < UN; ++u) {
-                    const size_t at = part(min(e0 + u, parts - 1));
-                    const float4* other = reinterpret_cast<const float4*>(p.part_o) + at * (S::REGS4 * 32) + lane;
-#pragma unroll
-                    for (int nt = 0; nt < C::NTT; ++nt) {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) v[u][nt][j] = __ldcg(ml + at * NT + nt * 8 + 2 * c + j);
-#pragma unroll
-                        for (int ms = 0; ms < C::KS; ++ms) x[u][ms][nt] = __ldcg(other + (ms * C::NTT + nt) * 32);
-                    }
+                for (int nt = 0; nt < C::NTT; ++nt) {
+                    const float4 ml = state[(S::REGS4 + nt) * 32];
+                    fold_state<C>(st, nt, make_float2(ml.x, ml.y), make_float2(ml.z, ml.w),
+                                  [&](int ms) { return state[(ms * C::NTT + nt) * 32]; });
                 }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->hand_free[h]));
+        }
+        const int parts = it.nsplit;                 // CTAs that hold parts of these rows
+        if (parts > 1) {
+            // Piece e lies in range range0 + e.  A range holds one unit that goes on from the range
+            // before and one that goes on into the next at most, which gives every piece and every
+            // ticket its place by range.
+            const auto slot = [&](int e) {
+                return static_cast<size_t>(2 * (it.range0 + e) + (e == 0 ? 1 : 0)) * HC + h;
+            };
+            // Many pieces are merged in two levels: groups of about sqrt(parts) neighbours first, then
+            // the groups.
+            int size = parts;
+            if (parts > S::MERGE_ONE)
+                for (size = S::MERGE_LEAST; size * size < parts;) ++size;
+            int e = it.split;                        // the piece this state stands for
+            int first = e / size * size, step = 1, n = min(size, parts - first);
+            bool top = size == parts, last = true;
+            float2* ml = reinterpret_cast<float2*>(p.part_ml);
+            for (;;) {
+                const size_t own = slot(e);
+                float4* mine = reinterpret_cast<float4*>(p.part_o) + own * (S::REGS4 * 32) + lane;
 #pragma unroll
-                for (int u = 0; u < UN; ++u) {
-                    if (e0 + u >= parts) break;
+                for (int ms = 0; ms < C::KS; ++ms)
 #pragma unroll
-                    for (int nt = 0; nt < C::NTT; ++nt) {
-                        float f[2], g[2];
+                    for (int nt = 0; nt < C::NTT; ++nt)
+                        mine[(ms * C::NTT + nt) * 32] =
+                            make_float4(st.o[ms][nt][0], st.o[ms][nt][1], st.o[ms][nt][2], st.o[ms][nt][3]);
+                if (r == 0) {
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const float2 w = v[u][nt][j];
-                            const float m = w.y > 0.f ? fmaxf(st.m[nt][j], w.x) : st.m[nt][j];
-                            f[j] = m > -INFINITY ? fast_exp2(st.m[nt][j] - m) : 1.f;
-                            g[j] = w.y > 0.f ? fast_exp2(w.x - m) : 0.f;
-                            st.m[nt][j] = m;
-                            st.l[nt][j] = st.l[nt][j] * f[j] + g[j] * w.y;
+                    for (int nt = 0; nt < C::NTT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            ml[own * NT + nt * 8 + 2 * c + j] = make_float2(st.m[nt][j], st.l[nt][j]);
+                }
+                // One acquire-release add by lane 0: the other lanes' stores come before it
+                // (__syncwarp), the loads of the last warp after it.
+                __syncwarp();
+                if (n > 1) {
+                    if (lane == 0) {
+                        int* ticket = p.tickets + ((top ? 0 : gridDim.x) + it.range0 + first) * HC + h;
+                        last = ticket_add(ticket) == n - 1;
+                        if (last) *ticket = 0;       // ready for the next call
+                    }
+                    last = __shfl_sync(FULL_MASK, last, 0);
+                    if (!last) break;
+                    __syncwarp();
+                    // all pieces in order (this warp's own among them), so the bits do not depend
+                    // on which warp is last
+                    reset_state(st);
+                    constexpr int UN = C::NTT == 1 ? 3 : 1;      // pieces in flight
+#pragma unroll 1
+                    for (int e0 = 0; e0 < n; e0 += UN) {
+                        float2 v[UN][C::NTT][2];
+                        float4 x[UN][C::KS][C::NTT];
+#pragma unroll
+                        for (int u = 0; u < UN; ++u) {
+                            const size_t at = slot(first + min(e0 + u, n - 1) * step);
+                            const float4* other = reinterpret_cast<const float4*>(p.part_o) + at * (S::REGS4 * 32) + lane;
+#pragma unroll
+                            for (int nt = 0; nt < C::NTT; ++nt) {
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) v[u][nt][j] = __ldcg(ml + at * NT + nt * 8 + 2 * c + j);
+#pragma unroll
+                                for (int ms = 0; ms < C::KS; ++ms) x[u][ms][nt] = __ldcg(other + (ms * C::NTT + nt) * 32);
+                            }
                         }
 #pragma unroll
-                        for (int ms = 0; ms < C::KS; ++ms) {
-                            const float4 y = x[u][ms][nt];
-                            st.o[ms][nt][0] = st.o[ms][nt][0] * f[0] + y.x * g[0];
-                            st.o[ms][nt][1] = st.o[ms][nt][1] * f[1] + y.y * g[1];
-                            st.o[ms][nt][2] = st.o[ms][nt][2] * f[0] + y.z * g[0];
-                            st.o[ms][nt][3] = st.o[ms][nt][3] * f[1] + y.w * g[1];
+                        for (int u = 0; u < UN; ++u) {
+                            if (e0 + u >= n) break;
+#pragma unroll
+                            for (int nt = 0; nt < C::NTT; ++nt)
+                                fold_state<C>(st, nt, v[u][nt][0], v[u][nt][1], [&](int ms) { return x[u][ms][nt]; });
                         }
                     }
                 }
+                if (top) break;
+                top = true;
+                e = first;
+                first = 0;
+                step = size;
+                n = (parts + size - 1) / size;
             }
+            if (!last) continue;
         }
         if constexpr (FP8) {
             const float vs = __ldg(p.v_scale + kvh);

@@ -84,8 +84,8 @@ cudaError_t launch_prefix(bool fp8, int head_dim, int block_size, int ctas, cons
 // Attention over a span of each sequence's keys (decode_span.cuh): the decode's parameters and
 // the rule of the rows.
 struct SpanParams {
-    // d.part_o [part][4 warps][head_tile * head_dim] in the accumulators' layout, d.part_ml
-    // [part][4 warps][head_tile][2]; d.tickets per (sequence, kv head, row tile); split_blocks,
+    // d.part_o [part][heads][head_tile * head_dim] in the accumulators' layout, d.part_ml
+    // [part][heads][head_tile][2], two parts per CTA; d.tickets two per CTA and head; split_blocks,
     // max_splits and merge_kernel are not used
     DecodeParams d;
     int block_size;

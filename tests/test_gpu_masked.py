@@ -209,6 +209,41 @@ def test_workspace_is_reused_streams_and_graphs():
     c.pool.destroy()
 
 
+def test_one_workspace_for_batches_of_any_size():
+    """A workspace of the largest call, zeroed once, under calls of other shapes: every call has to
+    find its counters at zero, whatever the ones before left in the rest."""
+    cs = [Cache(ctx=[900] * b, hq=8 * hk, hk=hk, d=128, bs=16, q_len=q, seed=b) for b, hk, q in
+          ((2, 1, 1), (40, 4, 1), (5, 2, 3), (64, 1, 1), (3, 4, 2))]
+    ws = torch.zeros(max(kp.paged_attention_masked_workspace_size(c.pool, c.B, c.hq, c.q_len, c.max_blocks, 0, s)
+                         for c in cs for s in (0, 16)), dtype=torch.uint8, device="cuda")
+    wants = [c.reference() for c in cs]
+    for s in (16, 0):
+        for c, want in zip(cs, wants):
+            c.check(*run(c, s, workspace=ws), want)
+    for c in cs:
+        assert c.pool.device_errors() == 0
+        c.pool.destroy()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("hk,q_len", [(4, 1), (2, 1), (1, 1), (4, 3), (2, 2), (1, 3)])
+def test_units_cut_into_many_pieces(hk, q_len, fp8):
+    """Two sequences over the whole grid: pieces merged in groups, then the groups; the same bits
+    every time."""
+    c = Cache(ctx=[15000, 4100], hq=8 * hk, hk=hk, d=128, bs=16, q_len=q_len, fp8=fp8, seed=3)
+    ws = torch.zeros(kp.paged_attention_masked_workspace_size(c.pool, 2, c.hq, q_len, c.max_blocks, 0, 16),
+                     dtype=torch.uint8, device="cuda")
+    want = c.reference()
+    for split in (0, 16):
+        first = run(c, split, workspace=ws)
+        c.check(*first, want)
+        for _ in range(5):
+            again = run(c, split, workspace=ws)
+            assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    assert c.pool.device_errors() == 0
+    c.pool.destroy()
+
+
 def test_window_shrinks_the_workspace():
     c = Cache(ctx=[700], hq=8, hk=2, d=128, bs=16)
     size = lambda w: kp.paged_attention_masked_workspace_size(c.pool, 1, 8, 1, c.max_blocks, w, 16)  # noqa: E731
