@@ -246,7 +246,9 @@ struct SpanPlan {
     long long units;
 };
 
-// Least positions of a CTA's range with the automatic choice.
+// Least positions of a CTA's range with the automatic choice: with fewer, small calls have more pieces
+// to merge, with more, fewer SMs at work (one sequence of 480 tokens: 5 10.4 us, 6 10.8, 10 12.6; four
+// samples of one prompt 17.2, 17.1, 21.6; larger calls do not depend on it).
 constexpr int kSpanLeast = 2 + kvp::SPAN_PAD;
 
 kv_status make_span_plan(const kv_pool* pl, int batch, int q_heads, int q_len, int max_blocks,
@@ -265,11 +267,21 @@ kv_status make_span_plan(const kv_pool* pl, int batch, int q_heads, int q_len, i
     const long long subs = static_cast<long long>(span_blocks) * (pl->block_size / 16) + kvp::SPAN_PAD;
     if (p.head_groups * subs > (1 << 30)) return KV_ERR_UNSUPPORTED;        // positions of a kv head group
     const long long resident = static_cast<long long>(pl->num_sms) * kvp::SPAN_CTAS;
-    p.heads = pl->kv_heads % 4 == 0 ? 4 : pl->kv_heads % 2 == 0 ? 2 : 1;
-    p.units = static_cast<long long>(batch) * (pl->kv_heads / p.heads) * p.head_groups;
     p.least = split_tokens > 0 ? split_tokens / 16 : kSpanLeast;
-    const long long most = (p.units * subs + p.least - 1) / p.least;
-    p.ctas = static_cast<int>(most < resident ? most : resident);
+    // Kv heads per CTA.  Four (where they divide): a warp owns its rows, and a unit's beginning and
+    // end are paid once for four heads -- 64 x 4,096 tokens of 8 heads, 8-bit: 125 us, with two heads
+    // 148, with one 203; bf16 163 / 166 / 184.  Two where four would leave CTAs without work, so that
+    // the same tokens are spread over twice the CTAs: 4 x 512 tokens of 8 heads 12.1 / 11.0 / 11.4 us,
+    // 16 x 512 14.2 / 12.8 / 14.7; with the grid just full they are even (64 x 512 tokens of 4 heads
+    // 15.7 / 16.3 / 20.5).
+    const auto cut = [&](int heads) {
+        p.heads = heads;
+        p.units = static_cast<long long>(batch) * (pl->kv_heads / heads) * p.head_groups;
+        const long long most = (p.units * subs + p.least - 1) / p.least;
+        p.ctas = static_cast<int>(most < resident ? most : resident);
+    };
+    cut(pl->kv_heads % 4 == 0 ? 4 : pl->kv_heads % 2 == 0 ? 2 : 1);
+    if (p.heads == 4 && p.ctas < resident) cut(2);
     *out = p;
     return KV_OK;
 }
