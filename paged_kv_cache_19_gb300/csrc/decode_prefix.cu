@@ -17,8 +17,13 @@
 //   * 0-3 and 4-7: two softmax teams, one per slot (128 rows: thread = row = tensor-memory lane).
 //     A pair of more than 128 rows has a row tile in each slot and both slots take every token
 //     tile; a pair of fewer has the same rows in both and the slots take alternate tiles, so
-//     that either way one slot's softmax runs while the tensor cores work for the other.
-//   * 8: loads.  A 128-token tile is 128 / block_size blocks, one TMA box each for K and for V:
+//     that either way one slot's softmax runs while the tensor cores work for the other; then team
+//     1 hands its state to team 0 through shared memory, which folds it into its own.  A row's
+//     scores are one thread's: its maximum and sum need no exchange.  The outputs leave through
+//     shared memory, so that a piece's rows are written whole.
+//   * 8: loads.  It walks the CTA's range and hands every run on (PFX_ITEMS ahead), so that only one
+//     warp reads the groups' arrays.  A 128-token tile is 128 / block_size blocks, one TMA box each
+//     for K and for V:
 //     8 slots x 128-byte pieces x octets of slots, so that the tile in shared memory is the
 //     tensor cores' canonical 128-byte-swizzled layout with 8-token groups one after another.
 //     K and V tiles go through one ring in the order the MMAs consume them.  Blocks past the
@@ -30,9 +35,19 @@
 //   * 10-13 (fp8 cache): convert each landed K or V tile of e4m3 codes to f16 (exact) into the
 //     ring the MMAs read.  The rows are f16 then too: a row of q is scaled by a power of two to
 //     below 2^15 first, undone in its score factor; probabilities are f16.
+//     Codes as the operand of an 8-bit MMA would need 8-bit probabilities next to them, off by
+//     2^-4; f16 ones are off by 2^-11, bf16 ones (bf16 cache, whose values f16 cannot hold) by 2^-8.
 // The output is rescaled only when the running maximum grows by more than 2^8 (log2 units):
 // until then the older maximum stays the reference, which is exact because the division at the
 // end uses the sum taken against the same reference.
+//
+// Measured on a GB300: 128 sequences of 64 query heads over 8 kv heads (1,024 rows a kv head) behind
+// one document of 16,384 tokens take the pass 62 us, 69 GFLOP a call = 1.1 PFLOP/s, the tensor cores
+// busy in 47 % of the cycles: a unit of 256 rows x 128 tokens costs about 2,850 cycles of MMA (the
+// score MMAs read Q and K from shared memory, 64 KB for 2 x 128 x 128 scores, and run at its
+// rate) and 1,590 of softmax beside them; the beginning of a run costs about 3,600 (q), its end 5,500
+// (8-bit: 10,000 for q, whose rows are scaled first).  32 groups of 8 sequences (32 rows, 512 tokens)
+// take about 22 us, bound by those.
 //
 // Every wait is bounded; a late barrier sets KV_DEVERR_TIMEOUT, every role leaves its loops, and
 // the CTA waits for its copies and MMAs in flight and frees its tensor memory.

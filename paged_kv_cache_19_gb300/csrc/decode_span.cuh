@@ -29,8 +29,18 @@
 // pieces of a unit cut by a range border go through global memory: each leaves its fp32 state in the
 // accumulators' layout, and the warp that finishes last merges them in order (tickets by range and
 // head, zero between calls); many pieces in two levels.
-// SPAN_FIGURES
-// Bound by the K/V bytes of the visible blocks.  The cap costs one ex2 and one reciprocal per
+// Bound by the K/V bytes of the visible blocks where there are many, by the kernel's beginning and
+// end where there are few, and with an 8-bit cache by the conversion of its codes in the consumer
+// warps.  Measured on a GB300, 32 query heads over 8 kv heads of 128 numbers, blocks of 16 unless said:
+//   one sequence of 300 tokens, capped                                    10.1 us
+//   64 sequences, window of 1,000 tokens, capped: 260 MB                  50.2 us (5.2 TB/s; about 4 us
+//     to start and 5 at the end, where the last pieces are merged and ranges end unevenly)
+//   64 sequences to 16 K tokens with a bias: 2.66 GB                     387 us (6.9 TB/s)
+//   packed documents, 4 new tokens, 8-bit: 77 MB                          29.2 us (2.6 TB/s)
+//   one sequence of 65,536 tokens, 4 kv heads: 134 MB                     42 us
+// Tried: one CTA per unit and chunk of tokens (9.6 / 59 / 433 / 38 us for the first four), a range per
+// warp instead of per CTA (15 / 54 / 414 / 38); all pieces of a unit merged by one warp (137 us for
+// the last).  The cap costs one ex2 and one reciprocal per
 // score (capped_tanh), the bias one add and one multiply; both are template flags, so a plain
 // mask pays for neither.  Every wait is bounded (WAIT_LIMIT_NS); a warp whose wait runs out sets
 // KV_DEVERR_TIMEOUT and leaves, and the producer waits for its copies in flight.
@@ -416,7 +426,10 @@ struct SpanCfg : DecodeCfg<FP8, D, SPAN_TOK, NT> {
     static constexpr int NST = BUDGET / (HSTAGE + LSE) < 16 ? BUDGET / (HSTAGE + LSE) : 16;
     static constexpr int SMEM = 1024 + NST * (HSTAGE + LSE) + HAND + CTL;
     static constexpr int QUEUE = 8;                 // items handed on ahead
-    // Pieces of a unit from which the merge takes two levels, and the least group.
+    // More pieces of a unit than this are merged in two levels, by groups of at least MERGE_LEAST: 48
+    // pieces (one sequence of 4,096 tokens, 4 kv heads) 25.8 us in one level, 16.4 in two, 300 pieces
+    // (65,536 tokens) 137 and 42; limits of 6, 12 and 20 give the same times, a few pieces are
+    // merged soonest without a second ticket.
     static constexpr int MERGE_ONE = 12, MERGE_LEAST = 3;
     static_assert(NST >= 3 && SMEM <= 227 * 1024, "a ring of three stages at least");
 };
