@@ -385,8 +385,10 @@ typedef struct kv_attention_mask {
  *     of block_size).  The result does not depend on it up to rounding.
  *   workspace: at least paged_attention_masked_workspace_size() bytes, never 0,
  *     zero-filled before its first use; every call leaves its counters at zero
- *     again (after KV_DEVERR_TIMEOUT, zero it before reuse).  Calls that share one
- *     must not overlap.  One kernel launch per call.
+ *     again (after KV_DEVERR_TIMEOUT, zero it before reuse).  Calls of any sizes and
+ *     pools of one device may share one, also with paged_shared_prefix_attention, if
+ *     they do not overlap; what another kind of call wrote to is no longer zero.
+ *     One kernel launch per call.
  *   Shapes, tables, outputs and errors as in paged_attention_multi_query.
  */
 kv_status paged_attention_masked(const kv_pool* pool, const void* q, int q_heads, int q_len,
@@ -423,9 +425,9 @@ kv_status paged_attention_masked_workspace_size(const kv_pool* pool, int batch, 
  *   n_groups == 0 is allowed (nothing is shared; the arrays may be NULL).
  *   kv_split_tokens: as in paged_attention_masked, for the members' own parts.
  *   workspace: at least paged_shared_prefix_workspace_size()
- *   bytes, zero-filled before its first use; calls that share one must not
- *   overlap.  Everything else as in paged_attention_multi_query.  Two kernel
- *   launches (one when n_groups is 0 or the batch is 1).
+ *   bytes, zero-filled before its first use and shared as that of
+ *   paged_attention_masked.  Everything else as in paged_attention_multi_query.
+ *   Two kernel launches (one when n_groups is 0 or the batch is 1).
  */
 kv_status paged_shared_prefix_attention(const kv_pool* pool, const void* q, int q_heads, int q_len,
                                         const int32_t* block_tables, int max_blocks,

@@ -31,12 +31,12 @@
 // head, zero between calls); many pieces in two levels.
 // Bound by the K/V bytes of the visible blocks where there are many, by the kernel's beginning and
 // end where there are few, and with an 8-bit cache by the conversion of its codes in the consumer
-// warps.  Measured on a GB300, 32 query heads over 8 kv heads of 128 numbers, blocks of 16 unless said:
+// warps.  Measured on a GB300, 32 query heads over 8 kv heads of 128 numbers unless said:
 //   one sequence of 300 tokens, capped                                    10.1 us
 //   64 sequences, window of 1,000 tokens, capped: 260 MB                  50.2 us (5.2 TB/s; about 4 us
 //     to start and 5 at the end, where the last pieces are merged and ranges end unevenly)
-//   64 sequences to 16 K tokens with a bias: 2.66 GB                     387 us (6.9 TB/s)
-//   packed documents, 4 new tokens, 8-bit: 77 MB                          29.2 us (2.6 TB/s)
+//   8 sequences to 128 K tokens, 64 query heads, with a bias: 2.66 GB    387 us (6.9 TB/s)
+//   33 sequences of packed documents, 7 new tokens, 32 kv heads, 8-bit: 77 MB  29.2 us (2.6 TB/s)
 //   one sequence of 65,536 tokens, 4 kv heads: 134 MB                     42 us
 // Tried: one CTA per unit and chunk of tokens (9.6 / 59 / 433 / 38 us for the first four), a range per
 // warp instead of per CTA (15 / 54 / 414 / 38); all pieces of a unit merged by one warp (137 us for

@@ -213,6 +213,27 @@ def test_another_stream_and_a_replayed_graph_with_other_groups():
     c.pool.destroy()
 
 
+def test_one_workspace_for_masked_and_shared_calls_of_any_size():
+    groups = [[(2, 40)], [(30, 9), (3, 25)], [(64, 4)], [(2, 2)]]
+    cs = [Cache(ctx=batch(g, 16, 300), hq=8 * hk, hk=hk, d=128, bs=16, shared=g, seed=hk) for g, hk in zip(groups, (1, 4, 8, 2))]
+    need = 0
+    for c in cs:
+        for split in (0, 16):
+            need = max(need, kp.paged_attention_masked_workspace_size(c.pool, c.B, c.hq, 1, c.max_blocks, 0, split),
+                       kp.paged_shared_prefix_workspace_size(c.pool, c.B, c.hq, 1, c.max_blocks, len(c.blocks), split))
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    wants = [c.reference() for c in cs]
+    for split in (16, 0):
+        for c, want in zip(cs, wants):
+            c.check(*run(c, split, workspace=ws), want)
+            out = torch.full_like(c.q, float("nan"))
+            kp.paged_attention_masked(c.pool, c.q, c.tables, c.lens, c.scale, kv_split_tokens=split, workspace=ws, out=out)
+            c.check(out, None, want)
+    for c in cs:
+        assert c.pool.device_errors() == 0
+        c.pool.destroy()
+
+
 def test_refusals():
     c = Cache(ctx=[40, 50], hq=4, hk=2, d=64, bs=16, shared=[(2, 1)])
     off, blk = i32(c.offsets), i32(c.blocks)
