@@ -35,7 +35,7 @@ struct kv_pool {
                             // per box (the wide tcgen05 decode)
     CUtensorMap tmh;        // latent pools with blocks of 64: one 128-byte piece of 32 slots
                             // per box (the narrow tcgen05 decode)
-    CUtensorMap tmsk, tmsv; // K and V pools in boxes of 16 slots (the span kernel)
+    CUtensorMap tmsk[3], tmsv[3]; // K and V pools in boxes of 16 slots of 1, 2, 4 kv heads (the span kernel)
     CUtensorMap tmpk, tmpv; // K and V pools in octets of slots (the shared prefix pass)
     int has_tc;
     int num_sms;
@@ -115,6 +115,29 @@ kv_status encode_pool_map(const kv_pool* p, uint8_t* base, CUtensorMap* map, int
                                                                           : row / 128), 1,
                                static_cast<cuuint32_t>(slots_per_box > 0 ? slots_per_box
                                                                          : p->block_size), 1};
+    const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
+    const CUtensorMapDataType dt = p->dtype == KV_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                             : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    CUresult r = fn(map, dt, 5, base, dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? KV_OK : KV_ERR_CUDA;
+}
+
+// Tile map of one pool half for the span kernel: dims (innermost first) = 128-byte row piece, pieces
+// per token row, slot, kv head, block; a box is 16 slots of `heads` kv heads, written head by head,
+// each as encode_pool_map's tile.
+kv_status encode_span_map(const kv_pool* p, uint8_t* base, int heads, CUtensorMap* map)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return KV_ERR_CUDA;
+    const cuuint64_t row = static_cast<cuuint64_t>(p->head_dim) * p->elem;
+    const cuuint64_t token = row * p->kv_heads;
+    const cuuint64_t dims[5] = {128 / p->elem, row / 128, static_cast<cuuint64_t>(p->block_size),
+                                static_cast<cuuint64_t>(p->kv_heads), static_cast<cuuint64_t>(p->num_blocks)};
+    const cuuint64_t strides[4] = {128, token, row, token * p->block_size};
+    const cuuint32_t box[5] = {static_cast<cuuint32_t>(128 / p->elem), static_cast<cuuint32_t>(row / 128), 16,
+                               static_cast<cuuint32_t>(heads), 1};
     const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
     const CUtensorMapDataType dt = p->dtype == KV_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                              : CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -462,8 +485,10 @@ kv_status kv_pool_create(int num_blocks, int block_size, int kv_heads, int head_
         st = KV_ERR_CUDA;
     if (st == KV_OK) st = encode_pool_map(p, p->k, &p->tmk);
     if (st == KV_OK) st = encode_pool_map(p, p->v, &p->tmv);
-    if (st == KV_OK) st = encode_pool_map(p, p->k, &p->tmsk, 16);
-    if (st == KV_OK) st = encode_pool_map(p, p->v, &p->tmsv, 16);
+    for (int i = 0; i < 3 && kv_heads % (1 << i) == 0; ++i) {
+        if (st == KV_OK) st = encode_span_map(p, p->k, 1 << i, &p->tmsk[i]);
+        if (st == KV_OK) st = encode_span_map(p, p->v, 1 << i, &p->tmsv[i]);
+    }
     if (st == KV_OK) st = encode_octet_map(p, p->k, &p->tmpk);
     if (st == KV_OK) st = encode_octet_map(p, p->v, &p->tmpv);
     if (st == KV_OK) {
@@ -885,7 +910,8 @@ kv_status launch_span(const kv_pool* pool, const SpanPlan& plan, kvp::SpanRule r
                       void* stream)
 {
     const auto launch = pool->dtype == KV_DTYPE_BF16 ? kvp::launch_span_bf16 : kvp::launch_span_fp8;
-    return launch(rule, pool->head_dim, plan.head_tile, plan.heads, plan.ctas, pool->tmsk, pool->tmsv, p,
+    const int map = plan.heads / 2;                  // 1, 2, 4 heads
+    return launch(rule, pool->head_dim, plan.head_tile, plan.heads, plan.ctas, pool->tmsk[map], pool->tmsv[map], p,
                   static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? KV_OK
                : KV_ERR_CUDA;

@@ -184,12 +184,21 @@ struct CausalRows {
     __device__ __forceinline__ int value_hi() const { return lim; }
 };
 
-// One cache block (BS tokens of one kv head, K tile at tk, V tile at tv in
-// shared memory) folded into the warp's online-softmax state, under the rule of `rows`.
-template <bool FP8, int D, int BS, int NT, class Rows>
-__device__ __forceinline__ void process_block_rows(uint32_t tk, uint32_t tv, const Rows& rows,
-                                                   const uint32_t (&qf)[D / 16][NT / 8][2],
-                                                   WarpState<DecodeCfg<FP8, D, BS, NT>>& st, int lane)
+// Where the K and V tiles of a block lie in shared memory: its first 16 tokens, and its others
+// (offset so that token t is found at t from there too).
+struct BlockTiles {
+    uint32_t k0, k1, v0, v1;
+    __device__ __forceinline__ BlockTiles(uint32_t k, uint32_t v) : k0(k), k1(k), v0(v), v1(v) {}
+    __device__ __forceinline__ BlockTiles(uint32_t ka, uint32_t kb, uint32_t va, uint32_t vb) : k0(ka), k1(kb), v0(va), v1(vb) {}
+    __device__ __forceinline__ uint32_t k(int mt) const { return mt == 0 ? k0 : k1; }
+    __device__ __forceinline__ uint32_t v(int mt) const { return mt == 0 ? v0 : v1; }
+};
+
+// One cache block (BS tokens of one kv head in shared memory) folded into the warp's
+// online-softmax state, under the rule of `rows`.
+template <bool FP8, int D, int BS, int NT, class Rows, class State>
+__device__ __forceinline__ void process_block_rows(const BlockTiles& tiles, const Rows& rows,
+                                                   const uint32_t (&qf)[D / 16][NT / 8][2], State& st, int lane)
 {
     using C = DecodeCfg<FP8, D, BS, NT>;
     const int r = lane >> 2;
@@ -211,17 +220,17 @@ __device__ __forceinline__ void process_block_rows(uint32_t tk, uint32_t tv, con
 #pragma unroll
             for (int ks = 0; ks < C::KS; ++ks) {
                 uint32_t a[4];
-                ldsm_x4(swz<C::DCH>(tk, tok, 2 * ks + (lane >> 4)), a);
+                ldsm_x4(swz<C::DCH>(tiles.k(mt), tok, 2 * ks + (lane >> 4)), a);
 #pragma unroll
                 for (int nt = 0; nt < C::NTT; ++nt)
                     mma_bf16_16816(s[mt][nt], a, qf[ks][nt][0], qf[ks][nt][1]);
             }
         } else {
             const int ta = mt * 16 + r;
-            const uint4 x0 = lds128(swz<1>(tk, ta, 2 * c));
-            const uint4 x1 = lds128(swz<1>(tk, ta, 2 * c + 1));
-            const uint4 y0 = lds128(swz<1>(tk, ta + 8, 2 * c));
-            const uint4 y1 = lds128(swz<1>(tk, ta + 8, 2 * c + 1));
+            const uint4 x0 = lds128(swz<1>(tiles.k(mt), ta, 2 * c));
+            const uint4 x1 = lds128(swz<1>(tiles.k(mt), ta, 2 * c + 1));
+            const uint4 y0 = lds128(swz<1>(tiles.k(mt), ta + 8, 2 * c));
+            const uint4 y1 = lds128(swz<1>(tiles.k(mt), ta + 8, 2 * c + 1));
             const uint32_t wa[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
             const uint32_t wb[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
 #pragma unroll
@@ -321,7 +330,7 @@ __device__ __forceinline__ void process_block_rows(uint32_t tk, uint32_t tv, con
 #pragma unroll
             for (int ms = 0; ms < C::KS; ++ms) {
                 uint32_t a[4];
-                ldsm_x4_trans(swz<C::DCH>(tv, tok, 2 * ms + (quad & 1)), a);
+                ldsm_x4_trans(swz<C::DCH>(tiles.v(mt), tok, 2 * ms + (quad & 1)), a);
                 a[0] &= mlo;
                 a[1] &= mlo;
                 a[2] &= mhi;
@@ -334,10 +343,10 @@ __device__ __forceinline__ void process_block_rows(uint32_t tk, uint32_t tv, con
             // Thread (r, c) reads d = 16r .. 16r+15 of tokens t0, t0+1, t0+8, t0+9.
             // Slice ms = 2w holds d = 16r + 4w (row r) and 16r + 4w + 1 (row r+8);
             // slice 2w+1 holds d = 16r + 4w + 2 and + 3.
-            uint4 v0 = lds128(swz<1>(tv, t0, r));
-            uint4 v1 = lds128(swz<1>(tv, t0 + 1, r));
-            uint4 v2 = lds128(swz<1>(tv, t0 + 8, r));
-            uint4 v3 = lds128(swz<1>(tv, t0 + 9, r));
+            uint4 v0 = lds128(swz<1>(tiles.v(mt), t0, r));
+            uint4 v1 = lds128(swz<1>(tiles.v(mt), t0 + 1, r));
+            uint4 v2 = lds128(swz<1>(tiles.v(mt), t0 + 8, r));
+            uint4 v3 = lds128(swz<1>(tiles.v(mt), t0 + 9, r));
             if (partial) {
                 const uint4 z = make_uint4(0u, 0u, 0u, 0u);
                 if (!held(t0)) v0 = z;
@@ -381,7 +390,7 @@ __device__ __forceinline__ void process_block(uint32_t tk, uint32_t tv, int lim,
                                               const uint32_t (&qf)[D / 16][NT / 8][2], float sl2,
                                               WarpState<DecodeCfg<FP8, D, BS, NT>>& st, int lane)
 {
-    process_block_rows<FP8, D, BS, NT>(tk, tv, CausalRows<NT / 8>{lim, dt, sl2}, qf, st, lane);
+    process_block_rows<FP8, D, BS, NT>(BlockTiles(tk, tv), CausalRows<NT / 8>{lim, dt, sl2}, qf, st, lane);
 }
 
 // The per-thread row sums of a warp summed over the 8 row groups sharing a column.

@@ -413,6 +413,7 @@ struct SpanCfg : DecodeCfg<FP8, D, SPAN_TOK, NT> {
     using C = DecodeCfg<FP8, D, SPAN_TOK, NT>;
     static constexpr int NCW = 4;                   // consumer warps
     static constexpr int WPH = NCW / HC;            // of one kv head
+    static constexpr bool PAIR = FP8 && WPH == 1 && NT == 8;      // a warp takes two sub-blocks at a time
     static constexpr int THREADS = (NCW + 1) * 32;
     static constexpr int MINB = SPAN_CTAS;          // CTAs per SM
     static constexpr int HSTAGE = HC * C::STAGE;    // K tiles of the heads, then V tiles; or the query
@@ -597,10 +598,9 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         SpanWalk<RULE, NT, HC> walk;
         walk.init(sp, ctl->range, total, ranges);
         const int per_block = sp.block_size / SPAN_TOK;                 // 1 or 2
-        // lane i < 2 HC loads the K (i < HC) or V tile of kv head kg * HC + i % HC
-        const int my_h = lane % HC;
-        const CUtensorMap* my_map = lane < HC ? &tmk : &tmv;
-        const uint32_t my_off = static_cast<uint32_t>((lane < HC ? 0 : HC * C::TILE) + my_h * C::TILE);
+        // lane 0 loads the K tiles of the heads, lane 1 the V tiles
+        const CUtensorMap* my_map = lane == 0 ? &tmk : &tmv;
+        const uint32_t my_off = lane == 0 ? 0u : static_cast<uint32_t>(HC * C::TILE);
         int ids = -1, ids_b = -1, ids_at = 0;        // table entries ids_at .. ids_at + 31 of sequence ids_b
         int n = 0;                                   // stages issued
         bool ok = true;
@@ -643,7 +643,16 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             PieceRows<NT, S::RPS> pr{0, 0};
             int2 run[SEGS];
             int pieces = 0;                          // stages of pieces
-            if (SUFFIX && it.seq.group >= 0 && it.split == 0) {
+            const auto count = [&](int g) {          // stages of segment g: the most any head has
+                int y = run[g].y;
+#pragma unroll
+                for (int o = HC / 2; o >= 1; o >>= 1) y = max(y, __shfl_xor_sync(FULL_MASK, y, o));
+                return __shfl_sync(FULL_MASK, y, 0);
+            };
+            // Looked up as late as the last sub-block, which has to say whether pieces follow: the loads
+            // before it need not wait for the shared pass.
+            const auto count_pieces = [&]() {
+                if (!SUFFIX || it.seq.group < 0 || it.split != 0) return;
                 grid_dependency_wait();              // the pieces of the shared pass are there
                 const PrefixGroup gr = load_prefix_group(sp.shared, it.seq.group);
                 const int pairs = prefix_pairs(sp.shared, gr);
@@ -660,18 +669,8 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     }
                     if (a < nh) a = pr.end(a);
                 }
-            }
-            const auto count = [&](int g) {          // stages of segment g: the most any head has
-                int y = run[g].y;
 #pragma unroll
-                for (int o = HC / 2; o >= 1; o >>= 1) y = max(y, __shfl_xor_sync(FULL_MASK, y, o));
-                return __shfl_sync(FULL_MASK, y, 0);
-            };
-            const auto count_pieces = [&]() {
-                if (SUFFIX && pr.nh > 0) {
-#pragma unroll
-                    for (int g = 0; g < SEGS; ++g) pieces += count(g);
-                }
+                for (int g = 0; g < SEGS; ++g) pieces += count(g);
             };
 
             // ---- the query rows
@@ -700,9 +699,9 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 ok = arm((good ? TAG_KV : TAG_SKIP) | (i + 1 == it.n && pieces == 0 ? TAG_LAST : 0),
                          good ? static_cast<uint32_t>(S::HSTAGE) : 0u);
                 if (!ok) break;
-                if (good && lane < 2 * HC)
-                    tma_load_5d(stage() + my_off, my_map, 0, 0, it.kg * HC + my_h,
-                                per_block == 2 ? (sub & 1) * SPAN_TOK : 0, blk, bar());
+                if (good && lane < 2)
+                    tma_load_5d(stage() + my_off, my_map, 0, 0, per_block == 2 ? (sub & 1) * SPAN_TOK : 0,
+                                it.kg * HC, blk, bar());
                 ++n;
             }
             if (!ok || pieces == 0) continue;
@@ -792,7 +791,33 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 if ((tag & 3) == TAG_KV && mine) {
                     const uint32_t tk = smem_u32(st_sm) + h * C::TILE;
                     rows.base = sub * SPAN_TOK;
-                    process_block_rows<FP8, D, SPAN_TOK, NT>(tk, tk + HC * C::TILE, rows, qf, st, lane);
+                    if constexpr (S::PAIR) {
+                        // the next stage with this one, where it is the next sub-block
+                        const int s2 = s + 1 == NST ? 0 : s + 1;
+                        int tag2 = TAG_Q;
+                        if (!last) {
+                            ok = all_ok(mbar_wait_bounded(smem_u32(&ctl->full[s2]),
+                                                          static_cast<uint32_t>((taken + 1) / NST) & 1u, wait_ns));
+                            if (!ok) break;
+                            tag2 = ctl->tag[s2];
+                        }
+                        if ((tag2 & 3) == TAG_KV) {
+                            const uint32_t tk2 = smem_u32(smem + s2 * S::HSTAGE) + h * C::TILE;
+                            constexpr uint32_t FIRST = C::TILE;         // (16 tokens of 128 bytes)
+                            process_block_rows<FP8, D, 2 * SPAN_TOK, NT>(
+                                BlockTiles(tk, tk2 - FIRST, tk + HC * C::TILE, tk2 + HC * C::TILE - FIRST), rows, qf, st, lane);
+                            last = tag2 & TAG_LAST;
+                            __syncwarp();
+                            if (lane == 0) {
+                                mbar_arrive(smem_u32(&ctl->empty[s]));
+                                mbar_arrive(smem_u32(&ctl->empty[s2]));
+                            }
+                            sub += 2;
+                            ++taken;
+                            continue;
+                        }
+                    }
+                    process_block_rows<FP8, D, SPAN_TOK, NT>(BlockTiles(tk, tk + HC * C::TILE), rows, qf, st, lane);
                 }
                 if (SUFFIX && (tag & 3) == TAG_PIECE && mine && (tag >> (24 + h) & 1))
                     fold_piece<FP8, D, NT>(reinterpret_cast<const float*>(st_sm + h * C::STAGE),
