@@ -374,7 +374,9 @@ typedef struct kv_attention_mask {
  *     max(first_keys[b], p - window + 1) <= t < max(p + 1, min(prefix_lens[b], ctx)),
  *   ctx = context_lens[b]; the score of a seen key is
  *     x = scale * q . K[t];  x = softcap * tanh(x / softcap);  x -= slope_h * |p - t|.
- *   A query that sees no key gets out = 0, lse = -inf.  Blocks that no query of a
+ *   A query that sees no key gets out = 0, lse = -inf.  What no query of a sequence
+ *   sees may hold anything; a value that one query sees and another does not has to
+ *   be finite for the other's sake.  Blocks that no query of a
  *   tile of rows sees are not read, and their table entries not looked at: blocks
  *   that fell out of a window may have been freed and reused.
  *   mask: HOST struct, copied by the call; NULL = no change.  softcap >= 0 with a
@@ -418,7 +420,8 @@ kv_status paged_attention_masked_workspace_size(const kv_pool* pool, int batch, 
  *   arrays.  group_offsets: int32 [n_groups + 1], not decreasing, in [0, batch];
  *   group_blocks: int32 [n_groups], in [0, max_blocks].  Sequences outside every
  *   group, groups of one, and groups with 0 shared blocks share nothing; a
- *   context may end inside its group's shared blocks (0 included).  Offsets that
+ *   context may end inside its group's shared blocks (0 included; values behind it
+ *   that others see have to be finite).  Offsets that
  *   break the rule (KV_DEVERR_GROUP): nothing is shared; a block count that
  *   does (KV_DEVERR_GROUP): that group shares nothing.  The results are right
  *   either way.

@@ -18,9 +18,10 @@
 // equal contiguous ranges, one per CTA.
 //   * One producer warp walks the CTA's range, hands every unit on through a queue in shared memory
 //     and streams what it needs through a ring of stages: the query rows, then its sub-blocks, HC
-//     heads at a time (5-D TMA tensor loads), then the pieces of the shared pass (bulk copies).  It
-//     runs ahead over unit borders, so the consumers read nothing from global memory themselves and
-//     find the next unit's lengths and data there.
+//     heads at a time (one 5-D TMA tensor load for their K tiles, one for V; a load per head and tile
+//     took 8-bit caches 117 us instead of 111 for 64 x 4,096 tokens), then the pieces of the shared
+//     pass (bulk copies).  It runs ahead over unit borders, so the consumers read nothing from global
+//     memory themselves and find the next unit's lengths and data there.
 //   * Four consumer warps, 4 / HC per kv head, fold their head's tile of a sub-block (every
 //     (4 / HC)-th one) into an online-softmax state in registers (decode_common.cuh,
 //     process_block_rows under the rule of SpanRows).  With four heads a warp owns its rows and
@@ -33,10 +34,11 @@
 // end where there are few, and with an 8-bit cache by the conversion of its codes in the consumer
 // warps.  Measured on a GB300, 32 query heads over 8 kv heads of 128 numbers unless said:
 //   one sequence of 300 tokens, capped                                    10.1 us
-//   64 sequences, window of 1,000 tokens, capped: 260 MB                  50.2 us (5.2 TB/s; about 4 us
+//   64 sequences, window of 1,000 tokens, capped: 260 MB                  50.4 us (5.2 TB/s; about 4 us
 //     to start and 5 at the end, where the last pieces are merged and ranges end unevenly)
 //   8 sequences to 128 K tokens, 64 query heads, with a bias: 2.66 GB    387 us (6.9 TB/s)
-//   33 sequences of packed documents, 7 new tokens, 32 kv heads, 8-bit: 77 MB  29.2 us (2.6 TB/s)
+//   33 sequences of packed documents, 7 new tokens, 32 kv heads, 8-bit: 77 MB  27.6 us (2.8 TB/s)
+//   64 sequences of 4,096 tokens, 64 query heads: bf16 165 us (6.5 TB/s), 8-bit 104 us (5.1 TB/s)
 //   one sequence of 65,536 tokens, 4 kv heads: 134 MB                     42 us
 // Tried: one CTA per unit and chunk of tokens (9.6 / 59 / 433 / 38 us for the first four), a range per
 // warp instead of per CTA (15 / 54 / 414 / 38); all pieces of a unit merged by one warp (137 us for
@@ -408,12 +410,18 @@ __device__ __forceinline__ void fold_piece(const float* o, const float* lse, int
         }
 }
 
+// Whether a warp takes two sub-blocks at a time: an 8-bit cache's 16 tokens are too little work between
+// two waits, and the two tiles are independent.  One / two: 64 sequences of 4,096 tokens 111 / 104 us,
+// packed documents 28.8 / 27.6; behind a shared prefix, whose own parts are short, 81 / 84.  (With
+// bf16 the loads are what a warp waits for, and 16-row tiles lack the registers.)
+template <bool FP8, int NT, int HC, int RULE>
+constexpr bool span_pairs() { return FP8 && NT == 8 && HC == 4 && RULE != SPAN_SUFFIX; }
+
 template <bool FP8, int D, int NT, int HC>
 struct SpanCfg : DecodeCfg<FP8, D, SPAN_TOK, NT> {
     using C = DecodeCfg<FP8, D, SPAN_TOK, NT>;
     static constexpr int NCW = 4;                   // consumer warps
     static constexpr int WPH = NCW / HC;            // of one kv head
-    static constexpr bool PAIR = FP8 && WPH == 1 && NT == 8;      // a warp takes two sub-blocks at a time
     static constexpr int THREADS = (NCW + 1) * 32;
     static constexpr int MINB = SPAN_CTAS;          // CTAs per SM
     static constexpr int HSTAGE = HC * C::STAGE;    // K tiles of the heads, then V tiles; or the query
@@ -791,7 +799,8 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 if ((tag & 3) == TAG_KV && mine) {
                     const uint32_t tk = smem_u32(st_sm) + h * C::TILE;
                     rows.base = sub * SPAN_TOK;
-                    if constexpr (S::PAIR) {
+                    if constexpr (span_pairs<FP8, NT, HC, RULE>()) {
+                        static_assert(WPH == 1, "a warp takes every sub-block of its head");
                         // the next stage with this one, where it is the next sub-block
                         const int s2 = s + 1 == NST ? 0 : s + 1;
                         int tag2 = TAG_Q;
