@@ -46,7 +46,7 @@
 // busy in 47 % of the cycles: a unit of 256 rows x 128 tokens costs about 2,850 cycles of MMA (the
 // score MMAs read Q and K from shared memory, 64 KB for 2 x 128 x 128 scores, and run at its
 // rate) and 1,590 of softmax beside them; the beginning of a run costs about 3,600 (q), its end 5,500
-// (8-bit: 10,000 for q, whose rows are scaled first).  32 groups of 8 sequences (32 rows, 512 tokens)
+// (8-bit: more, the rows of q are scaled to f16 in place first).  32 groups of 8 sequences (32 rows, 512 tokens)
 // take about 22 us, bound by those.
 //
 // Every wait is bounded; a late barrier sets KV_DEVERR_TIMEOUT, every role leaves its loops, and
@@ -109,11 +109,7 @@ struct PfxCtl {
     int group0, ctas;                               // group that holds lo; CTAs with units
     long long scan[14];
     uint64_t x_full, e_done[2];                     // team 1's state handed over; a team is done with an item
-    union {
-        float q_up[2][PFX_TILE];                    // fp8: undoes a row's power-of-two scale (read at an
-                                                    // item's start)
-        float2 x_ml[PFX_TILE];                      // team 1's maxima and sums (written at its end)
-    };
+    float2 x_ml[PFX_TILE];                          // team 1's maxima and sums
 };
 
 
@@ -591,7 +587,6 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             const int rows = it.both ? it.rows : min(PFX_TILE, it.rows - s * PFX_TILE);
             constexpr int CH = D / 8;               // 16-byte chunks of a row
             constexpr int RPI = 32 / CH;            // rows of a warp-wide load
-            constexpr int INF = 8;                  // loads in flight (8-bit cache; else all of them)
             const int ch = lane % CH;
             int r = w * 32 + lane / CH;             // the lane's row, its member and row of the member
             int m = (first + r) / p.rows, rr = first + r - m * p.rows;
@@ -606,44 +601,41 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             };
             // (loops are kept rolled: a launch fetches its code once, and a tile or two per CTA is all
             // that a short prefix has to hide that behind)
-            if constexpr (!FP8) {
 #pragma unroll 2
-                for (int j = 0; j < CH; ++j, step()) {
-                    if (r < rows)
-                        cp_async16(target(), source());
-                    else
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(target()), "r"(0u) : "memory");
+            for (int j = 0; j < CH; ++j, step()) {
+                if (r < rows)
+                    cp_async16(target(), source());
+                else
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(target()), "r"(0u) : "memory");
+            }
+            cp_async_wait_all();
+            float q_up = 1.f;                       // undoes the row's power-of-two scale
+            if constexpr (FP8) {
+                // Each lane its row, in place: the largest magnitude to [2^14, 2^15) by a power of two,
+                // then f16.
+                __syncwarp();
+                const auto chunk = [&](int c) { return qs + (c >> 3) * (PFX_TILE * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4); };
+                uint32_t top = 0;                   // magnitudes of bf16 pairs order like integers
+#pragma unroll 4
+                for (int c = 0; c < CH; ++c) {
+                    const uint4 x = lds128(chunk(c));
+                    top = __vmaxu2(__vmaxu2(top, __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu)),
+                                   __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
                 }
-                cp_async_wait_all();
-            } else {
-#pragma unroll 1
-                for (int j0 = 0; j0 < CH; j0 += INF) {
-                    uint4 x[INF];
-                    const int r0 = r;
+                const uint32_t big = max(top << 16, top & 0xffff0000u);
+                const int ex = min(254, max(14, 268 - static_cast<int>(big >> 23)));      // of the factor
+                q_up = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
+                const float down = __uint_as_float(static_cast<uint32_t>(ex) << 23);
+#pragma unroll 2
+                for (int c = 0; c < CH; ++c) {
+                    const uint4 x = lds128(chunk(c));
+                    uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                    for (int j = 0; j < INF; ++j, step()) x[j] = r < rows ? __ldg(source()) : make_uint4(0u, 0u, 0u, 0u);
-                    r = r0;
-#pragma unroll
-                    for (int j = 0; j < INF; ++j, r += RPI) {
-                        // the row's largest magnitude to [2^14, 2^15) by a power of two, then f16
-                        uint32_t v[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-                        uint32_t big = 0;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            big = max(big, max((v[e] & 0x7fffu) << 16, v[e] & 0x7fff0000u));
-#pragma unroll
-                        for (int o = CH / 2; o >= 1; o >>= 1) big = max(big, __shfl_xor_sync(FULL_MASK, big, o));
-                        const int ex = min(254, max(14, 268 - static_cast<int>(big >> 23)));  // of the factor
-                        const float up = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
-                        const float down = __uint_as_float(static_cast<uint32_t>(ex) << 23);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            v[e] = pack_f16x2(__uint_as_float(v[e] << 16) * down, __uint_as_float(v[e] & 0xffff0000u) * down);
-                        if (ch == 0) ctl->q_up[s][r] = up;
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(target()), "r"(v[0]), "r"(v[1]),
-                                     "r"(v[2]), "r"(v[3])
-                                     : "memory");
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = pack_f16x2(__uint_as_float(v[e] << 16) * down, __uint_as_float(v[e] & 0xffff0000u) * down);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(chunk(c)), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                                 "r"(v[3])
+                                 : "memory");
                 }
             }
             fence_proxy_async_smem();
@@ -653,7 +645,7 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
 
             // ---- the row: its visible tokens of the prefix, its score factor
             float mult0 = p.scale_log2;
-            if constexpr (FP8) mult0 *= ctl->q_up[s][row] * __ldg(p.k_scale + it.kvh);
+            if constexpr (FP8) mult0 *= q_up * __ldg(p.k_scale + it.kvh);
             int lim = 1 << 30;                      // a row of padding: never masked, never stored
             const bool idle = w * 32 >= rows;       // a warp of padding: its probabilities are left
             if (row < rows) {                       // as they are, they reach its own rows alone
