@@ -8,6 +8,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
+#include <exception>
 
 #include "kv_paged.h"
 
@@ -35,6 +36,11 @@ struct Args {
         const int64_t v = integer(i);
         if (v < INT32_MIN || v > INT32_MAX) fail(PyExc_ValueError, name, "a 32-bit integer");
         return static_cast<int>(v);
+    }
+    // A size that the C ABI takes as an int.
+    void fits(int64_t n, const char* name)
+    {
+        if (n > INT32_MAX) fail(PyExc_ValueError, name, "of fewer than 2^31 entries per dimension");
     }
     float real(int i)
     {
@@ -123,6 +129,9 @@ struct Queries {
         heads = t->size(1);
         q_len = t->dim() == 4 ? t->size(2) : 1;
         max_blocks = b->size(1);
+        for (const int64_t n : {batch, heads, q_len}) a.fits(n, "q");
+        a.fits(max_blocks, "block_tables");
+        if (!a.ok) return;
         rows = batch * heads * q_len;
         q = a.data(qi, at::kBFloat16, rows * d, "q");
         tables = a.data<const int32_t>(ti, at::kInt, batch * max_blocks, "block_tables");
@@ -146,6 +155,10 @@ PyObject* norm_rope_append(PyObject*, PyObject* const* args, Py_ssize_t nargs)
     if (!a.ok) return nullptr;
     const int64_t n = q->size(0), heads = q->size(1), batch = tab->size(0), max_blocks = tab->size(1);
     const int64_t positions = rope != nullptr ? rope->size(0) : 0, rope_dim = rope != nullptr ? rope->size(1) : 0;
+    for (const int64_t m : {n, heads}) a.fits(m, "q");
+    for (const int64_t m : {batch, max_blocks}) a.fits(m, "block_tables");
+    a.fits(positions, "rope_table");
+    a.fits(rope_dim, "rope_table");
     const int q_len = a.small(13, "q_len");
     if (a.ok && (q_len < 1 || n % q_len != 0)) a.fail(PyExc_ValueError, "the tokens", "q_len per sequence");
     int64_t qs = 0, ks = 0, vs = 0;
@@ -212,6 +225,7 @@ PyObject* shared_prefix_attention(PyObject*, PyObject* const* args, Py_ssize_t n
     const int32_t* ctx = a.data<const int32_t>(4, at::kInt, q.batch, "context_lens");
     const at::Tensor* blk = a.tensor(6, "group_blocks");
     const int64_t groups = blk != nullptr ? blk->numel() : 0;
+    a.fits(groups, "group_blocks");
     const int32_t* offsets = a.data<const int32_t>(5, at::kInt, groups + 1, "group_offsets");
     const int32_t* blocks = a.data<const int32_t>(6, at::kInt, groups, "group_blocks");
     const float scale = a.real(7);
@@ -228,13 +242,27 @@ PyObject* shared_prefix_attention(PyObject*, PyObject* const* args, Py_ssize_t n
                                                    reinterpret_cast<void*>(stream)));
 }
 
-template <typename F>
-PyCFunction fast(F f) { return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)); }
+// The C entry: torch throws where a tensor has no strides or no memory (sparse, meta, fake).
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyObject* guarded(PyObject* self, PyObject* const* args, Py_ssize_t nargs)
+{
+    try {
+        return F(self, args, nargs);
+    } catch (const std::exception& e) {
+        if (!PyErr_Occurred()) PyErr_Format(PyExc_ValueError, "a tensor without plain memory: %s", e.what());
+    } catch (...) {
+        if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a tensor without plain memory");
+    }
+    return nullptr;
+}
+
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyCFunction fast() { return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<F>)); }
 
 PyMethodDef methods[] = {
-    {"norm_rope_append", fast(norm_rope_append), METH_FASTCALL, "paged_norm_rope_append"},
-    {"attention_masked", fast(attention_masked), METH_FASTCALL, "paged_attention_masked"},
-    {"shared_prefix_attention", fast(shared_prefix_attention), METH_FASTCALL, "paged_shared_prefix_attention"},
+    {"norm_rope_append", fast<norm_rope_append>(), METH_FASTCALL, "paged_norm_rope_append"},
+    {"attention_masked", fast<attention_masked>(), METH_FASTCALL, "paged_attention_masked"},
+    {"shared_prefix_attention", fast<shared_prefix_attention>(), METH_FASTCALL, "paged_shared_prefix_attention"},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", "Native argument checks of the per-layer calls.", -1, methods,

@@ -298,6 +298,24 @@ def test_refusals():
     c.pool.destroy()
 
 
+def test_sparse_tensors_raise():
+    """Torch throws for their strides and memory; the calls turn that into a ValueError."""
+    c = Cache(ctx=[40, 30], hq=4, hk=2, d=64, bs=16)
+    ws = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+    out, off, blk = torch.empty_like(c.q), i32([0, 2]), i32([1])
+    kv = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device="cuda")
+    base = dict(pool=c.pool, q=c.q, block_tables=c.tables, context_lens=c.lens, out=out)
+    for call, kw in ((kp.paged_attention_masked, dict(base, scale=1.0, workspace=ws, first_keys=c.lens)),
+                     (kp.paged_shared_prefix_attention, dict(base, scale=1.0, workspace=ws, group_offsets=off, group_blocks=blk)),
+                     (kp.paged_norm_rope_append, dict(base, q=c.q[:, :, 0], k=kv, v=kv))):
+        for name, t in kw.items():
+            if isinstance(t, torch.Tensor):
+                with pytest.raises((ValueError, RuntimeError)):
+                    call(**dict(kw, **{name: t.to_sparse()}))
+    assert c.pool.device_errors() == 0
+    c.pool.destroy()
+
+
 def test_a_stage_that_never_lands_times_out():
     c = Cache(ctx=[900], hq=4, hk=1, d=128, bs=16)
     kp.kv_debug_decode_stall(3, 20_000_000)

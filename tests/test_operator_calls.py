@@ -60,6 +60,30 @@ def test_host_tensors_are_refused(lib):
             call(*args[:1], 128, *args[2:])
 
 
+def test_tensors_without_plain_memory_are_refused(lib):
+    """Sparse, meta and fake tensors make torch throw below the binding; sizes past 32 bits do not
+    fit the C ABI.  Meta tensors stand in for the large ones."""
+    import torch
+    c = kp._native()
+    q, kv = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    t, l = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)  # noqa: E741
+    out = torch.empty_like(q)
+    calls = ((c.norm_rope_append, (1, 64, 2, q, kv, kv, t, l, None, None, 1e-6, None, False, 1, None, None, out, 0)),
+             (c.attention_masked, (1, 64, q, t, l, 1.0, 0.0, 0, None, None, None, 0, None, out, None, 0)),
+             (c.shared_prefix_attention, (1, 64, q, t, l, l, l[:1], 1.0, 0, None, out, None, 0)))
+    for call, args in calls:
+        for odd in (lambda x: x.to("meta"), lambda x: x.to_sparse(), lambda x: x.to(torch.float32).to_sparse()):
+            with pytest.raises(ValueError):
+                call(*[odd(x) if isinstance(x, torch.Tensor) else x for x in args])
+            for i, x in enumerate(args):
+                if isinstance(x, torch.Tensor):
+                    with pytest.raises(ValueError):
+                        call(*args[:i], odd(x), *args[i + 1:])
+        wide = torch.empty(2, 2 ** 32 + 3, dtype=torch.int32, device="meta")
+        with pytest.raises(ValueError, match="2.31|CUDA"):
+            call(*[wide if x is t else x for x in args])
+
+
 def groups(bm, seqs, **kw):
     order, off, blk = (t.tolist() for t in bm.prefix_groups(seqs, **kw))
     assert sorted(order) == list(range(len(seqs))) and off[0] == 0 and off[-1] == len(seqs) and len(off) == len(blk) + 1
