@@ -24,7 +24,7 @@
 //   * streaming (prompts): see paged_norm_rope_append_stream.
 // Measured on a GB300 (32 query heads and 8 kv heads of 128 numbers, normalised and rotated):
 //   1 token          2.0 us, 64 tokens 2.35 us: the latency of position -> table -> row and a launch
-//   185 tokens of 96 rows, rotated by half, 8-bit cache   4.4 us
+//   185 tokens of 96 rows, rotated by half, 8-bit cache   4.25 us
 //   8,191 tokens    39.5 us for 206 MB (5.2 TB/s, 77 % of the copy rate; the schedulers issue in 61 %
 //     of the cycles).  The direct form takes 62 us: it looks the place of every token up anew in each
 //     of the token's lane groups.
@@ -40,7 +40,7 @@ constexpr int NRA_THREADS = 256;
 // Rows per SM up to which a lane group of the direct form takes one row, or two (else four): fewer
 // rows per lane group start sooner, more of them pay a token's lookups once.  With 1 / 2 / 4 rows:
 // 1 token of 48 rows 2.05 / 2.40 / 3.2 us, 64 tokens 2.36 / 2.54 / 3.3, 185 tokens of 96 rows (8-bit)
-// 5.44 / 4.43 / 5.09; with 2 / 4: 456 tokens of 48 rows 5.02 / 5.27, 700 tokens 5.74 / 5.38.
+// 5.44 / 4.43 / 5.09 (before the codes came from products); with 2 / 4: 456 tokens of 48 rows 5.02 / 5.27, 700 tokens 5.74 / 5.38.
 constexpr int NRA_ROWS_1 = 54, NRA_ROWS_2 = 160;
 // Tokens per CTA from which the streaming form is taken.  Streaming / direct: 1,000 tokens 8.1 / 7.5 us,
 // 1,400 tokens 10.9 / 10.7, 2,000 tokens 13.8 / 15.4, 8,191 tokens 39.9 / 62.
@@ -65,13 +65,38 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
     return d;
 }
 
-// Four e4m3 codes of y / scale, low element first (the arithmetic of e4m3_codes8).
-__device__ __forceinline__ uint32_t e4m3_codes4(float2 lo, float2 hi, float scale)
+__device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b)
 {
-    const float2 a = make_float2(__fdiv_rn(lo.x, scale), __fdiv_rn(lo.y, scale));
-    const float2 b = make_float2(__fdiv_rn(hi.x, scale), __fdiv_rn(hi.y, scale));
     return (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3)) & 0xffffu) |
            (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3)) << 16);
+}
+
+// e4m3 codes of y / scale, low element first, the bits of e4m3_codes8 (the quotient rounded to
+// binary32, then the code).  The product with the reciprocal is off from that quotient by three
+// steps of binary32 at most (1.5 2^-23 relative: two roundings against one), and the codes change
+// only where the low 19 bits of a number are zero (between two codes: four significant bits below
+// the codes' own), so the product gives the same code unless it is within four steps of such a
+// number; then, and for scales whose reciprocal could leave the normal range, the division decides.
+// (8,192 tokens of 48 rows 42.0 us, 43.6 with divisions only; 185 tokens of 96 rows 4.25 and 4.42.)
+__device__ __forceinline__ uint2 e4m3_codes(const float2 (&y)[4], float scale)
+{
+    const float inv = __frcp_rn(scale);
+    const float2 inv2 = make_float2(inv, inv);
+    float2 q[4];
+    uint32_t near = ~0u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        q[e] = mul2(y[e], inv2);
+        near = min(near, min((__float_as_uint(q[e].x) + 4u) & 0x7ffffu, (__float_as_uint(q[e].y) + 4u) & 0x7ffffu));
+    }
+    const uint32_t bits = __float_as_uint(scale);
+    const bool exact = (bits & 0x7fffffu) == 0;     // a power of two: the product is the quotient
+    const bool normal = (bits >> 23) - 28u < 200u;  // positive, 2^-99 .. 2^100
+    if (!normal || (near <= 8 && !exact)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q[e] = make_float2(__fdiv_rn(y[e].x, scale), __fdiv_rn(y[e].y, scale));
+    }
+    return make_uint2(e4m3x4(q[0], q[1]), e4m3x4(q[2], q[3]));
 }
 
 __device__ __forceinline__ float2 bf16x2_floats(uint32_t w)
@@ -182,8 +207,9 @@ __device__ __forceinline__ void nra_store(uint16_t* dst, const NraLane& ln, cons
 
 __device__ __forceinline__ void nra_store_codes(uint8_t* dst, const NraLane& ln, const float2 (&y)[4], float scale)
 {
-    *reinterpret_cast<uint32_t*>(dst + ln.at[0]) = e4m3_codes4(y[0], y[1], scale);
-    *reinterpret_cast<uint32_t*>(dst + ln.at[1]) = e4m3_codes4(y[2], y[3], scale);
+    const uint2 codes = e4m3_codes(y, scale);
+    *reinterpret_cast<uint32_t*>(dst + ln.at[0]) = codes.x;
+    *reinterpret_cast<uint32_t*>(dst + ln.at[1]) = codes.y;
 }
 
 // Key (r < kv_heads) or value row of a cached token whose slot's rows begin at row `slot` of the

@@ -215,6 +215,32 @@ def test_without_norm_and_rotation_it_is_the_append():
         c.pool.destroy()
 
 
+@pytest.mark.parametrize("repeat", [1, 4])
+def test_every_bf16_value_rounds_as_the_append_does(repeat):
+    """All 65,536 bf16 patterns under many scales: quotients at, next to and far from the values
+    where the code changes, powers of two, and scales at the ends of the range."""
+    r = np.random.default_rng(5)
+    scales = np.concatenate([r.uniform(0.001, 0.1, 9), [1.0, 2.0 ** -7, 1 / 3, 0.3, 1e-40, 2.0 ** -149, 3e38, 1e-30, 1e30, 2.0 ** 100,
+                                                        1.5 * 2.0 ** -99, 448.0, 7.0, 0.9999999, 1.0000001, 17 / 16, 15 / 8]])
+    scales = np.resize(scales.astype(np.float32), 32)
+    n = 512 * repeat
+    rows = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(512, 1, 128)
+    rows = rows.expand(512, 32, 128).repeat(repeat, 1, 1).cuda()
+    q = torch.zeros(n, 8, 128, dtype=torch.bfloat16, device="cuda")
+    pool = kp.kv_pool_create(n // 32, 32, 32, 128, "fp8_e4m3")
+    pool.set_scales(scales, scales[::-1].copy())
+    tab = i32(r.permutation(n // 32)[None])
+    seq, pos = i32(np.zeros(n)), i32(np.arange(n))
+    kp.paged_norm_rope_append(pool, q, rows, rows, tab, token_seq=seq, token_pos=pos)
+    mine = [t.clone() for t in pool.raw_bytes()]
+    for t in pool.raw_bytes():
+        t.fill_(POISON)
+    kp.paged_kv_append(pool, rows, rows, tab, None, token_seq=seq, token_pos=pos)
+    for a, b in zip(mine, pool.raw_bytes()):
+        assert torch.equal(a, b)
+    pool.destroy()
+
+
 def test_far_positions_and_extreme_rows():
     """Rows of zeros (the norm's eps), of tiny and of large numbers, infinities kept to their row."""
     c = Call(hq=4, hk=2, d=128, bs=16, rope_dim=128, batch=1, seq=[0] * 4, pos=[70000, 0, 69999, 31], eps=1e-5)
