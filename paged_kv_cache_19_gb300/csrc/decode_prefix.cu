@@ -62,6 +62,11 @@ namespace {
 
 constexpr float PFX_RESCALE_LOG2 = 8.f;
 constexpr int PFX_MASKS = 16;                       // ring of per-tile block masks
+// A CTA's range has sqrt(PFX_CUT x tiles of the longest run) positions at least: a longer range takes the
+// pass longer, every further piece of a run its members' merge.  With 0 (every CTA works) / 0.25 / 0.5 /
+// 1 / 2, few members behind long prefixes: 3 sequences behind 12,215 tokens 48 / 34 / 36 / 41 / 46 us,
+// 5 behind 11,788 54 / 42 / 40 / 41 / 44, 14 behind 3,185 32 / 28 / 25 / 26 / 28; many runs do not care.
+constexpr float PFX_CUT = 0.5f;
 
 template <bool FP8, int D, int BS>
 struct PfxCfg {
@@ -108,6 +113,7 @@ struct PfxCtl {
     long long base;                                 // first unit of group0
     int group0, ctas;                               // group that holds lo; CTAs with units
     long long scan[14];
+    int longest[14];                                // tiles of the longest run, by warp
     uint64_t x_full, e_done[2];                     // team 1's state handed over; a team is done with an item
     float2 x_ml[PFX_TILE];                          // team 1's maxima and sums
 };
@@ -306,6 +312,7 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     // total and the checks, then the group that holds the range's first unit.
     {
         long long sum = 0;
+        int longest = 0;                            // tiles of a run
         bool ok = true, blocks_ok = true;
         for (int g = tid; g < p.n_groups; g += C::THREADS) {
             ok = ok && prefix_offsets_ok(p, g);
@@ -315,16 +322,26 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             w.g = g;
             w.load(p, BS);
             sum += w.units;
+            if (w.units > 0) longest = max(longest, w.tiles);
         }
         if ((!ok || !blocks_ok) && blockIdx.x == 0) atomicOr(p.err, KV_DEVERR_GROUP);
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
-        if (lane == 0) ctl->scan[warp] = sum;
+        longest = __reduce_max_sync(FULL_MASK, longest);
+        if (lane == 0) {
+            ctl->scan[warp] = sum;
+            ctl->longest[warp] = longest;
+        }
         const bool all = __syncthreads_and(ok);     // bad offsets: nothing is shared
         long long units = 0;
-        for (int w = 0; w < C::THREADS / 32; ++w) units += ctl->scan[w];
+        for (int w = 0; w < C::THREADS / 32; ++w) {
+            units += ctl->scan[w];
+            longest = max(longest, ctl->longest[w]);
+        }
         if (!all) units = 0;
-        const int ctas = units < gridDim.x ? static_cast<int>(units) : static_cast<int>(gridDim.x);
+        const long long least = max(1, static_cast<int>(sqrtf(PFX_CUT * static_cast<float>(longest))));
+        const long long most = (units + least - 1) / least;
+        const int ctas = most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
         const int c = blockIdx.x;
         const long long lo = c < ctas ? div_small(units * c, ctas) : 0;
         const long long hi = c < ctas ? div_small(units * (c + 1), ctas) : 0;

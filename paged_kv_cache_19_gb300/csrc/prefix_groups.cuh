@@ -7,7 +7,8 @@
 // row m * rows + r); they are cut into pairs of 128-row tiles (256 rows).  A run is one
 // (group, kv head, pair): PFX_PAD positions for what starting it costs, then its units, the 128-token
 // tiles of the prefix.  Positions are numbered in the order (group, kv head, pair, tile); CTA c of G
-// takes the positions [P c / G, P (c+1) / G) of all P.
+// takes the positions [P c / G, P (c+1) / G) of all P (G: the grid, or fewer where that keeps ranges
+// from being too short).
 #pragma once
 
 #include "device_common.cuh"

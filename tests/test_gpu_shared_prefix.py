@@ -67,6 +67,16 @@ def test_long_prefix_over_every_sm():
     c.pool.destroy()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_few_members_behind_long_prefixes(fp8):
+    """Runs cut into fewer pieces than there are SMs, beside short ones."""
+    groups = [(2, 390), (3, 30), (2, 1)]
+    c = Cache(ctx=batch(groups, 32, 50), hq=4, hk=1, d=128, bs=32, fp8=fp8, shared=groups, seed=6)
+    c.check(*run(c), c.reference())
+    assert c.pool.device_errors() == 0
+    c.pool.destroy()
+
+
 def test_contexts_that_end_inside_the_shared_blocks():
     """Rows that see part of the prefix, or nothing: empty places of a padded batch."""
     ctx = np.array([80, 16 * 20, 0, 1, 16 * 20 + 9, 17, 129, 128])
