@@ -419,7 +419,8 @@ kv_status paged_attention_masked_workspace_size(const kv_pool* pool, int batch, 
  *   group's first sequence are the ones read).  kv_bm_prefix_groups makes both
  *   arrays.  group_offsets: int32 [n_groups + 1], not decreasing, in [0, batch];
  *   group_blocks: int32 [n_groups], in [0, max_blocks].  Sequences outside every
- *   group, groups of one, and groups with 0 shared blocks share nothing; a
+ *   group, groups of one, and groups with 0 shared blocks share nothing, and
+ *   groups that would save little are computed as if they did not; a
  *   context may end inside its group's shared blocks (0 included; values behind it
  *   that others see have to be finite).  Offsets that
  *   break the rule (KV_DEVERR_GROUP): nothing is shared; a block count that

@@ -274,6 +274,13 @@ struct SpanPlan {
 // samples of one prompt 17.2, 17.1, 21.6; larger calls do not depend on it).
 constexpr int kSpanLeast = 2 + kvp::SPAN_PAD;
 
+// Tokens a group has to save at least, (members - 1) x shared, to be computed once: less costs more in
+// runs of the shared pass, pieces and their merge than it saves.  With 0 / 1,024 / 2,048 / 2,560: 41
+// pairs of sequences behind 1,364 tokens 60 / 62 / 53 / 53 us, 46 pairs behind 22 tokens (8-bit) 42 /
+// 17 / 17 / 17, 12 pairs behind 3,102 (8-bit) 29 / 29 / 32 / 34, 32 groups of 8 behind 512 161 / 161 /
+// 163 / 165, four samples behind 512 tokens 16.1 / 16.1 / 15.2 / 15.3.
+constexpr int kShareTokens = 2048;
+
 kv_status make_span_plan(const kv_pool* pl, int batch, int q_heads, int q_len, int max_blocks,
                          int span_blocks, int split_tokens, SpanPlan* out)
 {
@@ -1034,6 +1041,7 @@ kv_status paged_shared_prefix_attention(const kv_pool* pool, const void* q, int 
     s.max_blocks = max_blocks;
     s.num_blocks = pool->num_blocks;
     s.n_groups = n_groups;
+    s.share_least = (kShareTokens + pool->block_size - 1) / pool->block_size;
     s.pieces = static_cast<int>(l.pieces);
     s.scale_log2 = p.d.scale_log2;
     if (kvp::launch_prefix(pool->dtype == KV_DTYPE_FP8_E4M3, pool->head_dim, pool->block_size, pool->num_sms, pool->tmpk,

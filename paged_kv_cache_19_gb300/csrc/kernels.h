@@ -68,6 +68,7 @@ struct PrefixParams {
     uint32_t* err;
     int batch, kv_heads, q_len, rows, max_blocks, num_blocks, n_groups;
     int pieces;               // pieces the workspace holds
+    int share_least;          // blocks a group has to save at least to be computed once
     float scale_log2;
 };
 // Run slots and pieces the shared pass can use, for a grid of `ctas` (its workspace).

@@ -35,11 +35,12 @@ struct PrefixGroup {
     int blocks;                            // shared blocks; 0: computed without sharing
 };
 
-// Whether a group shares anything: its block count is in range, and a single sequence has nobody to
-// share with.
+// Whether a group shares anything: its block count is in range, a single sequence has nobody to
+// share with, and a run costs more than it saves where few sequences share little (share_least).
 __device__ __forceinline__ bool prefix_shares(const PrefixParams& p, int members, int blocks)
 {
-    return members >= 2 && blocks > 0 && blocks <= p.max_blocks;
+    return members >= 2 && blocks > 0 && blocks <= p.max_blocks &&
+           static_cast<long long>(members - 1) * blocks >= p.share_least;
 }
 
 __device__ __forceinline__ PrefixGroup load_prefix_group(const PrefixParams& p, int g)

@@ -146,6 +146,62 @@ def test_poison_behind_the_contexts_and_bad_blocks():
         c.pool.destroy()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_poison_and_bad_blocks_in_groups_that_save_much(fp8):
+    groups = [(21, 10), (30, 8)]
+    c = Cache(ctx=batch(groups, 16, 50), hq=8, hk=2, d=128, bs=16, shared=groups, fp8=fp8)
+    tab = c.tab.copy()
+    tab[:21, 4] = -1
+    tab[21:, 5] = 10 ** 6
+    c.tables = i32(tab)
+    got = run(c)
+    assert c.pool.device_errors() == kp.DEVERR_BLOCK_ID
+    c.check(*got, c.reference(lambda b, pos, t: (t > pos) | (t // 16 == (4 if b < 21 else 5))))
+    c.pool.destroy()
+
+
+def test_extreme_queries_in_a_group_that_saves_much():
+    groups = [(24, 12)]
+    c = Cache(ctx=batch(groups, 16, 30), hq=8, hk=2, d=128, bs=16, shared=groups, fp8=True)
+    f = torch.tensor([0.0, 2.0 ** -40, 2.0 ** 20, 1.0, 2.0 ** -14, 2.0 ** -130] * 4, device="cuda")[:, None, None, None]
+    c.scale *= 2.0 ** -20
+    c.q = (c.q.float() * f).to(torch.bfloat16)
+    c.q64 = c.q.double().cpu().numpy()
+    c.check(*run(c), c.reference())
+    c.pool.destroy()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.05, 0.3])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_scales_in_a_group_that_saves_much(scale, fp8):
+    groups = [(16, 12)]
+    c = Cache(ctx=batch(groups, 16, 30), hq=8, hk=2, d=128, bs=16, shared=groups, fp8=fp8)
+    c.scale = scale
+    c.check(*run(c), c.reference())
+    c.pool.destroy()
+
+
+def test_several_new_tokens_in_groups_that_save_much():
+    """Contexts that end inside the shared blocks, at their end and behind it, some of length 0."""
+    ctx = np.concatenate([np.full(20, 16 * 9) + np.arange(20) - 6, [5, 0, 16 * 9], np.full(18, 16 * 9 + 40)])
+    c = Cache(ctx=ctx, hq=4, hk=2, d=64, bs=16, q_len=5, shared=[(41, 9)])
+    c.check(*run(c), c.reference())
+    c.pool.destroy()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("members", [2, 3, 5, 6, 9])
+def test_groups_on_both_sides_of_the_sharing_rule(members, fp8):
+    """The same bits' meaning whether a group is computed once or not: groups that save 1,536 to
+    2,560 tokens next to each other."""
+    groups = [(members, b) for b in (1536 // 32 // (members - 1), 2048 // 32 // (members - 1), 2048 // 32 // (members - 1) + 1,
+                                     2560 // 32 // (members - 1))]
+    c = Cache(ctx=batch(groups, 32, 40), hq=4, hk=2, d=128, bs=32, fp8=fp8, shared=groups, seed=members)
+    c.check(*run(c), c.reference())
+    assert c.pool.device_errors() == 0
+    c.pool.destroy()
+
+
 def test_bad_groups_share_nothing_and_are_right():
     groups = [(7, 10), (3, 6)]
     c = Cache(ctx=batch(groups, 16, 50), hq=8, hk=2, d=128, bs=16, shared=groups)
