@@ -47,7 +47,7 @@
 // score MMAs read Q and K from shared memory, 64 KB for 2 x 128 x 128 scores, and run at its
 // rate) and 1,590 of softmax beside them; the beginning of a run costs about 3,600 (q), its end 5,500
 // (8-bit: more, the rows of q are scaled to f16 in place first).  32 groups of 8 sequences (32 rows, 512 tokens)
-// take about 22 us, bound by those.
+// take about 22 us, bound by those.  Whether a group is worth a run is decided by prefix_shares.
 //
 // Every wait is bounded; a late barrier sets KV_DEVERR_TIMEOUT, every role leaves its loops, and
 // the CTA waits for its copies and MMAs in flight and frees its tensor memory.
