@@ -6,6 +6,11 @@ marshal arguments (torch tensors -> device pointers, the current stream); those 
 that a step makes once per layer do it natively (binding/calls.cpp).
 Every step of the computation runs in the library's CUDA kernels; there is no
 CPU path, and importing a function without the built library raises.
+
+stream= (a torch stream or a raw handle) is where a call launches; without it, torch's current
+stream.  What a call allocates itself -- workspace and out, where they are not given -- belongs to
+that stream.  As with torch's own side streams, the inputs have to be ready on it and to live
+until it has used them, and whoever reads out on another stream waits for it.
 """
 from __future__ import annotations
 
@@ -171,6 +176,36 @@ def _pool_stream(stream, pool) -> int | None:
     return _stream(stream)
 
 
+def _made(make, stream, device, returned=False):
+    """make(), an allocation of a call, as work of the stream that the call launches on: its zeros
+    come before the kernel, and its memory is used again behind it.  A tensor that the caller gets
+    is kept for what the caller's current stream does with it, too."""
+    if stream is None:
+        return make()
+    if not hasattr(stream, "cuda_stream"):              # a raw handle; 0 and 1: the default stream
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream) > 1
+                  else torch.cuda.default_stream(device))
+    with torch.cuda.stream(stream):
+        t = make()
+    if returned:
+        here = torch.cuda.current_stream(device)
+        if here.cuda_stream != stream.cuda_stream:
+            t.record_stream(here)
+    return t
+
+
+def _workspace(need: int, q, stream, zeroed: bool = True):
+    """A workspace for one call."""
+    if need == 0:
+        return None
+    make = torch.zeros if zeroed else torch.empty
+    return _made(lambda: make(max(need, 16), dtype=torch.uint8, device=q.device), stream, q.device)
+
+
+def _like(q, stream):
+    return _made(lambda: torch.empty_like(q), stream, q.device, returned=True)
+
+
 _binding = None
 
 
@@ -313,8 +348,9 @@ def paged_norm_rope_append(pool: Pool, q, k, v, block_tables, context_lens=None,
     Returns the queries [T / q_len, Hq, q_len, d] ([T, Hq, d] for q_len 1 when out is not given)."""
     if out is None:
         n, heads, d = q.shape
-        out = torch.empty((n, heads, d) if q_len == 1 else (n // q_len, heads, q_len, d), dtype=torch.bfloat16,
-                          device=q.device)
+        shape = (n, heads, d) if q_len == 1 else (n // q_len, heads, q_len, d)
+        out = _made(lambda: torch.empty(shape, dtype=torch.bfloat16, device=q.device), stream, q.device,
+                    returned=True)
     status = (_binding or _native()).norm_rope_append(
         pool._h.value, pool.head_dim, pool.kv_heads, q, k, v, block_tables, context_lens, q_weight, k_weight, eps,
         rope_table, interleaved, q_len, token_seq, token_pos, out, _pool_stream(stream, pool))
@@ -373,13 +409,13 @@ def paged_decode_attention(pool: Pool, q, block_tables, context_lens, scale: flo
     d = q.shape[-1]
     max_blocks = block_tables.shape[1]
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream)
     _need(out, torch.bfloat16, "out")
     _need(lse, torch.float32, "lse")
     if workspace is None:
         need = paged_decode_workspace_size(pool, batch, q_heads, max_blocks, kv_split_tokens)
         # zero-filled: it holds the per-sequence chunk counters of the in-kernel merge
-        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device) if need else None
+        workspace = _workspace(need, q, stream)
     _need(workspace, torch.uint8, "workspace")
     ws_bytes = 0 if workspace is None else workspace.numel()
     _check(lib.paged_decode_attention(pool.handle, _ptr(q), int(q_heads), _ptr(block_tables),
@@ -403,12 +439,12 @@ def paged_decode_attention_split_merge(pool: Pool, q, block_tables, context_lens
     d = q.shape[-1]
     max_blocks = block_tables.shape[1]
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream)
     _need(out, torch.bfloat16, "out")
     _need(lse, torch.float32, "lse")
     if workspace is None:
         need = paged_decode_workspace_size(pool, batch, q_heads, max_blocks, kv_split_tokens)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device) if need else None
+        workspace = _workspace(need, q, stream, zeroed=False)
     _need(workspace, torch.uint8, "workspace")
     ws_bytes = 0 if workspace is None else workspace.numel()
     _check(lib.paged_decode_attention_split_merge(
@@ -431,7 +467,8 @@ def paged_merge_attention_states(outs, lses, out=None, lse=None, stream=None):
         raise ValueError("lses must have the shape of outs without its last dimension")
     rows = lses[0].numel() if n_src else 0
     if out is None:
-        out = torch.empty(outs.shape[1:], dtype=torch.bfloat16, device=outs.device)
+        out = _made(lambda: torch.empty(outs.shape[1:], dtype=torch.bfloat16, device=outs.device), stream,
+                    outs.device, returned=True)
     _need(out, torch.bfloat16, "out")
     _need(lse, torch.float32, "lse")
     if out.numel() != rows * d or (lse is not None and lse.numel() != rows):
@@ -466,13 +503,13 @@ def paged_attention_multi_query(pool: Pool, q, block_tables, context_lens, scale
     batch, q_heads, q_len, d = q.shape
     max_blocks = block_tables.shape[1]
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream)
     _need(out, torch.bfloat16, "out")
     _need(lse, torch.float32, "lse")
     if workspace is None:
         need = paged_multi_query_workspace_size(pool, batch, q_heads, q_len, max_blocks,
                                                 kv_split_tokens)
-        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device) if need else None
+        workspace = _workspace(need, q, stream)
     _need(workspace, torch.uint8, "workspace")
     ws_bytes = 0 if workspace is None else workspace.numel()
     _check(lib.paged_attention_multi_query(pool.handle, _ptr(q), int(q_heads), int(q_len),
@@ -496,11 +533,6 @@ def paged_attention_masked_workspace_size(pool: Pool, batch: int, q_heads: int, 
     return n.value
 
 
-def _zeroed(need: int, q):
-    """A workspace for one call (the caching allocator orders its reuse on the stream)."""
-    return torch.zeros(need, dtype=torch.uint8, device=q.device) if need else None
-
-
 def paged_attention_masked(pool: Pool, q, block_tables, context_lens, scale: float,
                            softcap: float = 0.0, window: int = 0, alibi_slopes=None,
                            first_keys=None, prefix_lens=None, kv_split_tokens: int = 0,
@@ -510,11 +542,11 @@ def paged_attention_masked(pool: Pool, q, block_tables, context_lens, scale: flo
     key per sequence (first_keys int32 [B]) and a prefix every query sees (prefix_lens int32
     [B]); q bf16 [B, Hq, d] or [B, Hq, q_len, d].  Returns out (shaped like q)."""
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream)
     if workspace is None:
-        workspace = _zeroed(paged_attention_masked_workspace_size(
+        workspace = _workspace(paged_attention_masked_workspace_size(
             pool, q.shape[0], q.shape[1], q.shape[2] if q.dim() == 4 else 1, block_tables.shape[1], window,
-            kv_split_tokens), q)
+            kv_split_tokens), q, stream)
     status = (_binding or _native()).attention_masked(
         pool._h.value, pool.head_dim, q, block_tables, context_lens, scale, softcap, window, alibi_slopes, first_keys,
         prefix_lens, kv_split_tokens, workspace, out, lse, _pool_stream(stream, pool))
@@ -542,11 +574,11 @@ def paged_shared_prefix_attention(pool: Pool, q, block_tables, context_lens, gro
     first group_blocks[g] entries of their tables (int32 [G]); BlockManager.prefix_groups makes
     both.  q bf16 [B, Hq, d] or [B, Hq, q_len, d].  Returns out (shaped like q)."""
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream)
     if workspace is None:
-        workspace = _zeroed(paged_shared_prefix_workspace_size(
+        workspace = _workspace(paged_shared_prefix_workspace_size(
             pool, q.shape[0], q.shape[1], q.shape[2] if q.dim() == 4 else 1, block_tables.shape[1],
-            group_blocks.numel(), kv_split_tokens), q)
+            group_blocks.numel(), kv_split_tokens), q, stream)
     status = (_binding or _native()).shared_prefix_attention(
         pool._h.value, pool.head_dim, q, block_tables, context_lens, group_offsets, group_blocks, scale,
         kv_split_tokens, workspace, out, lse, _pool_stream(stream, pool))
@@ -579,13 +611,13 @@ def paged_decode_step(pool: Pool, k_new, v_new, q, block_tables, context_lens,
         raise ValueError("k_new and v_new must hold batch * q_len tokens")
     max_blocks = block_tables.shape[1]
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream)
     _need(out, torch.bfloat16, "out")
     _need(lse, torch.float32, "lse")
     if workspace is None:
         need = paged_multi_query_workspace_size(pool, batch, q_heads, q_len, max_blocks,
                                                 kv_split_tokens)
-        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device) if need else None
+        workspace = _workspace(need, q, stream)
     _need(workspace, torch.uint8, "workspace")
     ws_bytes = 0 if workspace is None else workspace.numel()
     _check(lib.paged_decode_step(pool.handle, _ptr(k_new), _ptr(v_new), _ptr(q), int(q_heads),
@@ -767,12 +799,13 @@ def paged_mla_decode_attention(pool: Pool, q, block_tables, context_lens, scale:
     batch, q_heads = q.shape[0], q.shape[1]
     max_blocks = block_tables.shape[1]
     if out is None:
-        out = torch.empty(batch, q_heads, latent_dim, dtype=torch.bfloat16, device=q.device)
+        out = _made(lambda: torch.empty(batch, q_heads, latent_dim, dtype=torch.bfloat16, device=q.device),
+                    stream, q.device, returned=True)
     _need(out, torch.bfloat16, "out")
     _need(lse, torch.float32, "lse")
     if workspace is None:
         need = paged_mla_workspace_size(pool, batch, q_heads, max_blocks, kv_split_tokens)
-        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device) if need else None
+        workspace = _workspace(need, q, stream)
     _need(workspace, torch.uint8, "workspace")
     ws_bytes = 0 if workspace is None else workspace.numel()
     _check(lib.paged_mla_decode_attention(pool.handle, _ptr(q), int(q_heads), _ptr(block_tables),
@@ -798,12 +831,13 @@ def paged_mla_decode_step(pool: Pool, kv_new, q, block_tables, context_lens, sca
     batch, q_heads = q.shape[0], q.shape[1]
     max_blocks = block_tables.shape[1]
     if out is None:
-        out = torch.empty(batch, q_heads, latent_dim, dtype=torch.bfloat16, device=q.device)
+        out = _made(lambda: torch.empty(batch, q_heads, latent_dim, dtype=torch.bfloat16, device=q.device),
+                    stream, q.device, returned=True)
     _need(out, torch.bfloat16, "out")
     _need(lse, torch.float32, "lse")
     if workspace is None:
         need = paged_mla_workspace_size(pool, batch, q_heads, max_blocks, kv_split_tokens)
-        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device) if need else None
+        workspace = _workspace(need, q, stream)
     _need(workspace, torch.uint8, "workspace")
     ws_bytes = 0 if workspace is None else workspace.numel()
     _check(lib.paged_mla_decode_step(pool.handle, _ptr(kv_new), _ptr(q), int(q_heads),
