@@ -187,7 +187,7 @@ typedef enum kv_rope_style {
  *     with q_len new tokens per sequence: without token_seq / token_pos token i
  *     is token i % q_len of sequence i / q_len, at position context_lens[seq] -
  *     q_len + i % q_len (then num_tokens <= batch * q_len).  With either array
- *     q_len must be 1.
+ *     q_len must be 1.  num_tokens: a multiple of q_len.
  *   q_out: bf16 [num_tokens / q_len, q_heads, q_len, head_dim], the layout
  *     paged_attention_multi_query takes; must not overlap any input.
  *   fp32 arithmetic, each number rounded once: q and bf16 pools to nearest even,

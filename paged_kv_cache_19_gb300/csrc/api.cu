@@ -652,6 +652,7 @@ kv_status paged_norm_rope_append(kv_pool* pool, const void* q, int64_t q_stride,
     if ((token_seq != nullptr || token_pos != nullptr) && q_len != 1) return KV_ERR_INVALID_ARG;
     if (token_pos == nullptr && context_lens == nullptr) return KV_ERR_INVALID_ARG;
     if (token_seq == nullptr && num_tokens > static_cast<long long>(batch) * q_len) return KV_ERR_INVALID_ARG;
+    if (num_tokens % q_len != 0) return KV_ERR_INVALID_ARG;      // q_out holds whole sequences' tokens
     if ((q_weight == nullptr) != (k_weight == nullptr)) return KV_ERR_INVALID_ARG;
     if (q_weight != nullptr && !(std::isfinite(eps) && eps >= 0.f)) return KV_ERR_INVALID_ARG;
     if (rope != nullptr && (rope_positions <= 0 || rope_dim <= 0 || rope_dim % 16 != 0 || rope_dim > pool->head_dim))

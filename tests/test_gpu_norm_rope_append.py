@@ -355,3 +355,21 @@ def test_refusals():
                                       c.ctx.data_ptr(), 2, 1, out.data_ptr(), None) == kp.KV_ERR_INVALID_ARG
     latent.destroy()
     c.pool.destroy()
+
+
+@pytest.mark.parametrize("q_len,tokens", [(2, 3), (5, 4), (5, 9), (2, 1)])
+def test_a_part_of_a_sequences_tokens_is_refused(q_len, tokens):
+    """q_out has room for tokens / q_len sequences: a token behind them would be written past its end
+    (row (tokens // q_len) * q_heads * q_len and on)."""
+    c = Call(hq=4, hk=2, d=64, bs=16, rope_dim=64, q_len=q_len, ctx=[9, 20, 33])
+    out = torch.zeros((3, 4, q_len, 64), dtype=torch.bfloat16, device="cuda")
+    args = (c.q.data_ptr(), 512, c.k.data_ptr(), 512, c.v.data_ptr(), 512, 4)
+    rest = (c.dqw.data_ptr(), c.dkw.data_ptr(), 1e-6, c.dtable.data_ptr(), len(c.table), 64, 0, None, None,
+            c.dtab.data_ptr(), c.mb, c.ctx.data_ptr(), 3, q_len, out.data_ptr(), None)
+    lib = kp.load_library()
+    assert lib.paged_norm_rope_append(c.pool.handle, *args, tokens, *rest) == kp.KV_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert not out.any() and all((t == POISON).all() for t in c.pool.raw_bytes())
+    assert lib.paged_norm_rope_append(c.pool.handle, *args, 3 * q_len, *rest) == kp.KV_OK
+    assert c.pool.device_errors() == 0
+    c.check(out)
