@@ -373,3 +373,42 @@ def test_a_part_of_a_sequences_tokens_is_refused(q_len, tokens):
     assert lib.paged_norm_rope_append(c.pool.handle, *args, 3 * q_len, *rest) == kp.KV_OK
     assert c.pool.device_errors() == 0
     c.check(out)
+
+
+@pytest.mark.parametrize("n", [12, 1800])
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -140, 1e-30, 1e-6, 3e38])
+def test_rows_whose_squares_leave_the_range_of_fp32(eps, n, monkeypatch):
+    """The norm over the whole range of bf16 and of eps: rows of the smallest numbers, of the largest
+    ones, and in between (both forms of the kernel).
+
+    bf16_bound counts half a step as 2^-8 of the number, which holds from 2^-126 on.  Below, the
+    steps of bf16 stay 2^-133 apart, so half a step is 2^-134 whatever the number (the fp32 numbers
+    before it are off by 2^-149 there, inside the 2^-15 of the row's top or far below 2^-134)."""
+    usual = bf16_bound
+    monkeypatch.setitem(globals(), "bf16_bound", lambda ref, top: usual(ref, top) + 2.0 ** -134 * (np.abs(ref) < 2.0 ** -126))
+    c = Call(hq=4, hk=2, d=128, bs=16, rope_dim=64, batch=1, seq=np.zeros(n, int), pos=np.arange(n), eps=eps)
+    # standard normal numbers, at most 6 of them: 2^124 times that is finite in bf16
+    by = np.array([2.0 ** e for e in (-131, -120, -90, -75, -64, -50, 0, 40, 61, 66, 90, 124)])
+    x = torch.from_numpy(np.clip(c.x, -6, 6) * np.resize(by, n)[:, None, None]).to(torch.bfloat16)
+    assert torch.isfinite(x).all()
+    x[..., 0] = torch.where((x == 0).all(-1), torch.finfo(torch.bfloat16).smallest_normal, x[..., 0])
+    c.x = x.double().numpy()
+    # (the values are copied as they are; keys and queries are normed)
+    x = x.cuda()
+    c.q, c.k, c.v = x[:, :4], x[:, 4:6], x[:, 6:]
+    out = c.run()
+    assert c.pool.device_errors() == 0
+    c.check(out)
+
+
+def test_a_row_of_zeros_without_eps_is_not_a_number_and_stays_alone():
+    """0 / 0, as the formula has it, in its own row only."""
+    c = Call(hq=4, hk=2, d=128, bs=16, norm=True, rope_dim=0, ctx=[3, 9], eps=0.0)
+    c.x[0, 1] = 0.0
+    x = torch.from_numpy(c.x).to(torch.bfloat16).cuda()
+    c.q, c.k, c.v = x[:, :4], x[:, 4:6], x[:, 6:]
+    out = c.run()
+    assert torch.isnan(out[0, 1]).all()
+    c.x[0, 1] = 1.0
+    out[0, 1] = torch.from_numpy(c.qw).cuda()
+    c.check(out)
