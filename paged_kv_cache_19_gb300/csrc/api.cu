@@ -1030,7 +1030,6 @@ kv_status paged_shared_prefix_attention(const kv_pool* pool, const void* q, int 
     s.group_offsets = group_offsets;
     s.group_blocks = group_blocks;
     s.k_scale = pool->k_scale;
-    s.v_scale = pool->v_scale;
     s.runs = reinterpret_cast<int2*>(ws + l.runs);
     s.piece_lse = reinterpret_cast<float4*>(ws + l.piece_lse);
     s.piece_o = reinterpret_cast<float*>(ws + l.piece_o);

@@ -800,7 +800,7 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 }
             }
             if (!idle && !(it.both && s == 1)) {
-                const float inv = l_out > 0.f ? (FP8 ? __ldg(p.v_scale + it.kvh) : 1.f) / l_out : 0.f;
+                const float inv = l_out > 0.f ? 1.f / l_out : 0.f;
                 keep *= inv;
                 add *= inv;
                 const size_t at = (static_cast<size_t>(blockIdx.x) + it.run) * PFX_PAIR + s * PFX_TILE + row;

@@ -378,10 +378,9 @@ __device__ __forceinline__ void fold_state(WarpState<C>& st, int nt, float2 a, f
 }
 
 // Rows [a, b) of a piece -- normalised outputs o [row][D] and log-sum-exps (log2 units, 4 floats
-// apart; -inf: the row saw nothing) in shared memory -- folded into the state as one more block;
-// out_scale: the factor that takes its outputs to the state's units.
+// apart; -inf: the row saw nothing) in shared memory -- folded into the state as one more block.
 template <bool FP8, int D, int NT>
-__device__ __forceinline__ void fold_piece(const float* o, const float* lse, int a, int b, float out_scale,
+__device__ __forceinline__ void fold_piece(const float* o, const float* lse, int a, int b,
                                            WarpState<DecodeCfg<FP8, D, SPAN_TOK, NT>>& st, int lane)
 {
     using C = DecodeCfg<FP8, D, SPAN_TOK, NT>;
@@ -398,14 +397,13 @@ __device__ __forceinline__ void fold_piece(const float* o, const float* lse, int
             const float f = fast_exp2(st.m[nt][j] - m), w = fast_exp2(s - m);
             st.m[nt][j] = m;
             st.l[nt][j] = st.l[nt][j] * f + (r == 0 ? w : 0.f);     // the lanes' sums are added up at the end
-            const float g = w * out_scale;
             const float* x = o + (row - a) * D + (FP8 ? 16 * r : r);
 #pragma unroll
             for (int ms = 0; ms < C::KS; ++ms)
 #pragma unroll
                 for (int hi = 0; hi < 2; ++hi) {
                     float& y = st.o[ms][nt][2 * hi + j];
-                    y = y * f + g * x[FP8 ? 2 * ms + hi : 16 * ms + 8 * hi];
+                    y = y * f + w * x[FP8 ? 2 * ms + hi : 16 * ms + 8 * hi];
                 }
         }
 }
@@ -831,8 +829,7 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 if (SUFFIX && (tag & 3) == TAG_PIECE && mine && (tag >> (24 + h) & 1))
                     fold_piece<FP8, D, NT>(reinterpret_cast<const float*>(st_sm + h * C::STAGE),
                                            reinterpret_cast<const float*>(lse_sm + s * S::LSE + h * (S::RPS * 16)),
-                                           tag >> 8 & 0xff, tag >> 16 & 0xff,
-                                           FP8 ? 1.f / __ldg(p.v_scale + kvh) : 1.f, st, lane);
+                                           tag >> 8 & 0xff, tag >> 16 & 0xff, st, lane);
                 ++sub;
             }
             __syncwarp();
@@ -960,16 +957,9 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             }
             if (!last) continue;
         }
-        if constexpr (FP8) {
-            const float vs = __ldg(p.v_scale + kvh);
-#pragma unroll
-            for (int ms = 0; ms < C::KS; ++ms)
-#pragma unroll
-                for (int nt = 0; nt < C::NTT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) st.o[ms][nt][e] *= vs;
-        }
-        // ---- normalise and store
+        // ---- normalise and store.  An 8-bit cache's values get their scale last: the sums of codes
+        // times a large scale, or a small scale divided by the sum, could leave the range of fp32.
+        const float vs = FP8 ? __ldg(p.v_scale + kvh) : 1.f;
 #pragma unroll
         for (int nt = 0; nt < C::NTT; ++nt) {
             const float inv[2] = {st.l[nt][0] > 0.f ? 1.f / st.l[nt][0] : 0.f,
@@ -982,7 +972,7 @@ paged_decode_span(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     uint32_t w[8];
 #pragma unroll
                     for (int ms = 0; ms < C::KS; ++ms)
-                        w[ms] = pack_bf16x2(st.o[ms][nt][j] * inv[j], st.o[ms][nt][2 + j] * inv[j]);
+                        w[ms] = pack_bf16x2(st.o[ms][nt][j] * inv[j] * vs, st.o[ms][nt][2 + j] * inv[j] * vs);
                     if (mine + j < nh) {
                         uint4* dst = reinterpret_cast<uint4*>(p.out + (row0 + mine + j) * D + 16 * r);
                         dst[0] = make_uint4(w[0], w[1], w[2], w[3]);

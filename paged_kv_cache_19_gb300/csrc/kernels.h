@@ -61,10 +61,9 @@ struct PrefixParams {
     const int32_t* group_offsets;   // [n_groups + 1]
     const int32_t* group_blocks;    // [n_groups]
     const float* k_scale;     // [kv_heads] (fp8 cache)
-    const float* v_scale;
     int2* runs;               // per run slot: first piece, pieces
     float4* piece_lse;        // [piece][2][128]: log-sum-exp in log2 units (first of four), -inf: no key
-    float* piece_o;           // [piece][2][128][head_dim], normalised
+    float* piece_o;           // [piece][2][128][head_dim], normalised; fp8: in units of the values' scale
     uint32_t* err;
     int batch, kv_heads, q_len, rows, max_blocks, num_blocks, n_groups;
     int pieces;               // pieces the workspace holds

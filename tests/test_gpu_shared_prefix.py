@@ -386,3 +386,32 @@ def test_a_decode_step_of_a_forked_batch(fp8):
     assert pool.device_errors() == 0
     pool.destroy()
     bm.close()
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -129, 1.5 * 2.0 ** -132, 2.0 ** -100, 1.0, 2.0 ** 100, 1.25 * 2.0 ** 116])
+def test_the_ends_of_the_values_scale(scale):
+    """Every scale that kv_pool_set_scales takes, where the outputs are numbers of bf16: values of one
+    sign, codes 64 .. 448, so that an output is at least 64 scales and sum p|v| is the output itself.
+
+    Beside check's bound (twice 2^-8 of the output, probabilities and output rounded, and the scores'
+    2^-12), an output below 2^-126 is rounded by up to 2^-134, half a step of bf16's last numbers."""
+    groups = [(40, 12), (30, 20), (3, 0)]
+    c = Cache(ctx=batch(groups, 16, 300), hq=8, hk=2, d=128, bs=16, shared=groups, fp8=True, seed=13)
+    scale = float(np.float32(scale))
+    v = c.pool.tensors()[1]
+    codes = torch.from_numpy(np.random.default_rng(2).uniform(64, 448, v.shape).astype(np.float32)).to(v.dtype)
+    seen = ~torch.isnan(v.float())
+    v.copy_(torch.where(seen, codes.cuda().float(), float("nan")).to(v.dtype))
+    c.v = v.float().cpu().double().numpy()
+    c.pool.set_scales(c.ks, [scale] * 2)
+    want, _, want_lse, top = c.reference()          # in units of the scale
+    masked = torch.full_like(c.q, float("nan"))
+    kp.paged_attention_masked(c.pool, c.q, c.tables, c.lens, c.scale, out=masked)
+    shared, lse = run(c)
+    assert c.pool.device_errors() == 0 and (np.abs(lse.double().cpu().numpy() - want_lse) <= 2.0 ** -12 + 2.0 ** -19 * top).all()
+    want = want * scale                             # (64 bits: far from the ends of their range)
+    assert np.isfinite(want).all() and (np.abs(want) >= 2.0 ** -127).all() and want.max() < 2.0 ** 127
+    bound = (2.0 ** -7 + 2.0 ** -12 + 2.0 ** -19 * top[..., None]) * want + 2.0 ** -134
+    for got in (masked, shared):
+        assert (np.abs(got.double().cpu().numpy() - want) <= bound).all()
+    c.pool.destroy()
