@@ -151,7 +151,9 @@ PyObject* norm_rope_append(PyObject*, PyObject* const* args, Py_ssize_t nargs)
     const at::Tensor* rope = a.tensor(11, "rope_table", true);
     if (a.ok && q->dim() != 3) a.fail(PyExc_ValueError, "q", "[tokens, q_heads, head_dim]");
     if (a.ok && tab->dim() != 2) a.fail(PyExc_ValueError, "block_tables", "[batch, max_blocks]");
-    if (a.ok && rope != nullptr && rope->dim() != 2) a.fail(PyExc_ValueError, "rope_table", "[positions, rope_dim]");
+    // (an empty table has no address, and none means no rotation)
+    if (a.ok && rope != nullptr && (rope->dim() != 2 || rope->numel() == 0))
+        a.fail(PyExc_ValueError, "rope_table", "[positions, rope_dim], of one position at least");
     if (!a.ok) return nullptr;
     const int64_t n = q->size(0), heads = q->size(1), batch = tab->size(0), max_blocks = tab->size(1);
     const int64_t positions = rope != nullptr ? rope->size(0) : 0, rope_dim = rope != nullptr ? rope->size(1) : 0;

@@ -412,3 +412,13 @@ def test_a_row_of_zeros_without_eps_is_not_a_number_and_stays_alone():
     c.x[0, 1] = 1.0
     out[0, 1] = torch.from_numpy(c.qw).cuda()
     c.check(out)
+
+
+def test_a_rotation_table_without_rows_writes_nothing():
+    c = Call(hq=4, hk=2, d=64, bs=16, rope_dim=64, ctx=[3, 9])
+    out = torch.zeros_like(c.q)
+    for table in (c.dtable[:0], c.dtable[:, :0].contiguous()):
+        with pytest.raises(ValueError, match="rope_table"):
+            c.run(out=out, rope_table=table)
+    assert not out.any() and all((t == POISON).all() for t in c.pool.raw_bytes())
+    c.pool.destroy()

@@ -135,3 +135,14 @@ def test_groups_refusals(lib):
     assert lib.kv_bm_prefix_groups(None, None, 0, 1, None, None, None, ctypes.byref(n)) == kp.KV_ERR_INVALID_ARG
     assert lib.kv_bm_prefix_groups(bm._h, None, 1, 1, None, None, None, ctypes.byref(n)) == kp.KV_ERR_INVALID_ARG
     bm.close()
+
+
+@pytest.mark.parametrize("shape", [(0, 64), (5, 0), (0, 0), (64,)])
+def test_a_rotation_table_without_rows_is_refused(lib, shape):
+    """Its address is null, which the C call takes for "no rotation"."""
+    import torch
+    q, kv = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    t, l = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)  # noqa: E741
+    with pytest.raises(ValueError, match="rope_table"):
+        kp._native().norm_rope_append(1, 64, 2, q, kv, kv, t, l, None, None, 1e-6, torch.zeros(shape), False, 1, None, None,
+                                      torch.empty_like(q), 0)
