@@ -379,8 +379,9 @@ typedef struct kv_attention_mask {
  *   be finite for the other's sake.  Blocks that no query of a
  *   tile of rows sees are not read, and their table entries not looked at: blocks
  *   that fell out of a window may have been freed and reused.
- *   mask: HOST struct, copied by the call; NULL = no change.  softcap >= 0 with a
- *   finite 2 / softcap, window >= 0; slopes finite (not checked).
+ *   mask: HOST struct, copied by the call; NULL = no change.  softcap >= 0 with
+ *   2 / softcap and softcap * log2(e) finite in fp32 (scale * log2(e) too), window
+ *   >= 0; slopes below 2^127 in magnitude (not checked).
  *   kv_split_tokens: the work of a batch is cut into equal ranges, one per CTA
  *     that the GPU holds at a time; this is the least a range covers, in tokens of
  *     a group of kv heads and a tile of query rows (0 = automatic; else a positive multiple

@@ -865,6 +865,8 @@ kv_status launch_decode(const kv_pool* pool, const Plan& plan, dim3 grid, const 
     return e == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 // Validates a call of the span kernel and fills its decode parameters (nothing launched).
 // extra: workspace bytes the call needs behind the kernel's own.
 kv_status make_span_launch(const kv_pool* pool, const SpanPlan& plan, const void* q, int q_heads, int q_len,
@@ -872,7 +874,7 @@ kv_status make_span_launch(const kv_pool* pool, const SpanPlan& plan, const void
                            float scale, void* workspace, size_t workspace_bytes, size_t extra, void* out,
                            float* lse_out, kvp::SpanParams* sp)
 {
-    if (!std::isfinite(scale)) return KV_ERR_INVALID_ARG;
+    if (!std::isfinite(scale * kLog2e)) return KV_ERR_INVALID_ARG;      // scores are kept in log2 units
     if (batch == 0) return KV_OK;
     if (q == nullptr || block_tables == nullptr || context_lens == nullptr || out == nullptr || workspace == nullptr)
         return KV_ERR_INVALID_ARG;
@@ -906,7 +908,7 @@ kv_status make_span_launch(const kv_pool* pool, const SpanPlan& plan, const void
     p.rows = plan.rows;
     p.max_blocks = max_blocks;
     p.num_blocks = pool->num_blocks;
-    p.scale_log2 = scale * 1.4426950408889634f;
+    p.scale_log2 = scale * kLog2e;
     p.stop_stage = g_stop_stage.load(std::memory_order_relaxed);
     p.consumer_wait_ns = g_consumer_wait_ns.load(std::memory_order_relaxed);
     sp->block_size = pool->block_size;
@@ -966,7 +968,7 @@ kv_status paged_attention_masked(const kv_pool* pool, const void* q, int q_heads
 {
     kv_attention_mask m = {};
     if (mask != nullptr) m = *mask;
-    if (!(m.softcap >= 0.f) || !std::isfinite(m.softcap) || (m.softcap > 0.f && !std::isfinite(2.f / m.softcap)))
+    if (!(m.softcap >= 0.f) || !std::isfinite(m.softcap * kLog2e) || (m.softcap > 0.f && !std::isfinite(2.f / m.softcap)))
         return KV_ERR_INVALID_ARG;
     if (!aligned(m.alibi_slopes, 4) || !aligned(m.first_keys, 4) || !aligned(m.prefix_lens, 4))
         return KV_ERR_INVALID_ARG;
@@ -978,7 +980,7 @@ kv_status paged_attention_masked(const kv_pool* pool, const void* q, int q_heads
                           workspace, workspace_bytes, 0, out, lse_out, &p);
     if (st != KV_OK || batch == 0) return st;
     p.window = effective_window(pool, m.window, max_blocks);
-    p.cap_log2 = m.softcap * 1.4426950408889634f;
+    p.cap_log2 = m.softcap * kLog2e;
     p.cap_in = m.softcap > 0.f ? 2.f / m.softcap : 0.f;
     p.slopes = m.alibi_slopes;
     p.first_keys = m.first_keys;

@@ -327,3 +327,22 @@ def test_a_stage_that_never_lands_times_out():
     assert c.pool.device_errors() & kp.DEVERR_TIMEOUT
     c.check(*run(c, 256, window=500), c.reference(hide(500)))
     c.pool.destroy()
+
+
+def test_the_largest_caps_and_scales():
+    """Scores are kept in log2 units: a cap or a scale whose product with log2(e) is no fp32 number is
+    refused (it made every score NaN); the largest cap that has one changes nothing."""
+    c = Cache(ctx=[61, 300], hq=4, hk=2, d=64, bs=16)
+    want = c.reference()
+    top = float(np.finfo(np.float32).max) / 1.4427
+    for cap in (top, 2.0 ** 127, 2.0 ** 100, 2.0 ** 60):
+        c.check(*run(c, softcap=cap), want)
+    with pytest.raises(kp.KVError):
+        run(c, softcap=3e38)
+    c.scale = 3e38
+    with pytest.raises(kp.KVError):
+        run(c)
+    with pytest.raises(kp.KVError):
+        kp.paged_shared_prefix_attention(c.pool, c.q, c.tables, c.lens, i32([0, 2]), i32([1]), c.scale)
+    assert c.pool.device_errors() == 0
+    c.pool.destroy()
