@@ -49,6 +49,12 @@ struct Args {
         if (v == -1.0 && PyErr_Occurred()) ok = false;
         return static_cast<float>(v);
     }
+    bool truth(int i)
+    {
+        const int v = ok ? PyObject_IsTrue(a[i]) : 0;
+        if (v < 0) ok = false;
+        return v > 0;
+    }
     kv_pool* pool(int i)
     {
         if (ok && a[i] == Py_None) {
@@ -146,6 +152,7 @@ PyObject* norm_rope_append(PyObject*, PyObject* const* args, Py_ssize_t nargs)
     Args a{args};
     kv_pool* pool = a.pool(0);
     const int64_t d = a.integer(1), kv = a.integer(2);
+    const bool interleaved = a.truth(12);
     const at::Tensor* q = a.tensor(3, "q");
     const at::Tensor* tab = a.tensor(6, "block_tables");
     const at::Tensor* rope = a.tensor(11, "rope_table", true);
@@ -173,7 +180,6 @@ PyObject* norm_rope_append(PyObject*, PyObject* const* args, Py_ssize_t nargs)
     const float* kw = a.data<const float>(9, at::kFloat, d, "k_weight", true);
     const float eps = a.real(10);
     const float* table = a.data<const float>(11, at::kFloat, positions * rope_dim, "rope_table", true);
-    const int interleaved = a.ok ? PyObject_IsTrue(a.a[12]) : 0;
     const int32_t* seq = a.data<const int32_t>(14, at::kInt, n, "token_seq", true);
     const int32_t* pos = a.data<const int32_t>(15, at::kInt, n, "token_pos", true);
     void* out = a.data(16, at::kBFloat16, n * heads * d, "out");

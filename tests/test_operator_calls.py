@@ -146,3 +146,13 @@ def test_a_rotation_table_without_rows_is_refused(lib, shape):
     with pytest.raises(ValueError, match="rope_table"):
         kp._native().norm_rope_append(1, 64, 2, q, kv, kv, t, l, None, None, 1e-6, torch.zeros(shape), False, 1, None, None,
                                       torch.empty_like(q), 0)
+
+
+def test_an_argument_without_a_truth_value_is_refused(lib):
+    """The error of its conversion is the call's error (the call went on with the error set)."""
+    import torch
+    q, kv = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    t, l = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)  # noqa: E741
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        kp._native().norm_rope_append(1, 64, 2, q, kv, kv, t, l, None, None, 1e-6, None, torch.zeros(2), 1, None, None,
+                                      torch.empty_like(q), 0)
