@@ -73,6 +73,14 @@ struct Args {
         }
         return &THPVariable_Unpack(a[i]);
     }
+    // Address of a tensor's first number.  A fake tensor has a CUDA device and no memory: its null
+    // address would pass for an optional argument that is not there.
+    void* address(const at::Tensor& t, const char* name)
+    {
+        void* p = t.numel() > 0 ? t.data_ptr() : nullptr;
+        if (p == nullptr && t.numel() > 0) fail(PyExc_ValueError, name, "a tensor with memory");
+        return p;
+    }
     // Address of a contiguous CUDA tensor of n numbers (n < 0: any).
     template <typename T = void>
     T* data(int i, at::ScalarType type, int64_t n, const char* name, bool optional = false)
@@ -88,7 +96,7 @@ struct Args {
             ok = false;
             return nullptr;
         }
-        return static_cast<T*>(t->data_ptr());
+        return static_cast<T*>(address(*t, name));
     }
     // A [tokens, heads, d] bf16 tensor whose token rows are contiguous: address and token stride.
     const void* rows(int i, int64_t n, int64_t heads, int64_t d, const char* name, int64_t* stride)
@@ -104,7 +112,7 @@ struct Args {
             return nullptr;
         }
         *stride = n > 1 ? t->stride(0) : heads * d;
-        return t->data_ptr();
+        return address(*t, name);
     }
 };
 
@@ -250,7 +258,7 @@ PyObject* shared_prefix_attention(PyObject*, PyObject* const* args, Py_ssize_t n
                                                    reinterpret_cast<void*>(stream)));
 }
 
-// The C entry: torch throws where a tensor has no strides or no memory (sparse, meta, fake).
+// The C entry: torch throws where a tensor has no strides or no memory (sparse, meta).
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject* self, PyObject* const* args, Py_ssize_t nargs)
 {

@@ -156,3 +156,25 @@ def test_an_argument_without_a_truth_value_is_refused(lib):
     with pytest.raises(RuntimeError, match="ambiguous"):
         kp._native().norm_rope_append(1, 64, 2, q, kv, kv, t, l, None, None, 1e-6, None, torch.zeros(2), 1, None, None,
                                       torch.empty_like(q), 0)
+
+
+def test_fake_tensors_are_refused(lib):
+    """They have a CUDA device and no memory: one in the place of an optional tensor (a rotation
+    table, a log-sum-exp) was taken for none, and all of them together for a call of null pointers."""
+    import torch
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    c = kp._native()
+
+    def fake(t):
+        with FakeTensorMode():
+            return torch.empty(t.shape, dtype=t.dtype, device="cuda:0")
+
+    q, kv = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    t, l = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)  # noqa: E741
+    out, w, table = torch.empty_like(q), torch.zeros(64), torch.zeros(9, 64)
+    ws, lse = torch.zeros(64, dtype=torch.uint8), torch.zeros(2, 4)
+    for call, args in ((c.norm_rope_append, (1, 64, 2, q, kv, kv, t, l, w, w, 1e-6, table, False, 1, None, None, out, 0)),
+                       (c.attention_masked, (1, 64, q, t, l, 1.0, 0.0, 0, w[:4], l, l, 0, ws, out, lse, 0)),
+                       (c.shared_prefix_attention, (1, 64, q, t, l, t[0], l[:2], 1.0, 0, ws, out, lse, 0))):
+        with pytest.raises(ValueError, match="memory"):
+            call(*[fake(x) if isinstance(x, torch.Tensor) else x for x in args])
