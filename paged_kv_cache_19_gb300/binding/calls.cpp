@@ -18,6 +18,7 @@ namespace {
 struct Args {
     PyObject* const* a;
     bool ok = true;
+    int device = -1;                                // of the CUDA tensors
 
     void fail(PyObject* type, const char* name, const char* what)
     {
@@ -80,6 +81,27 @@ struct Args {
         void* p = t.numel() > 0 ? t.data_ptr() : nullptr;
         if (p == nullptr && t.numel() > 0) fail(PyExc_ValueError, name, "a tensor with memory");
         return p;
+    }
+    // The CUDA tensors among the first n arguments lie on one device (an address of another one is
+    // not for the kernels to read; tensors elsewhere are refused by name, below).
+    void one_device(Py_ssize_t n)
+    {
+        for (Py_ssize_t i = 0; ok && i < n; ++i) {
+            if (!THPVariable_Check(a[i])) continue;
+            const at::Tensor& t = THPVariable_Unpack(a[i]);
+            if (!t.is_cuda()) continue;
+            const int dev = static_cast<int>(t.get_device());
+            if (device >= 0 && dev != device) fail(PyExc_ValueError, "the tensors", "on one device");
+            device = dev;
+        }
+    }
+    // And that is the pool's.
+    bool on_device_of(const kv_pool* p)
+    {
+        int dev = -1;
+        if (ok && kv_pool_shape(p, nullptr, nullptr, nullptr, nullptr, nullptr, &dev) == KV_OK && dev != device)
+            fail(PyExc_ValueError, "the tensors", "on the pool's device");
+        return ok;
     }
     // Address of a contiguous CUDA tensor of n numbers (n < 0: any).
     template <typename T = void>
@@ -161,6 +183,7 @@ PyObject* norm_rope_append(PyObject*, PyObject* const* args, Py_ssize_t nargs)
     kv_pool* pool = a.pool(0);
     const int64_t d = a.integer(1), kv = a.integer(2);
     const bool interleaved = a.truth(12);
+    a.one_device(nargs);
     const at::Tensor* q = a.tensor(3, "q");
     const at::Tensor* tab = a.tensor(6, "block_tables");
     const at::Tensor* rope = a.tensor(11, "rope_table", true);
@@ -192,7 +215,7 @@ PyObject* norm_rope_append(PyObject*, PyObject* const* args, Py_ssize_t nargs)
     const int32_t* pos = a.data<const int32_t>(15, at::kInt, n, "token_pos", true);
     void* out = a.data(16, at::kBFloat16, n * heads * d, "out");
     const int64_t stream = a.integer(17);
-    if (!a.ok) return nullptr;
+    if (!a.on_device_of(pool)) return nullptr;
     return status(a, paged_norm_rope_append(pool, qp, qs, kp, ks, vp, vs, static_cast<int>(heads), static_cast<int>(n), qw, kw,
                                             eps, table, static_cast<int>(positions), static_cast<int>(rope_dim),
                                             interleaved ? KV_ROPE_INTERLEAVED : KV_ROPE_HALF, seq, pos, tables,
@@ -208,6 +231,7 @@ PyObject* attention_masked(PyObject*, PyObject* const* args, Py_ssize_t nargs)
     Args a{args};
     kv_pool* pool = a.pool(0);
     const int64_t d = a.integer(1);
+    a.one_device(nargs);
     const Queries q(a, 2, 3, d);
     const int32_t* ctx = a.data<const int32_t>(4, at::kInt, q.batch, "context_lens");
     const float scale = a.real(5);
@@ -223,7 +247,7 @@ PyObject* attention_masked(PyObject*, PyObject* const* args, Py_ssize_t nargs)
     void* out = a.data(13, at::kBFloat16, q.rows * d, "out");
     float* lse = a.data<float>(14, at::kFloat, q.rows, "lse", true);
     const int64_t stream = a.integer(15);
-    if (!a.ok) return nullptr;
+    if (!a.on_device_of(pool)) return nullptr;
     return status(a, paged_attention_masked(pool, q.q, static_cast<int>(q.heads), static_cast<int>(q.q_len), q.tables,
                                             static_cast<int>(q.max_blocks), ctx, static_cast<int>(q.batch), scale, &m, split, ws,
                                             ws_bytes, out, lse, reinterpret_cast<void*>(stream)));
@@ -237,6 +261,7 @@ PyObject* shared_prefix_attention(PyObject*, PyObject* const* args, Py_ssize_t n
     Args a{args};
     kv_pool* pool = a.pool(0);
     const int64_t d = a.integer(1);
+    a.one_device(nargs);
     const Queries q(a, 2, 3, d);
     const int32_t* ctx = a.data<const int32_t>(4, at::kInt, q.batch, "context_lens");
     const at::Tensor* blk = a.tensor(6, "group_blocks");
@@ -251,7 +276,7 @@ PyObject* shared_prefix_attention(PyObject*, PyObject* const* args, Py_ssize_t n
     void* out = a.data(10, at::kBFloat16, q.rows * d, "out");
     float* lse = a.data<float>(11, at::kFloat, q.rows, "lse", true);
     const int64_t stream = a.integer(12);
-    if (!a.ok) return nullptr;
+    if (!a.on_device_of(pool)) return nullptr;
     return status(a, paged_shared_prefix_attention(pool, q.q, static_cast<int>(q.heads), static_cast<int>(q.q_len), q.tables,
                                                    static_cast<int>(q.max_blocks), ctx, static_cast<int>(q.batch), offsets, blocks,
                                                    static_cast<int>(groups), scale, split, ws, ws_bytes, out, lse,

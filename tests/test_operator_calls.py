@@ -178,3 +178,27 @@ def test_fake_tensors_are_refused(lib):
                        (c.shared_prefix_attention, (1, 64, q, t, l, t[0], l[:2], 1.0, 0, ws, out, lse, 0))):
         with pytest.raises(ValueError, match="memory"):
             call(*[fake(x) if isinstance(x, torch.Tensor) else x for x in args])
+
+
+def test_tensors_of_two_devices_are_refused(lib):
+    """A kernel must not be given an address of another device than its pool's.  Fake tensors stand in
+    for the devices."""
+    import torch
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    c = kp._native()
+
+    def fake(t, device):
+        with FakeTensorMode():
+            return torch.empty(t.shape, dtype=t.dtype, device=device)
+
+    q, kv = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    t, l = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)  # noqa: E741
+    out, w, table = torch.empty_like(q), torch.zeros(64), torch.zeros(9, 64)
+    ws, lse = torch.zeros(64, dtype=torch.uint8), torch.zeros(2, 4)
+    for call, args in ((c.norm_rope_append, (1, 64, 2, q, kv, kv, t, l, w, w, 1e-6, table, False, 1, l, l, out, 0)),
+                       (c.attention_masked, (1, 64, q, t, l, 1.0, 0.0, 0, w[:4], l, l, 0, ws, out, lse, 0)),
+                       (c.shared_prefix_attention, (1, 64, q, t, l, l, l[:1], 1.0, 0, ws, out, lse, 0))):
+        for other in [i for i, x in enumerate(args) if isinstance(x, torch.Tensor)]:
+            with pytest.raises(ValueError, match="one device"):
+                call(*[fake(x, "cuda:1" if i == other else "cuda:0") if isinstance(x, torch.Tensor) else x
+                       for i, x in enumerate(args)])
