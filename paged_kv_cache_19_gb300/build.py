@@ -39,23 +39,49 @@ def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
 
 
+def _headers() -> list[str]:
+    return glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+
+
 def _deps() -> list[str]:
-    return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + glob.glob(os.path.join(INCLUDE, "*.h")) + [BINDING_SRC, os.path.abspath(__file__)])
+    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + _headers()
+
+
+def _newer(target: str, deps: list[str]) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(d) <= os.path.getmtime(target) for d in deps)
+
+
+def _binding_abi() -> str:
+    """What the binding is compiled against beside the library: another torch or Python may lay its
+    objects out differently, whatever the files' times."""
+    import torch
+    return f"torch {torch.__version__} at {os.path.dirname(torch.__file__)}, python {sys.version}\n"
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB, _deps())
+
+
+def binding_up_to_date() -> bool:
+    stamp = os.path.join(BUILD, "binding.abi")
+    if not os.path.exists(stamp) or not _newer(BINDING, [BINDING_SRC, *_headers()]):
+        return False
+    with open(stamp) as f:
+        return f.read() == _binding_abi()
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return library_up_to_date() and binding_up_to_date()
 
 
-def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile and link the library; returns its path."""
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
+def _run(cmd: list[str], what: str) -> str:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    return r.stdout + r.stderr
+
+
+def _build_library(verbose: bool, ptxas_info: bool) -> None:
     nvcc = _nvcc()
 
     def compile_one(src):
@@ -63,45 +89,51 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         cmd = [nvcc, *ARCH, *NVCC_FLAGS, "-c", src, "-o", obj]
         if ptxas_info:
             cmd += ["-Xptxas", "-v"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
+        said = _run(cmd, f"nvcc on {os.path.basename(src)}")
         if verbose or ptxas_info:
-            sys.stderr.write(r.stdout + r.stderr)
+            sys.stderr.write(said)
         return obj
-
-    def compile_binding():
-        import torch
-        root = os.path.dirname(torch.__file__)
-        obj = os.path.join(BUILD, "binding.o")
-        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-               "-I" + INCLUDE, "-I" + os.path.join(root, "include"),
-               "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
-               "-I" + sysconfig.get_paths()["include"], "-c", BINDING_SRC, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed on calls.cpp:\n{r.stdout}\n{r.stderr}")
-        return obj, os.path.join(root, "lib")
 
     # the longest translation units first
     srcs = sorted(sources(), key=lambda f: ("span" not in f, f))
     with ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 1)) as ex:
-        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, srcs))
-        binding_obj, torch_lib = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-Xlinker", "-soname=libkvpaged.so", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([nvcc, *ARCH, "-shared", "-Xlinker", "-soname=libkvpaged.so", "-o", tmp, *objs], "link")
     os.replace(tmp, LIB)
+
+
+def _compile_binding() -> tuple[str, str]:
+    import torch
+    root = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD, "binding.o")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-I" + INCLUDE, "-I" + os.path.join(root, "include"),
+          "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
+          "-I" + sysconfig.get_paths()["include"], "-c", BINDING_SRC, "-o", obj], "g++ on calls.cpp")
+    return obj, os.path.join(root, "lib")
+
+
+def _link_binding(obj: str, torch_lib: str) -> None:
     tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = ["g++", "-shared", "-o", tmp, binding_obj, LIB, "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
-           "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
+    _run(["g++", "-shared", "-o", tmp, obj, LIB, "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+          "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib], "link of the binding")
     os.replace(tmp, BINDING)
+    with open(os.path.join(BUILD, "binding.abi"), "w") as f:
+        f.write(_binding_abi())
+
+
+def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    """Compile and link the library and the binding, each where it is not up to date; returns the
+    library's path.  The library does not need the binding: where only the binding fails (it wants
+    Python's and torch's headers beside g++), the library is in place when the error is raised."""
+    os.makedirs(BUILD, exist_ok=True)
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        binding = ex.submit(_compile_binding) if force or not binding_up_to_date() else None
+        if force or not library_up_to_date():
+            _build_library(verbose, ptxas_info)
+        if binding is not None:
+            _link_binding(*binding.result())
     return LIB
 
 
