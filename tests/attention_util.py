@@ -125,3 +125,12 @@ class Cache:
             assert (s[~live] == -np.inf).all()
             off = np.abs(s[live] - lse[live])
             assert (off <= slack[live]).all(), off.max()
+
+
+SHARE_TOKENS = 2048    # what a group has to save, (members - 1) x shared tokens, to be computed once
+
+
+def sharing(offsets, blocks, bs):
+    """Indexes of the groups that the shared pass computes."""
+    n = np.diff(np.asarray(offsets))
+    return [g for g in range(len(n)) if n[g] >= 2 and blocks[g] > 0 and (n[g] - 1) * blocks[g] * bs >= SHARE_TOKENS]

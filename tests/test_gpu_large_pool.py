@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import paged_kv_cache_19_gb300 as kp
-from attention_util import Cache
+from attention_util import Cache, sharing
 from gpu_util import i32
 
 pytestmark = pytest.mark.gpu
@@ -79,4 +79,33 @@ def test_two_calls_at_once_on_two_streams():
     for os_, w in zip(outs, want):
         assert all(torch.equal(o, w) for o in os_)
     assert c.pool.device_errors() == 0
+    c.pool.destroy()
+
+
+@pytest.mark.parametrize("fp8,bs,blocks", SIZES)
+def test_the_shared_pass_past_32_bits(fp8, bs, blocks):
+    """Groups that are computed once, every second of their blocks at the far end of a large pool."""
+    hk = 8 if not fp8 else 32
+    groups = [(30, 9), (1, 0), (13, 12)]
+    own = np.random.default_rng(3).integers(1, 90, 44)
+    ctx = np.concatenate([[b * bs] * m for m, b in groups]) + own
+    c = Cache(ctx=ctx, hq=2 * hk, hk=hk, d=128, bs=bs, fp8=fp8, shared=groups, seed=5)
+    assert sharing(c.offsets, c.blocks, bs) == [0, 2]
+    big = kp.kv_pool_create(blocks, bs, hk, 128, "fp8_e4m3" if fp8 else "bf16")
+    if fp8:
+        big.set_scales(c.ks, c.vs)
+    to = np.where(np.arange(c.nb) % 2 == 0, blocks - 1 - np.arange(c.nb), np.arange(c.nb))
+    far = to[c.tab[0, :9]] * (bs * hk * 128 * (1 if fp8 else 2))
+    assert (far > 2 ** 32).any() and (far < 2 ** 32).any()
+    at = torch.from_numpy(to).cuda()
+    for src, dst in zip(c.pool.raw_bytes(), big.raw_bytes()):
+        dst[at] = src
+    tab = i32(np.where(c.tab >= 0, to[np.maximum(c.tab, 0)], -1))
+    off, blk = i32(c.offsets), i32(c.blocks)
+    small, large = (kp.paged_shared_prefix_attention(p, c.q, t, c.lens, off, blk, c.scale)
+                    for p, t in ((c.pool, c.tables), (big, tab)))
+    assert torch.equal(small, large)
+    c.check(large, None, c.reference())
+    assert c.pool.device_errors() == 0 and big.device_errors() == 0
+    big.destroy()
     c.pool.destroy()

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import paged_kv_cache_19_gb300 as kp
-from attention_util import POISON, Cache
+from attention_util import POISON, Cache, sharing
 from gpu_util import i32
 
 pytestmark = pytest.mark.gpu
@@ -415,3 +415,95 @@ def test_the_ends_of_the_values_scale(scale):
     for got in (masked, shared):
         assert (np.abs(got.double().cpu().numpy() - want) <= bound).all()
     c.pool.destroy()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_groups_that_share_behind_many_that_do_not(fp8):
+    """The shared pass looks 320 or 448 groups over at a time: ones that share in the first round, in
+    later ones, and at the very end."""
+    groups = ([(1, 1)] * 10 + [(17, 8)] + [(1, 1)] * 400 + [(20, 9)] + [(1, 0)] * 500 + [(30, 5), (2, 3)] + [(1, 2)] * 60
+              + [(140, 1)])
+    c = Cache(ctx=batch(groups, 16, 20), hq=2, hk=1, d=128 if fp8 else 64, bs=16, fp8=fp8, shared=groups, seed=7)
+    assert sharing(c.offsets, c.blocks, 16) == [10, 411, 912, 974]
+    want = c.reference()
+    c.check(*run(c), want)
+    # only the groups from the second round on are named
+    c.check(*run(c, offsets=c.offsets[330:], blocks=c.blocks[330:]), want)
+    assert c.pool.device_errors() == 0
+    c.pool.destroy()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_bad_groups_beside_ones_that_share(fp8):
+    """A block count that breaks the rule: its group shares nothing, the others do.  Offsets that do:
+    nothing is shared.  Empty groups and sequences of no group between ones that share."""
+    groups = [(30, 10), (20, 16), (25, 12)]
+    c = Cache(ctx=batch(groups, 16, 50), hq=8, hk=2, d=128, bs=16, shared=groups, fp8=fp8)
+    want = c.reference()
+    o, far = [0, 30, 50, 75], c.max_blocks + 1
+    for off, blk in ((o, [-1, 16, 12]), (o, [10, far, 12]), (o, [10, 16, -(2 ** 31)]), (o, [2 ** 31 - 1, -1, 12]),
+                     ([0, 30, 29, 75], [10, 16, 12]), ([-1, 30, 50, 75], [10, 16, 12]), ([0, 30, 50, 76], [10, 16, 12]),
+                     ([0, 2 ** 31 - 1, 50, 75], [10, 16, 12])):
+        c.check(*run(c, offsets=off, blocks=np.array(blk)), want)
+        assert c.pool.device_errors() == kp.DEVERR_GROUP
+    for off, blk in (([0, 30, 30, 30, 50, 75, 75], [10, 16, 9, 16, 12, 4]), ([2, 29, 30, 30, 49], [10, 3, 16, 15]),
+                     ([31, 50], [16]), ([50, 50, 75], [9, 12])):
+        assert sharing(off, blk, 16)
+        c.check(*run(c, offsets=off, blocks=np.array(blk)), want)
+        assert c.pool.device_errors() == 0
+    c.pool.destroy()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_decode_step_of_a_batch_forked_behind_a_long_prompt(fp8):
+    """As test_a_decode_step_of_a_forked_batch, with a prompt long enough to be computed once: prompt,
+    forks and groups through the block manager, the new tokens appended, attention over the cache."""
+    hq, hk, d, bs, n, prompt, mb = 8, 2, 128, 16, 6, 533, 40
+    bm = kp.BlockManager(80, bs)
+    pool = kp.kv_pool_create(80, bs, hk, d, "fp8_e4m3" if fp8 else "bf16")
+    if fp8:
+        pool.set_scales([0.01, 0.02], [0.015, 0.01])
+    for t in pool.raw_bytes():
+        t.fill_(POISON)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    w = [torch.rand(d, generator=gen, device="cuda") + 0.5 for _ in range(2)]
+    a = np.arange(600)[:, None] * 10000.0 ** (-np.arange(0, d, 2) / d)
+    rope = torch.from_numpy(np.concatenate([np.cos(a), np.sin(a)], 1).astype(np.float32)).cuda()
+    bm.add_sequence(0)
+    bm.append_slots(0, prompt)
+    tab, _ = bm.build_tables([0], mb)
+    x = rand(prompt, hq + 2 * hk, d)
+    kp.paged_norm_rope_append(pool, x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:], tab.cuda(), q_weight=w[0], k_weight=w[1],
+                              rope_table=rope, token_seq=i32(np.zeros(prompt)), token_pos=i32(np.arange(prompt)))
+    for child in range(1, n):
+        bm.fork(0, child)
+    bm.add_sequence(n)                                # and one of its own
+    bm.append_slots(n, 20)
+    seqs = [n, *range(n)]
+    tab, _ = bm.build_tables([n], mb)
+    x = rand(20, hq + 2 * hk, d)
+    kp.paged_norm_rope_append(pool, x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:], tab.cuda(), q_weight=w[0], k_weight=w[1],
+                              rope_table=rope, token_seq=i32(np.zeros(20)), token_pos=i32(np.arange(20)))
+    for step in range(3):
+        copies = [cp for s in seqs if (cp := bm.append_slots(s, 1)) is not None]
+        if copies:
+            kp.kv_copy_blocks(pool, i32(copies))
+        order, off, blk = bm.prefix_groups(seqs)
+        assert sharing(off.numpy(), blk.tolist(), bs) == [1] and blk.tolist() == [0, prompt // bs]
+        tab, ctx = bm.build_tables([seqs[i] for i in order.tolist()], mb)
+        tab, ctx = tab.cuda(), ctx.cuda()
+        x = rand(n + 1, hq + 2 * hk, d)
+        q = kp.paged_norm_rope_append(pool, x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:], tab, ctx, q_weight=w[0],
+                                      k_weight=w[1], rope_table=rope)
+        out, lse = torch.empty_like(q), torch.empty(n + 1, hq, device="cuda")
+        kp.paged_shared_prefix_attention(pool, q, tab, ctx, off.cuda(), blk.cuda(), d ** -0.5, out=out, lse=lse)
+        c = object.__new__(Cache)                     # the oracle over the cache's own bytes
+        c.B, c.hq, c.hk, c.d, c.bs, c.q_len, c.scale, c.pool = n + 1, hq, hk, d, bs, 1, d ** -0.5, pool
+        c.ctx, c.tab, c.q64 = ctx.cpu().numpy(), tab.cpu().numpy(), q.double().cpu().numpy()[:, :, None]
+        k, v, ks, vs = (t.float().cpu().double().numpy() for t in pool.tensors())
+        c.k, c.v = k * ks[:, None], v * vs[:, None]
+        c.check(out, lse, c.reference())
+    assert pool.device_errors() == 0
+    pool.destroy()
+    bm.close()
