@@ -476,11 +476,14 @@ kv_status paged_decode_step(kv_pool* pool, const void* k_new, const void* v_new,
                             void* out, float* lse_out, void* stream);
 
 /*
- * Test hook of the failure path of the decode kernels; the pages have no
+ * Test hook of the failure path of the kernels with a pipeline; the pages have no
  * counterpart (their engines raise on the host; this library's kernels bound
  * every pipeline wait instead, see KV_DEVERR_TIMEOUT).  Process-wide, read by
  * every later paged_decode_attention / paged_attention_multi_query /
- * paged_decode_step / split-merge / no-alloc launch:
+ * paged_decode_step / split-merge / no-alloc launch, by paged_attention_masked, both
+ * kernels of paged_shared_prefix_attention (in the shared pass the loads give up at
+ * that stage by themselves, and every other role with them), and
+ * paged_norm_rope_append where a prompt streams through it (a stage is a token):
  *   stop_stage: the producer of each CTA issues no load for the stages of its
  *     chunk from this index on (-1, the default: off), so the consumers' wait
  *     for that stage can only run out: they set KV_DEVERR_TIMEOUT, leave their

@@ -705,6 +705,8 @@ kv_status paged_norm_rope_append(kv_pool* pool, const void* q, int64_t q_stride,
     p.block_size = pool->block_size;
     p.q_len = q_len;
     p.chunks = 0;
+    p.stop_stage = g_stop_stage.load(std::memory_order_relaxed);
+    p.consumer_wait_ns = g_consumer_wait_ns.load(std::memory_order_relaxed);
     return kvp::launch_norm_rope_append(p, pool->head_dim, pool->dtype == KV_DTYPE_FP8_E4M3, pool->num_sms,
                                         static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? KV_OK
@@ -1046,6 +1048,7 @@ kv_status paged_shared_prefix_attention(const kv_pool* pool, const void* q, int 
     s.share_least = (kShareTokens + pool->block_size - 1) / pool->block_size;
     s.pieces = static_cast<int>(l.pieces);
     s.scale_log2 = p.d.scale_log2;
+    s.stop_stage = p.d.stop_stage;
     if (kvp::launch_prefix(pool->dtype == KV_DTYPE_FP8_E4M3, pool->head_dim, pool->block_size, pool->num_sms, pool->tmpk,
                            pool->tmpv, s, static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return KV_ERR_CUDA;

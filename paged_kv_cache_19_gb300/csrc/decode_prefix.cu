@@ -443,8 +443,9 @@ paged_prefix_pass(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 const int id = __shfl_sync(FULL_MASK, batch & 1 ? ids[1] : ids[0], mine);
                 const int s = n % NSLOT;
                 bool good = true;
-                if (lane == 0)
-                    good = pfx_wait(smem_u32(empty + s), (static_cast<uint32_t>(n / NSLOT) & 1u) ^ 1u, abort_flag);
+                if (lane == 0)                      // (test hook: at stop_stage the wait runs out)
+                    good = n != p.stop_stage &&
+                           pfx_wait(smem_u32(empty + s), (static_cast<uint32_t>(n / NSLOT) & 1u) ^ 1u, abort_flag);
                 if (!all_ok(good)) return false;
                 const uint32_t bar = smem_u32(full + s);
                 if (is_k) {

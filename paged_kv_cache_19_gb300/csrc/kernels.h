@@ -69,6 +69,7 @@ struct PrefixParams {
     int pieces;               // pieces the workspace holds
     int share_least;          // blocks a group has to save at least to be computed once
     float scale_log2;
+    int stop_stage;           // test hook: the loads give up at this tile (-1: never)
 };
 // Run slots and pieces the shared pass can use, for a grid of `ctas` (its workspace).
 inline long long prefix_run_slots(int batch, int kv_heads, int rows, int n_groups)
@@ -151,6 +152,8 @@ struct NormRopeParams {
     uint32_t* err;
     int num_tokens, batch, q_heads, kv_heads, max_blocks, num_blocks, block_size, q_len;
     uint32_t chunks;          // lane groups per token (set by the launcher)
+    int stop_stage;           // as in DecodeParams: tokens of a CTA of the streaming form
+    unsigned long long consumer_wait_ns;
 };
 
 // Absorbed multi-head latent attention over a latent pool [num_blocks,

@@ -427,6 +427,8 @@ paged_norm_rope_append_stream(const NormRopeParams p, int stage_bytes, int stage
                 const int tseq = __shfl_sync(FULL_MASK, seq, k);
                 const int tpos = __shfl_sync(FULL_MASK, pos, k);
                 const int tblk = __shfl_sync(FULL_MASK, blk, k);
+                ok = n != p.stop_stage;             // test hook: the rest never lands
+                if (!ok) break;
                 ok = all_ok(mbar_wait_bounded(smem_u32(&ctl.empty[s]), (static_cast<uint32_t>(n / stages) & 1u) ^ 1u));
                 if (!ok) break;
                 const uint32_t i = base + k;
@@ -456,7 +458,7 @@ paged_norm_rope_append_stream(const NormRopeParams p, int stage_bytes, int stage
             pos = pos2;
             blk = blk2;
         }
-        if (!ok && lane == 0) atomicOr(p.err, KV_DEVERR_TIMEOUT);
+        if (!ok && lane == 0 && n != p.stop_stage) atomicOr(p.err, KV_DEVERR_TIMEOUT);
         // copies still in flight must land before the CTA exits
         for (int j = max(0, n - stages); j < n; ++j)
             if (!mbar_wait_bounded(smem_u32(&ctl.full[j % stages]), static_cast<uint32_t>(j / stages) & 1u)) break;
@@ -476,9 +478,10 @@ paged_norm_rope_append_stream(const NormRopeParams p, int stage_bytes, int stage
         nra_weights(p.k_weight, ln, gk);
     }
     const long long q_step = static_cast<long long>(p.q_len) * D;
+    const unsigned long long wait_ns = p.consumer_wait_ns ? p.consumer_wait_ns : WAIT_LIMIT_NS;
     for (int n = 0; n < count; ++n) {
         const int s = n % stages;
-        if (!all_ok(mbar_wait_bounded(smem_u32(&ctl.full[s]), static_cast<uint32_t>(n / stages) & 1u))) {
+        if (!all_ok(mbar_wait_bounded(smem_u32(&ctl.full[s]), static_cast<uint32_t>(n / stages) & 1u, wait_ns))) {
             if (lane == 0) atomicOr(p.err, KV_DEVERR_TIMEOUT);
             break;
         }
