@@ -422,8 +422,8 @@ kv_status paged_attention_masked_workspace_size(const kv_pool* pool, int batch, 
  *   group_blocks: int32 [n_groups], in [0, max_blocks].  Sequences outside every
  *   group, groups of one, and groups with 0 shared blocks share nothing, and
  *   groups that would save little are computed as if they did not; a
- *   context may end inside its group's shared blocks (0 included; values behind it
- *   that others see have to be finite).  Offsets that
+ *   context may end inside its group's shared blocks (0 included).  The values in
+ *   the shared blocks have to be finite, also behind every member's context.  Offsets that
  *   break the rule (KV_DEVERR_GROUP): nothing is shared; a block count that
  *   does (KV_DEVERR_GROUP): that group shares nothing.  The results are right
  *   either way.
@@ -431,7 +431,10 @@ kv_status paged_attention_masked_workspace_size(const kv_pool* pool, int batch, 
  *   kv_split_tokens: as in paged_attention_masked, for the members' own parts.
  *   workspace: at least paged_shared_prefix_workspace_size()
  *   bytes, zero-filled before its first use and shared as that of
- *   paged_attention_masked.  Everything else as in paged_attention_multi_query.
+ *   paged_attention_masked.  Its size goes by the groups that could share: per kv head
+ *   and min(n_groups, batch / 2) a piece of 256 rows, 132 KB at head_dim 128 (256
+ *   sequences in as many groups: 164 MB with 8 kv heads, 583 MB with 32), so groups
+ *   of one are better left out of the arrays.  Everything else as in paged_attention_multi_query.
  *   Two kernel launches (one when n_groups is 0 or the batch is 1).
  */
 kv_status paged_shared_prefix_attention(const kv_pool* pool, const void* q, int q_heads, int q_len,

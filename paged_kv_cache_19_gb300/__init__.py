@@ -572,7 +572,10 @@ def paged_shared_prefix_attention(pool: Pool, q, block_tables, context_lens, gro
     """Attention of the new tokens of a batch ordered by groups that share leading blocks: group g
     is the sequences group_offsets[g] .. group_offsets[g + 1] - 1 (int32 [G + 1]) and shares the
     first group_blocks[g] entries of their tables (int32 [G]); BlockManager.prefix_groups makes
-    both.  q bf16 [B, Hq, d] or [B, Hq, q_len, d].  Returns out (shaped like q)."""
+    both.  q bf16 [B, Hq, d] or [B, Hq, q_len, d].  Returns out (shaped like q).
+
+    Without workspace a call allocates and clears one, hundreds of megabytes where there are many
+    groups: a step keeps its own."""
     if out is None:
         out = _like(q, stream)
     if workspace is None:

@@ -275,10 +275,18 @@ struct SpanPlan {
 constexpr int kSpanLeast = 2 + kvp::SPAN_PAD;
 
 // Tokens a group has to save at least, (members - 1) x shared, to be computed once: less costs more in
-// runs of the shared pass, pieces and their merge than it saves.  With 0 / 1,024 / 2,048 / 2,560: 41
-// pairs of sequences behind 1,364 tokens 60 / 62 / 53 / 53 us, 46 pairs behind 22 tokens (8-bit) 42 /
-// 17 / 17 / 17, 12 pairs behind 3,102 (8-bit) 29 / 29 / 32 / 34, 32 groups of 8 behind 512 161 / 161 /
-// 163 / 165, four samples behind 512 tokens 16.1 / 16.1 / 15.2 / 15.3.
+// runs of the shared pass, pieces and their merge than it saves.  With 0 / 1,024 / 2,048 / 2,560 / 4,096:
+//   32 groups of 8 behind 512 tokens                              161 / 161 / 163 / 165 / 173 us
+//   four samples of 512 tokens                                    16.1 / 16.1 / 15.2 / 15.3 / 15.1
+//   41 pairs of sequences behind 1,364, 8 kv heads                60 / 62 / 53 / 53 / 53
+//   46 pairs behind 22 (8-bit)                                    42 / 17 / 17 / 17 / 17
+//   16 pairs behind 2,196, 8 kv heads (8-bit)                     - / 52 / 47 / 37 / 37
+//   12 pairs behind 3,102, 2 kv heads (8-bit)                     29 / 29 / 32 / 34 / 24
+//   125 sequences behind 35, 3 new tokens (8-bit)                 - / 77 / 77 / 77 / 60
+// With nothing shared at all the last five take 47 / 17 / 32 / 19 / 56 us: pairs, and many members behind
+// little, want more than 2,048 tokens, the many groups of the first line fewer.  What sharing saves are
+// bytes (kv heads and element size count too), what it costs is a pass and its runs; a rule by tokens
+// alone is off by up to 42 % on single calls.
 constexpr int kShareTokens = 2048;
 
 kv_status make_span_plan(const kv_pool* pl, int batch, int q_heads, int q_len, int max_blocks,
