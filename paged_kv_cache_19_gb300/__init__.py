@@ -182,8 +182,9 @@ def _made(make, stream, device, returned=False):
     is kept for what the caller's current stream does with it, too."""
     if stream is None:
         return make()
-    if not hasattr(stream, "cuda_stream"):              # a raw handle; 0 and 1: the default stream
-        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream) > 1
+    if not isinstance(stream, torch.cuda.Stream):       # a handle; 0 and 1: the default stream
+        handle = _stream(stream)
+        stream = (torch.cuda.ExternalStream(handle, device=device) if handle > 1
                   else torch.cuda.default_stream(device))
     with torch.cuda.stream(stream):
         t = make()

@@ -124,6 +124,27 @@ def test_a_call_on_another_stream_than_the_current_one(handle):
     c.pool.destroy()
 
 
+class Handle:
+    """Another library's stream: all it has to have is its handle."""
+
+    def __init__(self, s):
+        self.cuda_stream = s.cuda_stream
+
+
+@pytest.mark.gpu
+def test_other_ways_to_name_a_stream():
+    c = Cache(ctx=[300, 70], hq=8, hk=2, d=64, bs=16)
+    want, s = c.reference(), torch.cuda.Stream()
+    for stream in (Handle(s), s.cuda_stream, torch.cuda.ExternalStream(s.cuda_stream), torch.cuda.current_stream(),
+                   torch.cuda.default_stream(), 0, 1, None):
+        torch.cuda.synchronize()
+        for f in (kp.paged_attention_masked, kp.paged_attention_multi_query):
+            out = f(c.pool, c.q, c.tables, c.lens, c.scale, stream=stream)
+            torch.cuda.synchronize()
+            c.check(out, None, want)
+    c.pool.destroy()
+
+
 @pytest.mark.gpu
 def test_norm_rope_append_on_another_stream_than_the_current_one():
     pool = kp.kv_pool_create(8, 16, 2, 64)
