@@ -160,3 +160,30 @@ def test_norm_rope_append_on_another_stream_than_the_current_one():
         torch.cuda.current_stream().wait_stream(s)
         assert torch.equal(out, x[:, :4])
     pool.destroy()
+
+
+@pytest.mark.gpu
+def test_a_side_stream_inside_a_capture():
+    """Workspace and out come from the graph's memory; the replays read the lengths of their time."""
+    groups = [(30, 9), (4, 40)]
+    ctx = np.concatenate([[b * 16] * m for m, b in groups]) + np.arange(34) * 5 + 40
+    c = Cache(ctx=ctx, hq=8, hk=2, d=64, bs=16, shared=groups, seed=3)
+    off, blk = i32(c.offsets), i32(c.blocks)
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s.wait_stream(torch.cuda.current_stream())
+        masked = kp.paged_attention_masked(c.pool, c.q, c.tables, c.lens, c.scale, stream=s)
+        shared = kp.paged_shared_prefix_attention(c.pool, c.q, c.tables, c.lens, off, blk, c.scale, stream=s.cuda_stream)
+        multi = kp.paged_attention_multi_query(c.pool, c.q, c.tables, c.lens, c.scale, kv_split_tokens=64, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+    for less in (0, 39, 17):
+        c.ctx = ctx - less
+        c.lens.copy_(i32(c.ctx))
+        g.replay()
+        torch.full((1 << 22,), 0x5A, dtype=torch.uint8, device="cuda")      # what the graph holds is not handed out
+        for got in (masked, shared, multi):
+            c.check(got, None, c.reference())
+    assert c.pool.device_errors() == 0
+    del masked, shared, multi
+    g.reset()
+    c.pool.destroy()
