@@ -25,7 +25,7 @@
 // Measured on a GB300 (32 query heads and 8 kv heads of 128 numbers, normalised and rotated):
 //   1 token          2.0 us, 64 tokens 2.35 us: the latency of position -> table -> row and a launch
 //   185 tokens of 96 rows, rotated by half, 8-bit cache   4.25 us
-//   8,191 tokens    39.5 us for 206 MB (5.2 TB/s, 77 % of the copy rate; the schedulers issue in 61 %
+//   8,191 tokens    39.6 us for 206 MB (5.2 TB/s, 77 % of the copy rate; the schedulers issue in 64 %
 //     of the cycles).  The direct form takes 62 us: it looks the place of every token up anew in each
 //     of the token's lane groups.
 #include "append_row.cuh"
