@@ -184,6 +184,8 @@ def test_tensors_of_two_devices_are_refused(lib):
     """A kernel must not be given an address of another device than its pool's.  Fake tensors stand in
     for the devices."""
     import torch
+    if torch.cuda.is_available() and torch.cuda.device_count() < 2:
+        pytest.skip("a fake tensor of a second device wants one, or no device at all")
     from torch._subclasses.fake_tensor import FakeTensorMode
     c = kp._native()
 
